@@ -71,7 +71,8 @@ typedef enum {
                                 replaced by plain loads, so this version never reports it */
   SPEC_ERR_UNSUPPORTED = 6,  /* host: more shared memory than the device offers, or more than
                                 2^31 - 1 row segments in one call */
-  SPEC_ERR_SCRATCH_LIMIT = 7 /* host: spec_verify_noalloc asked for more than its fixed scratch */
+  SPEC_ERR_SCRATCH_LIMIT = 7, /* host: spec_verify_noalloc asked for more than its fixed scratch */
+  SPEC_ERR_CACHE_RANGE = 8   /* device: a length or page number outside the paged cache (spec_kv.h) */
 } spec_status;
 
 typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;

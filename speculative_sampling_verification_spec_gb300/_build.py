@@ -1,10 +1,11 @@
 """In-tree build of libspecverify.so (CUDA kernels for sm_103a + the C ABI).
 
-Seven compilation units, one -gencode, compiled in parallel and linked with the
+Eight compilation units, one -gencode, compiled in parallel and linked with the
 shared cudart (so the process keeps a single CUDA runtime with PyTorch): the
-host side (csrc/spec_verify.cu) and six groups of kernels (csrc/kernel_unit.cu
-with SPECV_UNIT = 1..6; both include csrc/spec_kernels.cuh).  The library is
-written next to this file.
+host side of verification (csrc/spec_verify.cu), six groups of its kernels
+(csrc/kernel_unit.cu with SPECV_UNIT = 1..6; both include
+csrc/spec_kernels.cuh), and the paged key/value cache (csrc/spec_kv.cu).  The
+library is written next to this file.
 """
 from __future__ import annotations
 
@@ -15,14 +16,14 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-HDR = os.path.join(ROOT, "include", "spec_verify.h")
+HDRS = [os.path.join(ROOT, "include", h) for h in ("spec_verify.h", "spec_kv.h")]
 LIB = os.path.join(PKG, "libspecverify.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMPILE_FLAGS = ["-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC"]
 LINK_FLAGS = [*ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath,/usr/local/cuda/lib64"]
 # (source, extra defines); the heaviest units first, so they start first
-UNITS = [("kernel_unit.cu", ["-DSPECV_UNIT=%d" % u]) for u in (6, 5, 2, 1, 4, 3)] + [("spec_verify.cu", [])]
+UNITS = [("kernel_unit.cu", ["-DSPECV_UNIT=%d" % u]) for u in (6, 5, 2, 1, 4, 3)] + [("spec_kv.cu", []), ("spec_verify.cu", [])]
 
 
 def nvcc() -> str:
@@ -33,7 +34,7 @@ def nvcc() -> str:
 
 
 def sources():
-    return [HDR, __file__] + sorted(glob.glob(os.path.join(CSRC, "*.cu*"))) + \
+    return [*HDRS, __file__] + sorted(glob.glob(os.path.join(CSRC, "*.cu*"))) + \
         sorted(glob.glob(os.path.join(CSRC, "*.h")))
 
 

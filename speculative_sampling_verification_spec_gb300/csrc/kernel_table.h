@@ -18,4 +18,7 @@ const void* stream_bf16_topp();
 const void* stream_f32_k();
 const void* stream_bf16_k();
 
+// adds n to the kernels that spec_launch_count reports (spec_verify.cu)
+void count_launches(int n);
+
 }  // namespace specv_units

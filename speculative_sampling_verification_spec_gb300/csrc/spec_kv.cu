@@ -1,0 +1,252 @@
+// spec_kv.cu -- the paged 8-bit cache: argument checks, launch planning and the C
+// ABI entry points of include/spec_kv.h, with the append, general attention and
+// join kernels.
+#include "kernel_table.h"
+#include "spec_kv_append.cuh"
+#include "spec_kv_attn.cuh"
+
+#include <algorithm>
+#include <cmath>
+
+namespace {
+
+using namespace spec_kv_detail;
+
+// CTAs the attention's tile list is cut for: the 152 SMs times the CTAs that stay
+// resident on one (constants, so that the workspace size needs no device).
+constexpr int kSMs = 152;
+constexpr int kGenCtas = kSMs * 4;
+
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool pow2_page(int s) { return s == 16 || s == 32 || s == 64 || s == 128; }
+
+spec_status check_shapes(const spec_kv_cache* c, const spec_kv_params* p) {
+  if (!c || !p) return SPEC_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || !pow2_page(c->page_size) || c->Hkv < 1) return SPEC_ERR_INVALID_ARG;
+  if (c->D < 16 || c->D > kGenMaxD || c->D % 16) return SPEC_ERR_INVALID_ARG;
+  if (p->B < 0 || p->T < 1 || p->Hq < 1 || p->Hq % c->Hkv) return SPEC_ERR_INVALID_ARG;
+  if (p->dtype != SPEC_F32 && p->dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  // rows and tiles are counted in 32 bits
+  if (static_cast<int64_t>(p->B) * p->T * p->Hq > (int64_t(1) << 30)) return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+spec_status check_cache(const spec_kv_cache* c, const spec_kv_params* p) {
+  if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16)) return SPEC_ERR_INVALID_ARG;
+  if (c->page_stride < 0 || c->head_stride < 0 || c->token_stride < 0 || c->page_stride % 16 || c->head_stride % 16 ||
+      c->token_stride % 16 || c->scale_page_stride < 0 || c->scale_head_stride < 0)
+    return SPEC_ERR_INVALID_ARG;
+  if (!p->page_table || !p->seq_lens || p->max_pages < 1 || p->table_stride < 0) return SPEC_ERR_INVALID_ARG;
+  const int64_t tiles = (static_cast<int64_t>(p->max_pages) * c->page_size + kTile - 1) / kTile;
+  // positions, and tiles of the whole call, are counted in 32 bits
+  if (static_cast<int64_t>(p->max_pages) * c->page_size > INT_MAX - kTile) return SPEC_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(std::max(1, p->B)) * c->Hkv > (int64_t(1) << 30) / tiles) return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+bool bad_strides(int64_t seq, int64_t tok, int64_t head) { return seq < 0 || tok < 0 || head < 0; }
+
+void fill_cache(const spec_kv_cache* c, const spec_kv_params* p, KvArgs& a) {
+  a.k_codes = c->k_codes;
+  a.v_codes = c->v_codes;
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.page_stride = c->page_stride;
+  a.head_stride = c->head_stride;
+  a.token_stride = c->token_stride;
+  a.scale_page_stride = c->scale_page_stride;
+  a.scale_head_stride = c->scale_head_stride;
+  a.table = p->page_table;
+  a.table_stride = p->table_stride;
+  a.seq_lens = p->seq_lens;
+  a.new_lens = p->new_lens;
+  a.status = p->status;
+  a.B = p->B;
+  a.T = p->T;
+  a.Hq = p->Hq;
+  a.Hkv = c->Hkv;
+  a.G = p->Hq / c->Hkv;
+  a.D = c->D;
+  a.log_page = 0;
+  while ((1 << a.log_page) < c->page_size) ++a.log_page;
+  a.num_pages = c->num_pages;
+  a.max_pages = p->max_pages;
+  a.q_seq = p->q_seq_stride;
+  a.q_tok = p->q_tok_stride;
+  a.q_head = p->q_head_stride;
+  a.o_seq = p->o_seq_stride;
+  a.o_tok = p->o_tok_stride;
+  a.o_head = p->o_head_stride;
+}
+
+template <typename E, int PC, bool WARP>
+const void* append_ptr() {
+  return reinterpret_cast<const void*>(&spec_kv_append_kernel<E, PC, WARP>);
+}
+template <typename E>
+const void* append_fn(bool vec, bool warp) {
+  return vec ? (warp ? append_ptr<E, 8, true>() : append_ptr<E, 8, false>())
+             : (warp ? append_ptr<E, 1, true>() : append_ptr<E, 1, false>());
+}
+
+// How the attention's work is cut; a function of B, T, Hq, Hkv, D and dtype.
+struct AttnPlan {
+  int rows = 0, nrt = 0, nranges = 0, slot_rows = 0;
+  size_t off_ml = 0, off_o = 0, ws_bytes = 0;
+};
+
+AttnPlan plan_attention(const spec_kv_cache* c, const spec_kv_params* p) {
+  AttnPlan pl;
+  const int64_t rows = static_cast<int64_t>(p->T) * (p->Hq / c->Hkv);
+  pl.rows = kGenRows;
+  pl.slot_rows = kGenRows;
+  pl.nrt = static_cast<int>((rows + kGenRows - 1) / kGenRows);
+  pl.nranges = std::max(1, kGenCtas / pl.nrt);
+  // with one range nothing is shared, so no partial results
+  const size_t slots = pl.nranges > 1 ? static_cast<size_t>(2) * pl.nranges * pl.nrt : 0;
+  pl.off_ml = round_up((static_cast<size_t>(p->B) + 1) * sizeof(int32_t), 256);
+  pl.off_o = pl.off_ml + round_up(slots * pl.slot_rows * sizeof(float2), 256);
+  pl.ws_bytes = pl.off_o + round_up(slots * pl.slot_rows * c->D * sizeof(float), 256);
+  return pl;
+}
+
+}  // namespace
+
+extern "C" {
+
+spec_status spec_kv_append(const void* q, const void* k, const void* v, const float* cos_sin,
+                           const spec_kv_cache* cache, const spec_kv_params* params, void* q_out) {
+  spec_status s = check_shapes(cache, params);
+  if (s != SPEC_OK) return s;
+  const spec_kv_params* p = params;
+  if (p->rot_dim < 0 || p->rot_dim % 2 || p->rot_dim > cache->D) return SPEC_ERR_INVALID_ARG;
+  if (p->rot_dim > 0 && (!cos_sin || p->rot_len < 1 || !aligned(cos_sin, 16))) return SPEC_ERR_INVALID_ARG;
+  if (p->B == 0) return SPEC_OK;
+  s = check_cache(cache, p);
+  if (s != SPEC_OK) return s;
+  if (!k || !v || (q == nullptr) != (q_out == nullptr)) return SPEC_ERR_INVALID_ARG;
+  if (bad_strides(p->k_seq_stride, p->k_tok_stride, p->k_head_stride) ||
+      bad_strides(p->v_seq_stride, p->v_tok_stride, p->v_head_stride))
+    return SPEC_ERR_INVALID_ARG;
+  if (q && (bad_strides(p->q_seq_stride, p->q_tok_stride, p->q_head_stride) ||
+            bad_strides(p->o_seq_stride, p->o_tok_stride, p->o_head_stride)))
+    return SPEC_ERR_INVALID_ARG;
+  AppendArgs g = {};
+  KvArgs& a = g.a;
+  fill_cache(cache, p, a);
+  a.q = q;
+  a.out = q_out;
+  g.k = k;
+  g.v = v;
+  g.cos_sin = cos_sin;
+  g.k_seq = p->k_seq_stride;
+  g.k_tok = p->k_tok_stride;
+  g.k_head = p->k_head_stride;
+  g.v_seq = p->v_seq_stride;
+  g.v_tok = p->v_tok_stride;
+  g.v_head = p->v_head_stride;
+  g.rot = p->rot_dim;
+  g.rot_len = p->rot_len;
+  g.interleaved = p->interleaved ? 1 : 0;
+  const int S = cache->page_size;
+  const int64_t es = p->dtype == SPEC_F32 ? 4 : 2;
+  const auto vec_ok = [&](const void* ptr, int64_t a1, int64_t a2, int64_t a3) {
+    return aligned(ptr, 16) && (a1 * es) % 16 == 0 && (a2 * es) % 16 == 0 && (a3 * es) % 16 == 0;
+  };
+  // eight pairs a thread where every chunk starts on a 16-byte boundary
+  const bool vec = p->rot_dim % 16 == 0 && vec_ok(k, g.k_seq, g.k_tok, g.k_head) &&
+                   vec_ok(v, g.v_seq, g.v_tok, g.v_head) &&
+                   (!q || (vec_ok(q, a.q_seq, a.q_tok, a.q_head) && vec_ok(q_out, a.o_seq, a.o_tok, a.o_head)));
+  const int per_tok = cache->D / (vec ? 16 : 2);
+  g.units_page = (p->T - 1 + S - 1) / S + 1;
+  const int64_t units = static_cast<int64_t>(p->B) * g.units_page * cache->Hkv * 2;
+  if (units > INT_MAX) return SPEC_ERR_UNSUPPORTED;
+  g.units = static_cast<int>(units);
+  // a unit fits a warp's registers or takes a CTA
+  const bool warp = std::min(p->T, S) * per_tok <= 32 * kAppendIter;
+  const int threads = warp ? kAppendWarpThreads : kAppendCtaThreads;
+  g.unit_blocks = warp ? (g.units + kAppendWarpThreads / 32 - 1) / (kAppendWarpThreads / 32) : g.units;
+  const int per_row = p->Hq * per_tok;
+  g.q_rows_block = std::max(1, 2 * threads / per_row);
+  const int64_t rows = static_cast<int64_t>(p->B) * p->T;
+  const int64_t q_blocks = q ? (rows + g.q_rows_block - 1) / g.q_rows_block : 0;
+  if (g.unit_blocks + q_blocks > INT_MAX) return SPEC_ERR_UNSUPPORTED;
+  const void* fn = p->dtype == SPEC_F32 ? append_fn<float>(vec, warp) : append_fn<__nv_bfloat16>(vec, warp);
+  void* args[] = {&g};
+  if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(g.unit_blocks + q_blocks)), dim3(threads), args, 0,
+                       static_cast<cudaStream_t>(p->stream)) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  specv_units::count_launches(1);
+  return SPEC_OK;
+}
+
+size_t spec_kv_attention_workspace_size(const spec_kv_cache* cache, const spec_kv_params* params) {
+  if (check_shapes(cache, params) != SPEC_OK) return 0;
+  return plan_attention(cache, params).ws_bytes;
+}
+
+spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const spec_kv_params* params, void* out,
+                              float* lse) {
+  spec_status s = check_shapes(cache, params);
+  if (s != SPEC_OK) return s;
+  const spec_kv_params* p = params;
+  if (p->window < 0 || !std::isfinite(p->scale)) return SPEC_ERR_INVALID_ARG;
+  if (p->B == 0) return SPEC_OK;
+  s = check_cache(cache, p);
+  if (s != SPEC_OK) return s;
+  if (!q || !out || bad_strides(p->q_seq_stride, p->q_tok_stride, p->q_head_stride) ||
+      bad_strides(p->o_seq_stride, p->o_tok_stride, p->o_head_stride))
+    return SPEC_ERR_INVALID_ARG;
+  const AttnPlan pl = plan_attention(cache, p);
+  if (!p->workspace || !aligned(p->workspace, 256) || p->workspace_bytes < pl.ws_bytes) return SPEC_ERR_INVALID_ARG;
+  KvArgs a = {};
+  fill_cache(cache, p, a);
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.window = p->window;
+  a.scale2 = static_cast<float>(static_cast<double>(p->scale) * 1.4426950408889634);
+  a.rows = pl.rows;
+  a.nrt = pl.nrt;
+  a.nranges = pl.nranges;
+  a.slot_rows = pl.slot_rows;
+  const int64_t ob = 4 * (p->dtype == SPEC_F32 ? 4 : 2);  // bytes of four channels
+  a.o_vec = aligned(out, static_cast<uintptr_t>(ob)) && a.o_seq % 4 == 0 && a.o_tok % 4 == 0 && a.o_head % 4 == 0;
+  char* ws = static_cast<char*>(p->workspace);
+  a.prefix = reinterpret_cast<int32_t*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
+  a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
+  const bool f32 = p->dtype == SPEC_F32;
+  cudaStream_t st = static_cast<cudaStream_t>(p->stream);
+  void* args[] = {&a};
+  const void* fn = f32 ? reinterpret_cast<const void*>(&spec_kv_attention_kernel<float>)
+                       : reinterpret_cast<const void*>(&spec_kv_attention_kernel<__nv_bfloat16>);
+  const int smem = gen_smem_bytes(a.D);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(pl.nranges * pl.nrt)), dim3(kGenThreads), args, smem, st) !=
+      cudaSuccess)
+    return SPEC_ERR_CUDA;
+  // the join kernel is a programmatic dependent launch: it may be scheduled while
+  // the last ranges finish, and waits before it reads or writes
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const void* jn = f32 ? reinterpret_cast<const void*>(&spec_kv_join_kernel<float>)
+                       : reinterpret_cast<const void*>(&spec_kv_join_kernel<__nv_bfloat16>);
+  if (cudaLaunchKernelExC(&cfg, jn, args) != cudaSuccess) return SPEC_ERR_CUDA;
+  specv_units::count_launches(2);
+  return SPEC_OK;
+}
+
+}  // extern "C"

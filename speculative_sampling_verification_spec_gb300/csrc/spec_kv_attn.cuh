@@ -1,0 +1,334 @@
+#pragma once
+// spec_kv_attn.cuh -- attention over the paged 8-bit cache: the kernel on the
+// ordinary float units, which takes every type, head size and alignment, and the
+// kernel that joins the ranges' partial results.
+//
+// One pass over the tokens with the running maximum m and sum l of each row's
+// softmax, in log2 units:  m' = max(m, x);  o = o 2^(m - m') + 2^(x - m') v;
+// l likewise.  All of it is held in float.
+#include "spec_kv_common.cuh"
+
+namespace spec_kv_detail {
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// reference and sum -> natural logarithm of the sum of the weights
+__device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.69314718055994531f; }
+
+constexpr int kGenThreads = 128;
+constexpr int kGenRows = 8;    // rows of a row tile
+constexpr int kGenSub = 32;    // tokens staged at a time: a lane's token in the scores
+constexpr int kGenMaxD = 256;
+constexpr int gen_smem_bytes(int D) { return 4 * (kGenRows * D + kGenSub * (D + 4)) + kGenSub * D; }
+
+// A CTA walks its pieces 32 tokens at a time.  The next 32 tokens' codes are in
+// registers (16-byte loads) while the present ones are worked on.  Scores: lane =
+// token, two rows a warp, so a row's maximum and sum stay in its warp.  Output:
+// thread = channel, eight rows in registers.
+template <typename E>
+__global__ void __launch_bounds__(kGenThreads) spec_kv_attention_kernel(const __grid_constant__ KvArgs a) {
+  constexpr int kVecs = 2 * kGenSub * (kGenMaxD / 16) / kGenThreads;  // 16-byte vectors a thread, keys and values
+  __shared__ RangePlan plan;
+  __shared__ int scratch[kGenThreads / 32];
+  extern __shared__ __align__(16) uint8_t dyn[];  // gen_smem_bytes(D)
+  __shared__ float sp[kGenRows][kGenSub];
+  __shared__ float sfac[kGenRows], sl[kGenRows], sm[kGenRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int range = blockIdx.x / a.nrt, rt = blockIdx.x - range * a.nrt;
+  make_plan_range<kGenThreads>(a, range, &plan, scratch, blockIdx.x == 0 ? a.prefix : nullptr);
+  if (plan.w0 >= plan.w1) return;
+  const int D = a.D, kst = D + 4, dv = D / 16;
+  float* sq = reinterpret_cast<float*>(dyn);  // [kGenRows][D]
+  float* sk = sq + kGenRows * D;              // [kGenSub][kst]: four floats of padding keep the lanes' banks apart
+  uint8_t* sv = reinterpret_cast<uint8_t*>(sk + kGenSub * kst);  // [kGenSub][D]
+  const int half_vecs = kGenSub * dv;  // vectors of the staged keys
+  Walk walk = walk_begin(plan, range, rt);
+  Piece p;
+  while (walk_next(a, walk, p)) {
+    const int j0 = p.tile0 * kTile, j1 = min(p.tile1 * kTile, p.L + p.n);
+    // queries in log2 units, zero rows past the last
+    for (int i = tid; i < kGenRows * D; i += kGenThreads) {
+      const int r = i / D, d = i - r * D;
+      float x = 0.0f;
+      if (r < p.nrows) {
+        const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
+        x = to_float(static_cast<const E*>(a.q)[p.b * a.q_seq + t * a.q_tok + (p.h * a.G + g) * a.q_head + d]) * a.scale2;
+      }
+      sq[i] = x;
+    }
+    float m[2] = {kNoRef, kNoRef}, l[2] = {0.0f, 0.0f};
+    int pos[2], low[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = warp * 2 + i;
+      pos[i] = r < p.nrows ? p.L + (p.row0 + r) / a.G : -1;
+      low[i] = a.window > 0 ? pos[i] - a.window : -1;  // sees positions in (low, pos]
+    }
+    float acc[2][kGenRows];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < kGenRows; ++r) acc[i][r] = 0.0f;
+
+    uint4 reg[kVecs];
+    auto fetch = [&](int base) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        int v = tid + i * kGenThreads;
+        const bool val = v >= half_vecs;
+        if (val) v -= half_vecs;
+        reg[i] = make_uint4(0, 0, 0, 0);
+        if (v < half_vecs) {
+          const int tok = v / dv, c = v - tok * dv, j = base + tok;
+          if (j < j1) {
+            const int page = page_of(a, p.b, j >> a.log_page);
+            if (page >= 0)
+              reg[i] = *reinterpret_cast<const uint4*>((val ? a.v_codes : a.k_codes) + page * a.page_stride +
+                                                       p.h * a.head_stride +
+                                                       (j & ((1 << a.log_page) - 1)) * a.token_stride + c * 16);
+          }
+        }
+      }
+    };
+    if (j0 < j1) fetch(j0);
+    for (int base = j0; base < j1; base += kGenSub) {
+      // scales of the lane's token; a page that is not the pool's gives NaN
+      const int j = base + lane;
+      float ks = 0.0f, vs = 0.0f;
+      if (j < j1) {
+        const int page = page_of(a, p.b, j >> a.log_page);
+        if (page < 0) {
+          ks = vs = __uint_as_float(0x7fc00000u);
+          if (warp == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+        } else {
+          const int64_t at = page * a.scale_page_stride + p.h * a.scale_head_stride;
+          ks = a.k_scale[at];
+          vs = a.v_scale[at];
+        }
+      }
+      __syncthreads();  // the staged tokens before have been read
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        int v = tid + i * kGenThreads;
+        const bool val = v >= half_vecs;
+        if (val) v -= half_vecs;
+        if (v < half_vecs) {
+          const int tok = v / dv, c = v - tok * dv;
+          if (val) {
+            *reinterpret_cast<uint4*>(&sv[tok * D + c * 16]) = reg[i];
+          } else {
+            const uint32_t w[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 lo = codes2_to_float2(static_cast<uint16_t>(w[e] & 0xffffu));
+              const float2 hi = codes2_to_float2(static_cast<uint16_t>(w[e] >> 16));
+              *reinterpret_cast<float4*>(&sk[tok * kst + c * 16 + e * 4]) = make_float4(lo.x, lo.y, hi.x, hi.y);
+            }
+          }
+        }
+      }
+      __syncthreads();
+      if (base + kGenSub < j1) fetch(base + kGenSub);
+      // scores of two rows
+      float s0 = 0.0f, s1 = 0.0f;
+      {
+        const float4* kp = reinterpret_cast<const float4*>(&sk[lane * kst]);
+        const float4* qa = reinterpret_cast<const float4*>(&sq[(warp * 2) * D]);
+        const float4* qb = reinterpret_cast<const float4*>(&sq[(warp * 2 + 1) * D]);
+#pragma unroll 4
+        for (int d = 0; d < D / 4; ++d) {
+          const float4 k4 = kp[d], a4 = qa[d], b4 = qb[d];
+          s0 = fmaf(k4.x, a4.x, fmaf(k4.y, a4.y, fmaf(k4.z, a4.z, fmaf(k4.w, a4.w, s0))));
+          s1 = fmaf(k4.x, b4.x, fmaf(k4.y, b4.y, fmaf(k4.z, b4.z, fmaf(k4.w, b4.w, s1))));
+        }
+      }
+      const float sc[2] = {s0 * ks, s1 * ks};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = warp * 2 + i;
+        const bool see = j < j1 && j <= pos[i] && j > low[i];
+        const float x = see ? sc[i] : -INFINITY;
+        float top = x;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+        const float mn = fmaxf(m[i], top), f = ex2(m[i] - mn);
+        const float w = ex2(x - mn);
+        m[i] = mn;
+        l[i] = fmaf(l[i], f, w);  // a lane's share of the sum
+        sp[r][lane] = see ? w * vs : -0.0f;  // -0: not seen
+        if (lane == 0) sfac[r] = f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int d = tid + i * kGenThreads;
+        if (d < D) {
+          float f[kGenRows];
+#pragma unroll
+          for (int r = 0; r < kGenRows; ++r) {
+            f[r] = sfac[r];
+            acc[i][r] *= f[r];
+          }
+          for (int t = 0; t < kGenSub; t += 2) {
+            const uint16_t c2 = static_cast<uint16_t>(sv[t * D + d] | (sv[(t + 1) * D + d] << 8));
+            const float2 v = codes2_to_float2(c2);
+#pragma unroll
+            for (int r = 0; r < kGenRows; ++r) {
+              const float2 w = *reinterpret_cast<const float2*>(&sp[r][t]);
+              // a token that the row does not see adds nothing, whatever its slot holds
+              if (__float_as_uint(w.x) != 0x80000000u) acc[i][r] = fmaf(w.x, v.x, acc[i][r]);
+              if (__float_as_uint(w.y) != 0x80000000u) acc[i][r] = fmaf(w.y, v.y, acc[i][r]);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int d = 16; d; d >>= 1) l[i] += __shfl_xor_sync(kFull, l[i], d);
+      if (lane == 0) {
+        sl[warp * 2 + i] = l[i];
+        sm[warp * 2 + i] = m[i];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int d = tid + i * kGenThreads;
+      if (d < D) {
+#pragma unroll
+        for (int r = 0; r < kGenRows; ++r) {
+          if (r >= p.nrows) continue;
+          if (p.whole) {
+            const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
+            from_float(acc[i][r] / sl[r], static_cast<E*>(a.out) + p.b * a.o_seq + t * a.o_tok + (p.h * a.G + g) * a.o_head + d);
+          } else {
+            a.part_o[(static_cast<int64_t>(p.slot) * a.slot_rows + r) * D + d] = acc[i][r];
+          }
+        }
+      }
+    }
+    if (tid < p.nrows) {
+      const int gr = p.row0 + tid, t = gr / a.G, g = gr - t * a.G;
+      if (p.whole) {
+        if (a.lse) a.lse[(static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g] = lse_of(sm[tid], sl[tid]);
+      } else {
+        a.part_ml[static_cast<int64_t>(p.slot) * a.slot_rows + tid] = make_float2(sm[tid], sl[tid]);
+      }
+    }
+    __syncthreads();  // queries and statistics are rewritten by the next piece
+  }
+}
+
+// One warp a row (sequence, token, query head): rows shared by several ranges are
+// added up in the order of the ranges; rows with nothing to attend are zero, rows
+// of a sequence with bad lengths NaN; the others are written already.
+constexpr int kJoinWarps = 4;
+
+template <typename E>
+__device__ __forceinline__ void store4(const KvArgs& a, E* o, float4 x) {
+  if constexpr (sizeof(E) == 4) {
+    if (a.o_vec) {
+      *reinterpret_cast<float4*>(o) = x;
+      return;
+    }
+  } else {
+    if (a.o_vec) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+      *reinterpret_cast<uint2*>(o) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      return;
+    }
+  }
+  from_float(x.x, o);
+  from_float(x.y, o + 1);
+  from_float(x.z, o + 2);
+  from_float(x.w, o + 3);
+}
+
+template <typename E>
+__global__ void __launch_bounds__(32 * kJoinWarps) spec_kv_join_kernel(const __grid_constant__ KvArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
+  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  const int64_t row = mine < rows ? mine : rows - 1;
+  const int hq = static_cast<int>(row % a.Hq);
+  const int64_t bt = row / a.Hq;
+  const int b = static_cast<int>(bt / a.T), t = static_cast<int>(bt - static_cast<int64_t>(b) * a.T);
+  const SeqSpan s = seq_span(a, b);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the ranges' results are complete
+  if (mine >= rows) return;
+  E* o = static_cast<E*>(a.out) + b * a.o_seq + t * a.o_tok + hq * a.o_head;
+  if (s.bad || t >= s.n) {
+    const float x = s.bad ? __uint_as_float(0x7fc00000u) : 0.0f;
+    for (int d = lane * 4; d < a.D; d += 128) store4(a, o + d, make_float4(x, x, x, x));
+    if (lane == 0) {
+      if (a.lse) a.lse[row] = s.bad ? x : -INFINITY;
+      if (s.bad) report(a.status, SPEC_ERR_CACHE_RANGE);
+    }
+    return;
+  }
+  const int total = a.prefix[a.B];
+  const int per = max(1, (total + a.nranges - 1) / a.nranges);
+  const int h = hq / a.G, g = hq - h * a.G;
+  const int wb = a.prefix[b] + h * s.nt;
+  const int c0 = wb / per, c1 = (wb + s.nt - 1) / per;
+  if (c0 == c1) return;
+  const int gr = t * a.G + g, rt = gr / a.rows, r = gr - rt * a.rows;
+  const auto slot_row = [&](int c) {
+    return static_cast<int64_t>(2 * (c * a.nrt + rt) + (c == c0 ? 1 : 0)) * a.slot_rows + r;
+  };
+  float top = kNoRef;
+  for (int c = c0 + lane; c <= c1; c += 32) {
+    const float2 ml = a.part_ml[slot_row(c)];
+    top = fmaxf(top, ml.x);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+  float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+  float l = 0.0f;
+  for (int cb = c0; cb <= c1; cb += 32) {
+    // weights of up to 32 parts, one a lane
+    float wl = 0.0f, ll = 0.0f;
+    if (cb + lane <= c1) {
+      const float2 ml = a.part_ml[slot_row(cb + lane)];
+      if (!(ml.y == 0.0f)) {  // a part without tokens for this row left no output
+        wl = exp2f(ml.x - top);
+        ll = ml.y;
+      }
+    }
+    const int m = min(32, c1 - cb + 1);
+#pragma unroll 4
+    for (int i = 0; i < m; ++i) {
+      const float w = __shfl_sync(kFull, wl, i), li = __shfl_sync(kFull, ll, i);
+      if (li == 0.0f) continue;
+      l = fmaf(w, li, l);
+      const float* po = a.part_o + slot_row(cb + i) * a.D;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int d = lane * 4 + k * 128;
+        if (d < a.D) {
+          const float4 x = *reinterpret_cast<const float4*>(po + d);
+          acc[k].x = fmaf(w, x.x, acc[k].x);
+          acc[k].y = fmaf(w, x.y, acc[k].y);
+          acc[k].z = fmaf(w, x.z, acc[k].z);
+          acc[k].w = fmaf(w, x.w, acc[k].w);
+        }
+      }
+    }
+  }
+  const float inv = 1.0f / l;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int d = lane * 4 + k * 128;
+    if (d < a.D) store4(a, o + d, make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
+  }
+  if (lane == 0 && a.lse) a.lse[row] = lse_of(top, l);
+}
+
+}  // namespace spec_kv_detail

@@ -1,0 +1,229 @@
+#pragma once
+// spec_kv_common.cuh -- what the paged-cache kernels share: their arguments, how
+// the attention's work is cut into ranges of tiles, and small device helpers.
+//
+// The attention's work is a list of tiles of kTile tokens: sequence after
+// sequence, within a sequence head after head, within a head in order of
+// position.  The list is cut into `nranges` equal ranges (from the lengths on
+// the device, so a batch of unequal sequences is spread evenly and no length
+// crosses to the host); a range is walked by one CTA for one row tile.  A (head,
+// row tile) that lies in one range is finished there; one that several ranges
+// share leaves a partial result (unnormalised output, reference, sum) per range
+// in the workspace, and the join kernel adds them in order.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "spec_kv.h"
+
+namespace spec_kv_detail {
+
+constexpr int kTile = 128;          // tokens of a tile
+constexpr int kMinScaleExp = -100;  // scales are at least 2^kMinScaleExp
+constexpr float kNoRef = -1e30f;    // softmax reference before any token
+constexpr unsigned kFull = 0xffffffffu;
+
+struct KvArgs {
+  // cache
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scale;
+  float* v_scale;
+  int64_t page_stride, head_stride, token_stride, scale_page_stride, scale_head_stride;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int32_t* status;
+  int32_t B, T, Hq, Hkv, G, D;
+  int32_t log_page, num_pages, max_pages, window;
+  // attention
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_seq, q_tok, q_head, o_seq, o_tok, o_head;
+  float scale2;       // scale * log2(e): scores are kept in log2 units
+  int32_t rows;       // rows of a row tile (row = t * G + head in group)
+  int32_t nrt;        // row tiles of a sequence
+  int32_t nranges;    // ranges of the tile list
+  int32_t o_vec;      // outputs may be stored four channels at a time
+  int32_t slot_rows;  // rows a partial slot has room for
+  int32_t* prefix;    // workspace: [B + 1] tiles before each sequence
+  float* part_o;      // workspace: [slots][slot_rows][D]
+  float2* part_ml;    // workspace: [slots][slot_rows] (reference, sum)
+};
+
+__device__ __forceinline__ void report(int32_t* status, int code) {
+  if (status) atomicCAS(status, 0, code);
+}
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_float(float x, float* p) { *p = x; }
+__device__ __forceinline__ void from_float(float x, __nv_bfloat16* p) { *p = __float2bfloat16_rn(x); }
+
+// two e4m3 codes -> two floats (exact)
+__device__ __forceinline__ float2 codes2_to_float2(uint16_t c) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+
+// The tokens of sequence b and the tiles its rows read: positions [t0 * kTile,
+// L + n).  No tiles when it has no new token or its lengths are out of range.
+struct SeqSpan {
+  int L, n, t0, nt;
+  bool bad;
+};
+__device__ __forceinline__ SeqSpan seq_span(const KvArgs& a, int b) {
+  SeqSpan s;
+  s.L = a.seq_lens[b];
+  s.n = a.new_lens ? a.new_lens[b] : a.T;
+  const int64_t cap = static_cast<int64_t>(a.max_pages) << a.log_page;
+  s.bad = s.L < 0 || s.n < 0 || s.n > a.T || static_cast<int64_t>(s.L) + s.n > cap;
+  s.t0 = 0;
+  s.nt = 0;
+  if (!s.bad && s.n > 0) {
+    const int first = (a.window > 0 && s.L + 1 > a.window) ? s.L + 1 - a.window : 0;
+    s.t0 = first / kTile;
+    s.nt = (s.L + s.n + kTile - 1) / kTile - s.t0;
+  }
+  return s;
+}
+
+// A CTA's view of the tile list: the range [w0, w1), and where w0 lies.
+struct RangePlan {
+  int per, w0, w1;
+  int b, off;  // sequence that holds w0, and w0's offset in its tiles (all heads)
+};
+
+// All threads of the CTA (NT of them) take part; `plan` and `scratch` are in
+// shared memory.  When prefix is given, it gets the tiles before each sequence.
+template <int NT>
+__device__ void make_plan_range(const KvArgs& a, int range, RangePlan* plan, int* scratch, int32_t* prefix) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c = (a.B + NT - 1) / NT;
+  const int b0 = min(a.B, tid * c), b1 = min(a.B, b0 + c);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += seq_span(a, b).nt * a.Hkv;
+  int inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(kFull, inc, d);
+    if (lane >= d) inc += o;
+  }
+  __syncthreads();  // the plan of the range before has been read
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  int before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  const int per = max(1, (total + a.nranges - 1) / a.nranges);
+  const int64_t start = static_cast<int64_t>(range) * per;
+  const int w0 = start < total ? static_cast<int>(start) : total;
+  const int w1 = min(total, w0 + per);
+  if (tid == 0) {
+    plan->per = per;
+    plan->w0 = w0;
+    plan->w1 = w1;
+    if (prefix) prefix[a.B] = total;
+  }
+  if (w0 < w1 && before <= w0 && w0 < before + mine) {
+    int at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int k = seq_span(a, b).nt * a.Hkv;
+      if (w0 < at + k) {
+        plan->b = b;
+        plan->off = w0 - at;
+        break;
+      }
+      at += k;
+    }
+  }
+  if (prefix) {
+    int at = before;
+    for (int b = b0; b < b1; ++b) {
+      prefix[b] = at;
+      at += seq_span(a, b).nt * a.Hkv;
+    }
+  }
+  __syncthreads();
+}
+
+// One piece of work: a (sequence, head, row tile) and the tiles of it that this
+// range holds.  Every role of a CTA walks the same pieces.
+struct Piece {
+  int b, h;
+  int L, n;          // tokens before the new ones; new tokens
+  int row0, nrows;   // rows of this row tile
+  int tile0, tile1;  // absolute tiles [tile0, tile1); may be empty
+  bool whole;        // the item lies in this range alone
+  int slot;          // else: where its partial result goes
+};
+
+struct Walk {
+  int w, w1, b, off;  // next tile of the list; sequence and offset in it
+  int per, w0, range, rt;
+};
+
+__device__ __forceinline__ Walk walk_begin(const RangePlan& p, int range, int rt) {
+  Walk k;
+  k.w = p.w0;
+  k.w0 = p.w0;
+  k.w1 = p.w1;
+  k.b = p.b;
+  k.off = p.off;
+  k.per = p.per;
+  k.range = range;
+  k.rt = rt;
+  return k;
+}
+
+// The next piece that has rows; false at the range's end.
+__device__ __forceinline__ bool walk_next(const KvArgs& a, Walk& k, Piece& p) {
+  while (k.w < k.w1) {
+    const SeqSpan s = seq_span(a, k.b);
+    const int all = s.nt * a.Hkv;
+    if (k.off >= all) {  // on to the next sequence
+      ++k.b;
+      k.off = 0;
+      continue;
+    }
+    const int h = k.off / s.nt, t = k.off - h * s.nt;
+    const int take = min(s.nt - t, k.w1 - k.w);
+    const int wb = k.w - t;  // list index of the item's first tile
+    p.whole = wb / k.per == (wb + s.nt - 1) / k.per;
+    p.slot = 2 * (k.range * a.nrt + k.rt) + (wb >= k.w0 ? 1 : 0);
+    k.w += take;
+    k.off += take;
+    p.b = k.b;
+    p.h = h;
+    p.L = s.L;
+    p.n = s.n;
+    p.row0 = k.rt * a.rows;
+    p.nrows = min(a.rows, s.n * a.G - p.row0);
+    if (p.nrows <= 0) continue;
+    // tiles that some row of this row tile sees
+    const int t_first = p.row0 / a.G, t_last = (p.row0 + p.nrows - 1) / a.G;
+    const int hi = (s.L + t_last) / kTile + 1;
+    const int first = (a.window > 0 && s.L + t_first + 1 > a.window) ? s.L + t_first + 1 - a.window : 0;
+    p.tile0 = max(s.t0 + t, first / kTile);
+    p.tile1 = min(s.t0 + t + take, hi);
+    if (p.tile1 < p.tile0) p.tile1 = p.tile0;
+    return true;
+  }
+  return false;
+}
+
+// page number of a token's page, -1 where it is not one of the pool's
+__device__ __forceinline__ int page_of(const KvArgs& a, int b, int page_index) {
+  const int pid = a.table[b * a.table_stride + page_index];
+  return (pid >= 0 && pid < a.num_pages) ? pid : -1;
+}
+
+}  // namespace spec_kv_detail

@@ -542,9 +542,16 @@ const char* spec_status_string(spec_status status) {
     case SPEC_ERR_TIMEOUT: return "a bounded device-side wait ran out";
     case SPEC_ERR_UNSUPPORTED: return "problem too large for one launch (rows x segments, or shared memory)";
     case SPEC_ERR_SCRATCH_LIMIT: return "request needs more scratch than spec_verify_noalloc's fixed array";
+    case SPEC_ERR_CACHE_RANGE: return "a length or a page number outside the paged cache";
   }
   return "unknown status";
 }
+
+}  // extern "C"
+
+void specv_units::count_launches(int n) { g_launches.fetch_add(static_cast<uint64_t>(n), std::memory_order_relaxed); }
+
+extern "C" {
 
 uint64_t spec_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 

@@ -1,0 +1,239 @@
+"""The paged 8-bit key/value cache of the target's verification pass: append and attention.
+
+`PagedKVCache` describes a pool of pages (e4m3 codes and one float32 scale for each page and key/value head);
+`spec_kv_append` and `spec_kv_attention` have the names of the C entry points they call (include/spec_kv.h) and, like
+the rest of the binding, only turn torch CUDA tensors into pointers, strides and a stream handle.  There is no CPU or
+PyTorch fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import struct
+
+import torch
+
+from . import binding
+
+EXPORTED = ("spec_kv_append", "spec_kv_attention", "spec_kv_attention_workspace_size")
+
+# spec_kv_cache and spec_kv_params of include/spec_kv.h, in native layout
+_CACHE = struct.Struct("@4i4P5q")
+_PARAMS = struct.Struct("@6if3i3P13q3PN")
+_F32, _BF16 = torch.float32, torch.bfloat16
+_DTYPES = {_F32: binding.SPEC_F32, _BF16: binding.SPEC_BF16}
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _lib():
+    L = binding.lib()
+    if L.spec_kv_append.argtypes is None:
+        P = ctypes.c_void_p
+        L.spec_kv_attention_workspace_size.argtypes = [P, P]
+        L.spec_kv_attention_workspace_size.restype = ctypes.c_size_t
+        L.spec_kv_attention.argtypes = [P] * 5
+        L.spec_kv_attention.restype = ctypes.c_int
+        L.spec_kv_append.restype = ctypes.c_int
+        L.spec_kv_append.argtypes = [P] * 7
+    return L
+
+
+class PagedKVCache:
+    """A pool of pages: k_codes, v_codes [num_pages, kv_heads, page_size, head_dim] (float8_e4m3fn or uint8; any
+    strides that are multiples of 16, channels contiguous, the same for both) and k_scale, v_scale
+    [num_pages, kv_heads] float32 (any strides, the same for both).  The tensors are the caller's; the object holds
+    their addresses, so it is made once and kept while they live."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale):
+        for t in (k_codes, v_codes):
+            if t.dim() != 4 or t.dtype not in _CODES or not t.is_cuda:
+                raise ValueError("codes must be CUDA float8_e4m3fn or uint8 [num_pages, kv_heads, page_size, head_dim]")
+            if t.stride(3) != 1:
+                raise ValueError("codes must be contiguous along the channels")
+        for t in (k_scale, v_scale):
+            if t.dim() != 2 or t.dtype != torch.float32 or not t.is_cuda or t.shape != k_codes.shape[:2]:
+                raise ValueError("scales must be CUDA float32 [num_pages, kv_heads]")
+        if k_codes.shape != v_codes.shape or k_codes.stride() != v_codes.stride() or \
+                k_scale.stride() != v_scale.stride():
+            raise ValueError("keys and values must have the same shapes and strides")
+        if len({t.device for t in (k_codes, v_codes, k_scale, v_scale)}) != 1:
+            raise ValueError("codes and scales must be on one device")
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k_codes.shape
+        self.device = k_codes.device
+        st = k_codes.stride()
+        self._packed = _CACHE.pack(self.num_pages, self.page_size, self.kv_heads, self.head_dim, k_codes.data_ptr(),
+                                   v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), st[0], st[1], st[2],
+                                   *k_scale.stride())
+
+    @classmethod
+    def empty(cls, num_pages, page_size, kv_heads, head_dim, device="cuda"):
+        """A pool with nothing stored (codes and scales are zero)."""
+        def codes():
+            return torch.zeros((num_pages, kv_heads, page_size, head_dim), dtype=torch.uint8,
+                               device=device).view(torch.float8_e4m3fn)
+        scales = [torch.zeros((num_pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(codes(), codes(), *scales)
+
+    def nbytes(self):
+        return sum(t.numel() * t.element_size() for t in (self.k_codes, self.v_codes, self.k_scale, self.v_scale))
+
+
+def _stream_of(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _new(shape, dtype, device, stream):
+    """An output for the call's stream.  One made for another stream than the current one comes from that stream's
+    memory, and is recorded on the current one, where the caller goes on to use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+_ws_cache = {}
+
+
+def _workspace(nbytes, device, stream):
+    """The workspace of (device, stream): calls on different streams may overlap, so each stream has its own."""
+    key = (device.index, _stream_of(stream, device))
+    ws = _ws_cache.get(key)
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.stream(stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _ws_cache[key] = ws
+    return ws
+
+
+def _check_table(cache, B, page_table, seq_lens, new_lens, status):
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
+            page_table.shape[1] < 1 or page_table.stride(1) != 1:
+        raise ValueError("page_table must be int32 [B, max_pages], contiguous along the pages")
+    for t in (seq_lens, new_lens):
+        if t is not None and (t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous()):
+            raise ValueError("seq_lens and new_lens must be contiguous int32 [B]")
+    for t in (page_table, seq_lens, new_lens, status):
+        if t is not None and t.device != cache.device:
+            raise ValueError("page_table, lengths and status must be on the cache's device")
+
+
+def _check_heads(name, t, shape, dtype, device):
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError("%s must be %s %s on %s, got %s %s on %s" % (name, dtype, tuple(shape), device, t.dtype,
+                                                                     tuple(t.shape), t.device))
+    if t.stride(3) != 1:
+        raise ValueError("%s must be contiguous along the channels" % name)
+
+
+def spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens=None, *, cos_sin=None, interleaved=False,
+                   q_out=None, status=None, stream=None):
+    """Rotate the new tokens' queries and keys by position and store their keys and values.
+
+    q [B, T, Hq, D] (or None), k and v [B, T, kv_heads, D]: float32 or bfloat16, any strides with the channels
+    contiguous.  page_table int32 [B, max_pages]; seq_lens int32 [B]: tokens stored before; new_lens int32 [B]: new
+    tokens, at most T (None: T each).  cos_sin float32 [positions, rot_dim]: cosines of a position's angles, then their
+    sines (None: no rotation); interleaved: pairs are neighbouring channels, else channels i and i + rot_dim / 2.
+    Returns the rotated queries (q_out, or a new contiguous tensor; zero in slots past new_lens); q_out may be q.
+    The cache is written in place."""
+    if not k.is_cuda:
+        raise ValueError("spec_* calls take CUDA tensors (copy host data to the GPU first)")
+    dtype = _DTYPES.get(k.dtype)
+    if dtype is None:
+        raise TypeError("keys must be float32 or bfloat16, got %s" % k.dtype)
+    if k.dim() != 4:
+        raise ValueError("k must be [B, T, kv_heads, head_dim]")
+    B, T, H, D = k.shape
+    if H != cache.kv_heads or D != cache.head_dim:
+        raise ValueError("k must be [B, T, %d, %d], got %s" % (cache.kv_heads, cache.head_dim, tuple(k.shape)))
+    dev = cache.device
+    _check_heads("k", k, k.shape, k.dtype, dev)
+    _check_heads("v", v, k.shape, k.dtype, dev)
+    _check_table(cache, B, page_table, seq_lens, new_lens, status)
+    rot = rot_len = cs = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != _F32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.device != dev:
+            raise ValueError("cos_sin must be contiguous float32 [positions, rot_dim] on the cache's device")
+        rot_len, rot = cos_sin.shape
+        cs = cos_sin.data_ptr()
+    hq, qs, os, qp, op = H, (0, 0, 0), (0, 0, 0), 0, 0
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("q must be [B, T, Hq, head_dim]")
+        hq = q.shape[2]
+        _check_heads("q", q, (B, T, hq, D), k.dtype, dev)
+        if q_out is None:
+            q_out = _new((B, T, hq, D), q.dtype, dev, stream)
+        else:
+            _check_heads("q_out", q_out, (B, T, hq, D), k.dtype, dev)
+        qs, os, qp, op = q.stride(), q_out.stride(), q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    ks, vs = k.stride(), v.stride()
+    prm = _PARAMS.pack(B, T, hq, dtype, page_table.shape[1], 0, 0.0, rot, rot_len, 1 if interleaved else 0,
+                       page_table.data_ptr(), seq_lens.data_ptr(), 0 if new_lens is None else new_lens.data_ptr(),
+                       page_table.stride(0), qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], os[0],
+                       os[1], os[2], _stream_of(stream, dev), 0 if status is None else status.data_ptr(), 0, 0)
+    code = _lib().spec_kv_append(qp, k.data_ptr(), v.data_ptr(), cs, cache._packed, prm, op)
+    if code != binding.SPEC_OK:
+        raise binding.SpecError(code, "spec_kv_append")
+    return q_out
+
+
+def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=None, window=0, out=None, lse=None,
+                      return_lse=False, status=None, ws=None, stream=None):
+    """Attention of the new tokens' (rotated) queries over everything stored for their sequence up to themselves.
+
+    q [B, T, Hq, D] float32 or bfloat16; page_table, seq_lens and new_lens as for the spec_kv_append that stored the
+    new tokens.  scale: factor of the scores (1 / sqrt(D)); window > 0: a query sees that many tokens, its own
+    included.  Returns out [B, T, Hq, D] (zero in slots past new_lens), or (out, lse) with lse [B, T, Hq] float32, the
+    natural logarithm of the sum of the weights, when return_lse or lse is given.  ws: a workspace of
+    spec_kv_attention_workspace_size bytes (uint8, CUDA); by default one is kept for each stream."""
+    if not q.is_cuda:
+        raise ValueError("spec_* calls take CUDA tensors (copy host data to the GPU first)")
+    dtype = _DTYPES.get(q.dtype)
+    if dtype is None:
+        raise TypeError("queries must be float32 or bfloat16, got %s" % q.dtype)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, Hq, head_dim]")
+    B, T, hq, D = q.shape
+    dev = cache.device
+    _check_heads("q", q, (B, T, hq, cache.head_dim), q.dtype, dev)
+    _check_table(cache, B, page_table, seq_lens, new_lens, status)
+    if out is None:
+        out = _new((B, T, hq, D), q.dtype, dev, stream)
+    else:
+        _check_heads("out", out, (B, T, hq, D), q.dtype, dev)
+    if lse is not None:
+        if lse.dtype != _F32 or lse.shape != (B, T, hq) or not lse.is_contiguous() or lse.device != dev:
+            raise ValueError("lse must be contiguous float32 [B, T, Hq] on the cache's device")
+    elif return_lse:
+        lse = _new((B, T, hq), _F32, dev, stream)
+    L = _lib()
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    qs, os = q.stride(), out.stride()
+    handle = _stream_of(stream, dev)
+
+    def pack(wp, wn):
+        return _PARAMS.pack(B, T, hq, dtype, page_table.shape[1], window, scale, 0, 0, 0, page_table.data_ptr(),
+                            seq_lens.data_ptr(), 0 if new_lens is None else new_lens.data_ptr(), page_table.stride(0),
+                            qs[0], qs[1], qs[2], 0, 0, 0, 0, 0, 0, os[0], os[1], os[2], handle,
+                            0 if status is None else status.data_ptr(), wp, wn)
+
+    if ws is None:
+        nbytes = L.spec_kv_attention_workspace_size(cache._packed, pack(0, 0))
+        ws = _workspace(max(nbytes, 256), dev, stream)
+    code = L.spec_kv_attention(q.data_ptr(), cache._packed, pack(ws.data_ptr(), ws.numel()), out.data_ptr(),
+                               0 if lse is None else lse.data_ptr())
+    if code != binding.SPEC_OK:
+        raise binding.SpecError(code, "spec_kv_attention")
+    return out if lse is None else (out, lse)
+
+
+def spec_kv_attention_workspace_size(cache, B, T, Hq, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of a spec_kv_attention call of this shape (0 if it is invalid)."""
+    prm = _PARAMS.pack(B, T, Hq, _DTYPES.get(dtype, -1), 1, 0, 1.0, 0, 0, 0, 0, 0, 0, *([0] * 13), 0, 0, 0, 0)
+    return int(_lib().spec_kv_attention_workspace_size(cache._packed, prm))
