@@ -1,11 +1,12 @@
 """In-tree build of libspecverify.so (CUDA kernels for sm_103a + the C ABI).
 
-Eight compilation units, one -gencode, compiled in parallel and linked with the
+Nine compilation units, one -gencode, compiled in parallel and linked with the
 shared cudart (so the process keeps a single CUDA runtime with PyTorch): the
 host side of verification (csrc/spec_verify.cu), six groups of its kernels
 (csrc/kernel_unit.cu with SPECV_UNIT = 1..6; both include
-csrc/spec_kernels.cuh), and the paged key/value cache (csrc/spec_kv.cu).  The
-library is written next to this file.
+csrc/spec_kernels.cuh), and the paged key/value cache (csrc/spec_kv.cu, with
+its tensor-core kernel in csrc/spec_kv_mma.cu).  The library is written next to
+this file.
 """
 from __future__ import annotations
 
@@ -23,7 +24,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMPILE_FLAGS = ["-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC"]
 LINK_FLAGS = [*ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath,/usr/local/cuda/lib64"]
 # (source, extra defines); the heaviest units first, so they start first
-UNITS = [("kernel_unit.cu", ["-DSPECV_UNIT=%d" % u]) for u in (6, 5, 2, 1, 4, 3)] + [("spec_kv.cu", []), ("spec_verify.cu", [])]
+UNITS = [("kernel_unit.cu", ["-DSPECV_UNIT=%d" % u]) for u in (6, 5, 2, 1, 4, 3)] + [("spec_kv_mma.cu", []), ("spec_kv.cu", []), ("spec_verify.cu", [])]
 
 
 def nvcc() -> str:

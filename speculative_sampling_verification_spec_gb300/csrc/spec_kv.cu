@@ -4,9 +4,12 @@
 #include "kernel_table.h"
 #include "spec_kv_append.cuh"
 #include "spec_kv_attn.cuh"
+#include "spec_kv_mma.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
+#include <utility>
 
 namespace {
 
@@ -16,6 +19,7 @@ using namespace spec_kv_detail;
 // resident on one (constants, so that the workspace size needs no device).
 constexpr int kSMs = 152;
 constexpr int kGenCtas = kSMs * 4;
+constexpr int kMmaCtas = kSMs * 2;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -91,25 +95,131 @@ const void* append_fn(bool vec, bool warp) {
              : (warp ? append_ptr<E, 1, true>() : append_ptr<E, 1, false>());
 }
 
-// How the attention's work is cut; a function of B, T, Hq, Hkv, D and dtype.
+// How the attention's work is cut; a function of B, T, Hq, Hkv, D and the kernel.
 struct AttnPlan {
   int rows = 0, nrt = 0, nranges = 0, slot_rows = 0;
   size_t off_ml = 0, off_o = 0, ws_bytes = 0;
 };
 
-AttnPlan plan_attention(const spec_kv_cache* c, const spec_kv_params* p) {
+AttnPlan plan_attention(const spec_kv_cache* c, const spec_kv_params* p, bool mma) {
   AttnPlan pl;
   const int64_t rows = static_cast<int64_t>(p->T) * (p->Hq / c->Hkv);
-  pl.rows = kGenRows;
-  pl.slot_rows = kGenRows;
-  pl.nrt = static_cast<int>((rows + kGenRows - 1) / kGenRows);
-  pl.nranges = std::max(1, kGenCtas / pl.nrt);
+  const int most = mma ? 64 : kGenRows;
+  pl.nrt = static_cast<int>((rows + most - 1) / most);
+  // row tiles of equal size, rounded up to what the kernel takes
+  pl.rows = mma ? static_cast<int>((rows + pl.nrt - 1) / pl.nrt + 15) / 16 * 16 : kGenRows;
+  pl.slot_rows = pl.rows;
+  pl.nranges = std::max(1, (mma ? kMmaCtas : kGenCtas) / pl.nrt);
   // with one range nothing is shared, so no partial results
   const size_t slots = pl.nranges > 1 ? static_cast<size_t>(2) * pl.nranges * pl.nrt : 0;
   pl.off_ml = round_up((static_cast<size_t>(p->B) + 1) * sizeof(int32_t), 256);
   pl.off_o = pl.off_ml + round_up(slots * pl.slot_rows * sizeof(float2), 256);
   pl.ws_bytes = pl.off_o + round_up(slots * pl.slot_rows * c->D * sizeof(float), 256);
   return pl;
+}
+
+// The tensor-core kernel serves bfloat16 queries of 64 or 128 channels.
+bool mma_shape(const spec_kv_cache* c, const spec_kv_params* p) {
+  return p->dtype == SPEC_BF16 && (c->D == 64 || c->D == 128);
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeTiled>(f);
+}
+
+// Order of the pool's token, head and page dimensions in a tensor map: by stride,
+// each a multiple of the one before (a dimension of one entry fits anywhere).
+// False: these strides are not a tensor map's, and the general kernel serves them.
+struct MapOrder {
+  int64_t extent[3], stride[3];
+  int box[3], at_head, at_page;
+};
+bool map_order(const spec_kv_cache* c, MapOrder* o) {
+  struct Dim {
+    int64_t extent, stride;
+    int which;
+  } d[3] = {{c->page_size, c->token_stride, 0}, {c->Hkv, c->head_stride, 1}, {c->num_pages, c->page_stride, 2}};
+  for (Dim& x : d)
+    if (x.extent == 1) x.stride = c->D;
+  for (int i = 1; i < 3; ++i)
+    for (int k = i; k > 0 && d[k].stride < d[k - 1].stride; --k) std::swap(d[k], d[k - 1]);
+  int64_t before = c->D;
+  for (int i = 0; i < 3; ++i) {
+    if (d[i].stride < before || d[i].stride % before || d[i].stride >= (int64_t(1) << 40)) return false;
+    before = d[i].stride;
+    o->extent[i] = d[i].extent;
+    o->stride[i] = d[i].stride;
+    o->box[i] = d[i].which == 0 ? c->page_size : 1;
+    if (d[i].which == 1) o->at_head = i;
+    if (d[i].which == 2) o->at_page = i;
+  }
+  return true;
+}
+
+bool make_map(EncodeTiled enc, const spec_kv_cache* c, const MapOrder& o, uint8_t* base, CUtensorMap* map) {
+  const cuuint64_t extent[4] = {static_cast<cuuint64_t>(c->D), static_cast<cuuint64_t>(o.extent[0]),
+                                static_cast<cuuint64_t>(o.extent[1]), static_cast<cuuint64_t>(o.extent[2])};
+  const cuuint64_t stride[3] = {static_cast<cuuint64_t>(o.stride[0]), static_cast<cuuint64_t>(o.stride[1]),
+                                static_cast<cuuint64_t>(o.stride[2])};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(c->D), static_cast<cuuint32_t>(o.box[0]),
+                             static_cast<cuuint32_t>(o.box[1]), static_cast<cuuint32_t>(o.box[2])};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, extent, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             c->D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// dynamic shared memory above 48 KB has to be allowed once for a kernel and device
+bool allow_smem(const void* fn, int slot, int bytes) {
+  static std::atomic<int> allowed[64][16];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (allowed[dev][slot].load(std::memory_order_acquire) >= bytes) return true;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  allowed[dev][slot].store(bytes, std::memory_order_release);
+  return true;
+}
+
+spec_status launch_general(const KvArgs& args, bool f32, int grid, cudaStream_t st) {
+  KvArgs a = args;
+  void* params[] = {&a};
+  const void* fn = f32 ? reinterpret_cast<const void*>(&spec_kv_attention_kernel<float>)
+                       : reinterpret_cast<const void*>(&spec_kv_attention_kernel<__nv_bfloat16>);
+  const int smem = gen_smem_bytes(a.D);
+  if (!allow_smem(fn, f32 ? 8 : 9, smem)) return SPEC_ERR_CUDA;
+  if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kGenThreads), params, smem, st) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  return SPEC_OK;
+}
+
+spec_status launch_mma(const KvArgs& args, const spec_kv_cache* c, const MapOrder& order, int grid, cudaStream_t st) {
+  KvArgs a = args;
+  MmaMaps maps;
+  EncodeTiled enc = encode_tiled();
+  if (!enc || !make_map(enc, c, order, c->k_codes, &maps.k) || !make_map(enc, c, order, c->v_codes, &maps.v))
+    return SPEC_ERR_CUDA;
+  maps.at_head = order.at_head;
+  maps.at_page = order.at_page;
+  int smem = 0;
+  const void* fn = specv_units::kv_mma(a.D, a.rows, &smem);
+  if (!fn || !allow_smem(fn, (a.D == 128 ? 4 : 0) + a.rows / 16 - 1, smem)) return SPEC_ERR_CUDA;
+  void* params[] = {&a, &maps};
+  if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kMmaThreads), params, smem, st) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  return SPEC_OK;
 }
 
 }  // namespace
@@ -184,7 +294,9 @@ spec_status spec_kv_append(const void* q, const void* k, const void* v, const fl
 
 size_t spec_kv_attention_workspace_size(const spec_kv_cache* cache, const spec_kv_params* params) {
   if (check_shapes(cache, params) != SPEC_OK) return 0;
-  return plan_attention(cache, params).ws_bytes;
+  // which kernel serves a call also depends on the cache's strides: room for either
+  const size_t general = plan_attention(cache, params, false).ws_bytes;
+  return mma_shape(cache, params) ? std::max(general, plan_attention(cache, params, true).ws_bytes) : general;
 }
 
 spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const spec_kv_params* params, void* out,
@@ -199,8 +311,12 @@ spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const s
   if (!q || !out || bad_strides(p->q_seq_stride, p->q_tok_stride, p->q_head_stride) ||
       bad_strides(p->o_seq_stride, p->o_tok_stride, p->o_head_stride))
     return SPEC_ERR_INVALID_ARG;
-  const AttnPlan pl = plan_attention(cache, p);
-  if (!p->workspace || !aligned(p->workspace, 256) || p->workspace_bytes < pl.ws_bytes) return SPEC_ERR_INVALID_ARG;
+  if (!p->workspace || !aligned(p->workspace, 256) ||
+      p->workspace_bytes < spec_kv_attention_workspace_size(cache, params))
+    return SPEC_ERR_INVALID_ARG;
+  MapOrder order = {};
+  const bool mma = mma_shape(cache, p) && map_order(cache, &order);
+  const AttnPlan pl = plan_attention(cache, p, mma);
   KvArgs a = {};
   fill_cache(cache, p, a);
   a.q = q;
@@ -212,6 +328,7 @@ spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const s
   a.nrt = pl.nrt;
   a.nranges = pl.nranges;
   a.slot_rows = pl.slot_rows;
+  a.q_vec = aligned(q, 16) && a.q_seq % 8 == 0 && a.q_tok % 8 == 0 && a.q_head % 8 == 0;
   const int64_t ob = 4 * (p->dtype == SPEC_F32 ? 4 : 2);  // bytes of four channels
   a.o_vec = aligned(out, static_cast<uintptr_t>(ob)) && a.o_seq % 4 == 0 && a.o_tok % 4 == 0 && a.o_head % 4 == 0;
   char* ws = static_cast<char*>(p->workspace);
@@ -220,16 +337,10 @@ spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const s
   a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
   const bool f32 = p->dtype == SPEC_F32;
   cudaStream_t st = static_cast<cudaStream_t>(p->stream);
+  const int grid = pl.nranges * pl.nrt;
+  s = mma ? launch_mma(a, cache, order, grid, st) : launch_general(a, f32, grid, st);
+  if (s != SPEC_OK) return s;
   void* args[] = {&a};
-  const void* fn = f32 ? reinterpret_cast<const void*>(&spec_kv_attention_kernel<float>)
-                       : reinterpret_cast<const void*>(&spec_kv_attention_kernel<__nv_bfloat16>);
-  const int smem = gen_smem_bytes(a.D);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return SPEC_ERR_CUDA;
-  if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(pl.nranges * pl.nrt)), dim3(kGenThreads), args, smem, st) !=
-      cudaSuccess)
-    return SPEC_ERR_CUDA;
   // the join kernel is a programmatic dependent launch: it may be scheduled while
   // the last ranges finish, and waits before it reads or writes
   cudaLaunchAttribute attr[1];

@@ -49,6 +49,7 @@ struct KvArgs {
   int32_t rows;       // rows of a row tile (row = t * G + head in group)
   int32_t nrt;        // row tiles of a sequence
   int32_t nranges;    // ranges of the tile list
+  int32_t q_vec;      // queries may be loaded 16 bytes at a time
   int32_t o_vec;      // outputs may be stored four channels at a time
   int32_t slot_rows;  // rows a partial slot has room for
   int32_t* prefix;    // workspace: [B + 1] tiles before each sequence

@@ -1,0 +1,626 @@
+#pragma once
+// spec_kv_mma.cuh -- attention over the paged 8-bit cache on the tensor cores, for
+// bfloat16 queries.
+//
+// The cache's bytes go from memory to the matrix instruction as they are: tensor
+// maps bring a tile of 128 tokens into swizzled shared memory, and both products
+// are 8-bit ones with float accumulators in tensor memory,
+//
+//   S^T [128 tokens x rows]   = K [128 x D]   Q^T [D x rows]
+//   O^T [D x rows]           += V^T [D x 128] P^T [128 x rows].
+//
+// Tokens and channels are the instruction's 128 rows and the query rows its
+// columns, so its cost goes with the rows there are (from 16) and not with 128.
+// A row is a (new token, query head) of one key/value head.
+//
+// What is not 8 bits is carried in two 8-bit pieces of 4 significant bits each:
+//   q / 2^e = hi + lo, two products into one accumulator (a bfloat16 has 8
+//     significant bits: exact but for 2^-17 of the row's largest channel);
+//   p = hi + lo / 16, the pieces side by side as columns of one product and added
+//     at the end (a relative 2^-8 at most, 2^-10.6 on average; sums are of the
+//     float p).
+//
+// A thread of the softmax warps holds one token: the token's two scales are
+// scalars of the thread, applied to the scores in float (the value scale as
+// exponent of 2, so that p is the weight of the 8-bit values).  The running
+// maximum of a row is over the threads; it is not needed exactly, only as a
+// reference that keeps p within the 8-bit range, so it is raised (and the
+// accumulators rescaled) only when a score passes it by more than 2^kSlack.
+//
+// Roles: warps 0-3 softmax and epilogue, warp 4 loads, one thread of warp 5
+// issues the products.  Scores are double-buffered, so the products of the next
+// tile run under the softmax of this one.  Two CTAs share an SM.
+#include <cuda_fp16.h>
+
+#include "spec_kv_attn.cuh"
+#include "spec_kv_append.cuh"
+#include "spec_kv_ptx.cuh"
+
+namespace spec_kv_detail {
+
+constexpr int kMmaThreads = 192;
+constexpr int kScaleRing = 8;       // tiles of scales; a loader is never this far ahead of the softmax
+constexpr int kSlack = 3;           // log2 of how far weights may pass the reference
+constexpr float kShift = 8 - kSlack;  // a raised reference is kShift below the largest score: weights stay within 2^8 < 448
+
+// stages of keys and of values, buffers of weights: what two CTAs an SM leave room for
+template <int D, int NR>
+struct MmaCfg {
+  static constexpr int kTileBytes = kTile * D;
+  static constexpr int KS = D == 64 ? 4 : NR <= 32 ? 3 : NR == 48 ? 3 : 2;
+  static constexpr int VS = D == 64 ? 4 : NR == 16 ? 3 : 2;
+  static constexpr int PB = (D == 64 || NR <= 32) ? 2 : 1;
+  static constexpr int kQBytes = NR * D;             // one piece
+  static constexpr int kPBytes = kTile * 2 * NR;     // both pieces
+  static constexpr int kOffV = 0;                    // values first: a 64-channel operand reads on into what follows
+  static constexpr int kOffK = kOffV + VS * kTileBytes;
+  static constexpr int kOffQ = kOffK + KS * kTileBytes;
+  static constexpr int kOffP = kOffQ + 2 * kQBytes;
+  static constexpr int kOffSmall = kOffP + PB * kPBytes;
+  static constexpr uint32_t kCols = 4 * NR <= 64 ? 64 : 4 * NR <= 128 ? 128 : 256;  // 2 x scores, 2 pieces of output
+};
+
+template <int D, int NR>
+struct MmaSmall {
+  using C = MmaCfg<D, NR>;
+  uint64_t k_full[C::KS], k_empty[C::KS], v_full[C::VS], v_empty[C::VS];
+  uint64_t s_full[2], p_full[C::PB], pv_done[C::PB], sc_full[kScaleRing], q_full, drain;
+  float4 rowtab[NR / 2];  // of two rows: factors of the scores, negated references
+  float2 scales[kScaleRing][kTile / 16];
+  float fac[NR];
+  float red[4][NR];
+  int pos[NR];
+  RangePlan plan;
+  int scratch[kMmaThreads / 32];
+  uint32_t tmem;
+  int gave_up;
+};
+
+template <int D, int NR>
+constexpr int mma_smem_bytes() {
+  return MmaCfg<D, NR>::kOffSmall + static_cast<int>(sizeof(MmaSmall<D, NR>)) + 1024;
+}
+
+// tensor maps of the pool: the channel, then token, head and page in the order of
+// their strides
+struct MmaMaps {
+  CUtensorMap k, v;
+  int32_t at_head, at_page;  // places among the three, 0 to 2
+};
+
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 pack2(float a, float b) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(u64 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// barrier 1: the four softmax warps
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// order-preserving integer image of a float (NaN aside), and back
+__device__ __forceinline__ int order_of(float x) {
+  const int b = __float_as_int(x);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float of_order(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
+// sums over the 32 lanes of 16 or 32 values each; lane r (mod the count) gets value r's
+template <int N>
+__device__ __forceinline__ float lane_sums(float* v) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (N == 16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(kFull, v[i], 16);
+  }
+#pragma unroll
+  for (int w = N / 2; w; w >>= 1) {
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const bool up = lane & w;
+      const float keep = up ? v[i + w] : v[i], send = up ? v[i] : v[i + w];
+      v[i] = keep + __shfl_xor_sync(kFull, send, w);
+    }
+  }
+  return v[0];
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kMmaThreads, 2)
+    spec_kv_attention_mma_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ MmaMaps maps) {
+  using C = MmaCfg<D, NR>;
+  extern __shared__ uint8_t dyn_raw[];
+  uint8_t* dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
+  MmaSmall<D, NR>& sm = *reinterpret_cast<MmaSmall<D, NR>*>(dyn + C::kOffSmall);
+  uint8_t* const sv = dyn + C::kOffV;
+  uint8_t* const sk = dyn + C::kOffK;
+  uint8_t* const sq = dyn + C::kOffQ;
+  uint8_t* const sp = dyn + C::kOffP;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kSwizzle = D == 128 ? kSwizzle128 : kSwizzle64;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::KS; ++i) {
+      bar_init(&sm.k_full[i], 1);
+      bar_init(&sm.k_empty[i], 1);
+    }
+    for (int i = 0; i < C::VS; ++i) {
+      bar_init(&sm.v_full[i], 1);
+      bar_init(&sm.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) bar_init(&sm.s_full[i], 1);
+    for (int i = 0; i < C::PB; ++i) {
+      bar_init(&sm.p_full[i], 4);
+      bar_init(&sm.pv_done[i], 1);
+    }
+    for (int i = 0; i < kScaleRing; ++i) bar_init(&sm.sc_full[i], 1);
+    bar_init(&sm.q_full, 4);
+    bar_init(&sm.drain, 1);
+    sm.gave_up = 0;
+    fence_bar_init();
+  }
+  if (warp == 4 && lane == 0) {
+    tma_prefetch_map(&maps.k);
+    tma_prefetch_map(&maps.v);
+  }
+  if (warp == 5) tmem_alloc(&sm.tmem, C::kCols);
+  const int range = blockIdx.x / a.nrt, rt = blockIdx.x - range * a.nrt;
+  asm volatile("griddepcontrol.launch_dependents;");
+  tc_fence_before();
+  make_plan_range<kMmaThreads>(a, range, &sm.plan, sm.scratch, blockIdx.x == 0 ? a.prefix : nullptr);
+  tc_fence_after();
+  const uint32_t tm = sm.tmem;
+  volatile int* const gave_up = &sm.gave_up;
+
+  if (sm.plan.w0 < sm.plan.w1) {
+    Walk walk = walk_begin(sm.plan, range, rt);
+    Piece p;
+    int n = 0;  // tiles so far, over all pieces
+
+    if (warp == 4) {
+      // ---------------------------------------------------------------- loads
+      const int np = kTile >> a.log_page;  // pages a tile
+      const uint32_t page_bytes = static_cast<uint32_t>(D) << a.log_page;
+      bool ok = true;
+      int nk = -1;
+      while (ok && walk_next(a, walk, p)) {
+        const int end = p.L + p.n;
+        const int first = p.tile0 * np, last = min(p.tile1 * np, (end + (1 << a.log_page) - 1) >> a.log_page);
+        // 32 pages at a time, one a lane: numbers, then scales; the next 32 are under way
+        const auto number = [&](int base) {
+          int pid = 0;
+          if (base + lane < last) {
+            pid = page_of(a, p.b, base + lane);
+            if (pid < 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+          }
+          return pid;
+        };
+        const auto scales = [&](int base, int pid) {
+          float2 s = make_float2(0.0f, 0.0f);
+          if (base + lane < last) {
+            if (pid < 0) {
+              s.x = s.y = __uint_as_float(0x7fc00000u);
+            } else {
+              const int64_t at = pid * a.scale_page_stride + p.h * a.scale_head_stride;
+              s.x = a.k_scale[at];
+              s.y = a.v_scale[at];
+            }
+          }
+          return s;
+        };
+        int base = first;
+        int pid = number(base), pid_next = 0;
+        float2 sc = scales(base, pid), sc_next = make_float2(0.0f, 0.0f);
+        for (int t = p.tile0; t < p.tile1; ++t, ++n) {
+          int in = t * np - base;  // the tile's first page among the 32
+          if (in == 32) {
+            base += 32;
+            in = 0;
+            pid = pid_next;
+            sc = sc_next;
+          }
+          const int mine = lane - in;  // this lane's page of the tile
+          const bool has = mine >= 0 && mine < np && base + lane < last;
+          const int cnt = min(np, last - (base + in));
+          // coordinates after the channel: token 0, the head and the page, in the maps' order
+          const int page = max(pid, 0);
+          const int y = maps.at_head == 0 ? p.h : maps.at_page == 0 ? page : 0;
+          const int z = maps.at_head == 1 ? p.h : maps.at_page == 1 ? page : 0;
+          const int w = maps.at_head == 2 ? p.h : maps.at_page == 2 ? page : 0;
+          const int ks = n % C::KS, vs = n % C::VS;
+          if (n >= C::KS) ok = bar_wait(&sm.k_empty[ks], (n / C::KS - 1) & 1, gave_up);
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          if (lane == 0) bar_arrive_expect(&sm.k_full[ks], cnt * page_bytes);
+          if (mine >= 0 && mine < np) sm.scales[n % kScaleRing][mine] = sc;
+          __syncwarp();
+          if (has)
+            tma_load_4d(sk + ks * C::kTileBytes + mine * page_bytes, &maps.k, 0, y, z, w, &sm.k_full[ks]);
+          if (lane == 0) bar_arrive(&sm.sc_full[n % kScaleRing]);
+          if (n >= C::VS) ok = bar_wait(&sm.v_empty[vs], (n / C::VS - 1) & 1, gave_up);
+          ok = __all_sync(kFull, ok);
+          if (!ok) {
+            nk = n + 1;  // this tile's keys are on their way
+            break;
+          }
+          if (lane == 0) bar_arrive_expect(&sm.v_full[vs], cnt * page_bytes);
+          __syncwarp();
+          if (has)
+            tma_load_4d(sv + vs * C::kTileBytes + mine * page_bytes, &maps.v, 0, y, z, w, &sm.v_full[vs]);
+          if (in == 0) pid_next = number(base + 32);
+          if (in == np) sc_next = scales(base + 32, pid_next);
+        }
+      }
+      if (!ok) {
+        // copies still under way have to land before the CTA ends
+        int quiet = 0;
+        if (nk < 0) nk = n;
+        for (int i = max(0, nk - C::KS); i < nk; ++i) bar_wait(&sm.k_full[i % C::KS], (i / C::KS) & 1, &quiet);
+        quiet = 0;
+        for (int i = max(0, n - C::VS); i < n; ++i) bar_wait(&sm.v_full[i % C::VS], (i / C::VS) & 1, &quiet);
+      }
+    } else if (warp == 5) {
+      // ------------------------------------------------------------- products
+      if (lane == 0) {
+        const uint32_t q0 = smem_u32(sq), k0 = smem_u32(sk), v0 = smem_u32(sv), p0 = smem_u32(sp);
+        constexpr uint32_t kDescS = instr_desc(128, NR, false, false);
+        constexpr uint32_t kDescO = instr_desc(128, 2 * NR, true, true);
+        bool ok = true;
+        int piece = 0;
+        const auto scores = [&](int i) {
+          const int st = i % C::KS;
+          ok = ok && bar_wait(&sm.k_full[st], (i / C::KS) & 1, gave_up);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t d = tm + (i & 1) * NR;
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              mma_f8(d, operand_desc(k0 + st * C::kTileBytes + k * 32, 16, 8 * D, kSwizzle),
+                     operand_desc(q0 + half * C::kQBytes + k * 2 * NR * 16, NR * 16, 128, kSwizzleNone), kDescS,
+                     half + k > 0);
+          mma_commit(&sm.k_empty[st]);
+          mma_commit(&sm.s_full[i & 1]);
+        };
+        while (ok && walk_next(a, walk, p)) {
+          const int m = p.tile1 - p.tile0;
+          if (m == 0) continue;
+          ok = bar_wait(&sm.q_full, piece & 1, gave_up);
+          ++piece;
+          scores(n);
+          if (m > 1) scores(n + 1);
+          for (int i = 0; ok && i < m; ++i, ++n) {
+            ok = bar_wait(&sm.p_full[n % C::PB], (n / C::PB) & 1, gave_up) &&
+                 bar_wait(&sm.v_full[n % C::VS], (n / C::VS) & 1, gave_up);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t va = v0 + (n % C::VS) * C::kTileBytes, pa = p0 + (n % C::PB) * C::kPBytes;
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k)
+              mma_f8(tm + 2 * NR, operand_desc(va + k * 32 * D, kTile * 64, 8 * D, kSwizzle),
+                     operand_desc(pa + k * 32 * 16, 128, kTile * 16, kSwizzleNone), kDescO, i + k > 0);
+            mma_commit(&sm.v_empty[n % C::VS]);
+            mma_commit(&sm.pv_done[n % C::PB]);
+            if (i + 2 < m) scores(n + 2);
+          }
+        }
+        if (!ok) {  // products still running have to end before tensor memory is released
+          int quiet = 0;
+          mma_commit(&sm.drain);
+          bar_wait(&sm.drain, 0, &quiet);
+        }
+      }
+      __syncwarp();
+    } else {
+      // -------------------------------------------------------------- softmax
+      const uint32_t tl = tm + (static_cast<uint32_t>(warp * 32) << 16);  // this warp's lanes
+      const uint32_t tO = tl + 2 * NR;
+      bool fail = false;
+      while (walk_next(a, walk, p)) {
+        const int m = p.tile1 - p.tile0;
+        float l[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) l[r] = 0.0f;
+        soft_sync();  // the piece before has been written out
+        if (m > 0 && !fail) {
+          // queries: 16 channels a thread
+          constexpr int kPer = D / 16;          // threads a row
+          constexpr int kStep = 128 / kPer;     // rows at a time
+          for (int r0 = 0; r0 < NR; r0 += kStep) {
+            const int r = r0 + tid / kPer, c = tid % kPer;
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+            if (r < p.nrows) {
+              const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
+              const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + p.b * a.q_seq + t * a.q_tok +
+                                         (p.h * a.G + g) * a.q_head + c * 16;
+              if (a.q_vec) {
+                load_n<__nv_bfloat16, 8>(src, x);
+                load_n<__nv_bfloat16, 8>(src + 8, x + 8);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = to_float(src[i]);
+              }
+            }
+            uint32_t top = 0;  // bits of the largest magnitude (NaN above infinity)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+            for (int d = kPer / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(kFull, top, d));
+            const bool fin = top < 0x7f800000u;
+            const float s = scale_for(__uint_as_float(top));
+            const float inv = 1.0f / s;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t h4 = 0, l4 = 0;
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const float2 y = make_float2(fin ? x[4 * i + e] * inv : 0.0f, fin ? x[4 * i + e + 1] * inv : 0.0f);
+                const uint16_t ch = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+                const float2 b = codes2_to_float2(ch);
+                const uint16_t cl =
+                    __nv_cvt_float2_to_fp8x2(make_float2(y.x - b.x, y.y - b.y), __NV_SATFINITE, __NV_E4M3);
+                h4 |= static_cast<uint32_t>(ch) << (8 * e);
+                l4 |= static_cast<uint32_t>(cl) << (8 * e);
+              }
+              hi[i] = h4;
+              lo[i] = l4;
+            }
+            if (r < NR) {
+              uint8_t* dst = sq + c * (NR * 16) + r * 16;
+              *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(dst + C::kQBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              if (c == 0) {
+                const bool row = r < p.nrows;
+                float* tab = reinterpret_cast<float*>(&sm.rowtab[r >> 1]);
+                // a row that is not there has a reference no score passes
+                tab[r & 1] = row ? (fin ? s * a.scale2 : __uint_as_float(0x7fc00000u)) : 0.0f;
+                tab[2 + (r & 1)] = row ? -kNoRef : kNoRef;
+                sm.pos[r] = row ? p.L + (p.row0 + r) / a.G : -1;
+              }
+            }
+          }
+          fence_async();
+          soft_sync();
+          if (lane == 0) bar_arrive(&sm.q_full);
+        }
+        const int end = p.L + p.n;
+        const int pos_lo = p.L + p.row0 / a.G, pos_hi = p.L + (p.row0 + p.nrows - 1) / a.G;
+        for (int t = p.tile0; t < p.tile1; ++t, ++n) {
+          const int j = t * kTile + tid;
+          if (!fail) fail = !bar_wait(&sm.sc_full[n % kScaleRing], (n / kScaleRing) & 1, gave_up);
+          float2 sc = sm.scales[n % kScaleRing][tid >> a.log_page];
+          // tiles that some row sees only in part
+          const bool edge = t * kTile + kTile - 1 > pos_lo || (a.window > 0 && t * kTile <= pos_hi - a.window);
+          const bool all_see = j <= pos_lo && (a.window <= 0 || j > pos_hi - a.window);
+          bool poison = false;
+          if (edge && !all_see) {
+            // no row may be touched by what it does not see: values that are not to be read are
+            // zero, NaN codes and scales of a token that some rows see go to those rows' sums
+            if (!fail) fail = !bar_wait(&sm.v_full[n % C::VS], (n / C::VS) & 1, gave_up);
+            uint8_t* row = sv + (n % C::VS) * C::kTileBytes + tid * D;  // whole rows: the swizzle stays inside
+            const bool gone = j >= end;
+            poison = !gone && !(sc.x == sc.x && sc.y == sc.y);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              uint4 w = make_uint4(0, 0, 0, 0);
+              bool write = gone;
+              if (!gone) {
+                w = *reinterpret_cast<const uint4*>(row + i * 16);
+                uint32_t* u = &w.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t nan = __vcmpeq4(u[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  if (nan) {
+                    u[e] &= ~nan;
+                    write = true;
+                    poison = true;
+                  }
+                }
+              }
+              if (write) *reinterpret_cast<uint4*>(row + i * 16) = w;
+            }
+            if (gone || !(sc.x == sc.x && sc.y == sc.y)) sc = make_float2(0.0f, 1.0f);
+          }
+          const float vs = sc.y < 7.8886090522101181e-31f ? 7.8886090522101181e-31f : sc.y;  // 2^-100
+          const float lv = log2f(vs), ivs = 1.0f / vs;
+          const u64 ks2 = pack2(sc.x, sc.x), lv2 = pack2(lv, lv), ivs2 = pack2(ivs, ivs);
+          const uint32_t tS = tl + (n & 1) * NR;
+          if (!fail) fail = !bar_wait(&sm.s_full[n & 1], (n >> 1) & 1, gave_up);
+          tc_fence_after();
+          float x[NR];
+          const auto sees = [&](int r) {
+            const int q = sm.pos[r];
+            return j <= q && (a.window <= 0 || j > q - a.window);
+          };
+          // scores in log2 units against the rows' references
+          const auto load_scores = [&]() {
+#pragma unroll
+            for (int c = 0; c < NR; c += 16) tmem_ld16(tS + c, &x[c]);
+            tmem_wait_ld_all<NR>(x);
+#pragma unroll
+            for (int r = 0; r < NR; r += 2) {
+              const float4 tab = sm.rowtab[r >> 1];
+              const u64 f = mul2(ks2, pack2(tab.x, tab.y));
+              unpack2(fma2(pack2(x[r], x[r + 1]), f, add2(lv2, pack2(tab.z, tab.w))), x[r], x[r + 1]);
+            }
+            if (edge) {
+#pragma unroll
+              for (int r = 0; r < NR; ++r) x[r] = sees(r) ? x[r] : -INFINITY;
+            }
+          };
+          load_scores();
+          float top = x[0];
+#pragma unroll
+          for (int r = 1; r < NR; ++r) top = fmaxf(top, x[r]);
+          // would some weight leave the 8-bit range?
+          if (soft_any(top > 8.0f)) {
+            // raise the references to the largest score so far
+#pragma unroll
+            for (int c = 0; c < NR; c += 16) tmem_ld16(tS + c, &x[c]);
+            tmem_wait_ld_all<NR>(x);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const float* tab = reinterpret_cast<const float*>(&sm.rowtab[r >> 1]);
+              float u = fmaf(x[r], sc.x * tab[r & 1], lv);
+              if (edge && !sees(r)) u = -INFINITY;
+              u = u == u ? u : -INFINITY;
+              const float w = of_order(__reduce_max_sync(kFull, order_of(u)));
+              if (lane == 0) sm.red[warp][r] = w;
+            }
+            soft_sync();
+            if (tid < NR) {
+              float* ref = reinterpret_cast<float*>(&sm.rowtab[tid >> 1]) + 2 + (tid & 1);
+              const float before = -*ref;
+              const float now = fmaxf(before, fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]),
+                                                    fmaxf(sm.red[2][tid], sm.red[3][tid])) - kShift);
+              sm.fac[tid] = now == before ? 1.0f : ex2(before - now);
+              *ref = -now;
+            }
+            soft_sync();
+#pragma unroll
+            for (int r = 0; r < NR; ++r) l[r] *= sm.fac[r];
+            if (t > p.tile0) {
+              if (!fail) fail = !bar_wait(&sm.pv_done[(n - 1) % C::PB], ((n - 1) / C::PB) & 1, gave_up);
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < 2 * NR; c += 16) {
+                float o[16];
+                tmem_ld16(tO + c, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= sm.fac[(c + i) % NR];
+                tmem_st16(tO + c, o);
+              }
+              tmem_wait_st();
+            }
+            load_scores();
+          }
+          // weights: two 8-bit pieces each, 16 rows of a token side by side
+          if (n >= C::PB && !fail) fail = !bar_wait(&sm.pv_done[n % C::PB], (n / C::PB - 1) & 1, gave_up);
+          uint8_t* dst = sp + (n % C::PB) * C::kPBytes + tid * 16;
+#pragma unroll
+          for (int c = 0; c < NR; c += 16) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t h4 = 0, l4 = 0;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int r = c + 4 * i + 2 * e;
+                const float w0 = ex2(x[r]), w1 = ex2(x[r + 1]);
+                unpack2(fma2(pack2(w0, w1), ivs2, pack2(l[r], l[r + 1])), l[r], l[r + 1]);
+                const __half2 h = __floats2half2_rn(w0, w1);
+                const uint16_t ch = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+                const __half2 b(__nv_cvt_fp8x2_to_halfraw2(ch, __NV_E4M3));
+                const __half2 d = __hmul2(__hsub2(h, b), __half2half2(__ushort_as_half(0x4c00)));  // x 16
+                const uint16_t cl = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(d), __NV_SATFINITE, __NV_E4M3);
+                h4 |= static_cast<uint32_t>(ch) << (16 * e);
+                l4 |= static_cast<uint32_t>(cl) << (16 * e);
+              }
+              hi[i] = h4;
+              lo[i] = l4;
+            }
+            *reinterpret_cast<uint4*>(dst + (c / 16) * (kTile * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + (c / 16 + NR / 16) * (kTile * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+          if (poison) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+              if (sees(r)) l[r] = __uint_as_float(0x7fc00000u);
+          }
+          fence_async();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&sm.p_full[n % C::PB]);
+        }
+        // ---- results of the piece
+        if (m > 0 && !fail) fail = !bar_wait(&sm.pv_done[(n - 1) % C::PB], ((n - 1) / C::PB) & 1, gave_up);
+        fail = soft_any(fail);
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c + 32 <= NR; c += 32) sm.red[warp][c + lane] = lane_sums<32>(l + c);
+        if constexpr (NR % 32 != 0) {
+          const float s = lane_sums<16>(l + NR / 32 * 32);
+          if (lane < 16) sm.red[warp][NR / 32 * 32 + lane] = s;
+        }
+        soft_sync();
+        if (tid < p.nrows) {
+          const float ref = m > 0 ? -reinterpret_cast<const float*>(&sm.rowtab[tid >> 1])[2 + (tid & 1)] : kNoRef;
+          float s = sm.red[0][tid] + sm.red[1][tid] + sm.red[2][tid] + sm.red[3][tid];
+          if (fail) s = __uint_as_float(0x7fc00000u);
+          const int gr = p.row0 + tid, t = gr / a.G, g = gr - t * a.G;
+          if (p.whole) {
+            if (a.lse) a.lse[(static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g] = lse_of(ref, s);
+            sm.fac[tid] = 1.0f / s;
+          } else {
+            a.part_ml[static_cast<int64_t>(p.slot) * a.slot_rows + tid] = make_float2(ref, s);
+          }
+        }
+        if (p.whole) soft_sync();
+        if (m > 0 && warp * 32 < D) {
+#pragma unroll
+          for (int c = 0; c < NR; c += 16) {
+            float o[32];  // both pieces
+            tmem_ld16(tO + c, o);
+            tmem_ld16(tO + NR + c, o + 16);
+            tmem_wait_ld_all<32>(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int r = c + i;
+              if (r < p.nrows) {
+                const float x = fmaf(o[16 + i], 0.0625f, o[i]);
+                if (p.whole) {
+                  const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
+                  from_float(x * sm.fac[r], static_cast<__nv_bfloat16*>(a.out) + p.b * a.o_seq + t * a.o_tok +
+                                                (p.h * a.G + g) * a.o_head + tid);
+                } else {
+                  a.part_o[(static_cast<int64_t>(p.slot) * a.slot_rows + r) * D + tid] = x;
+                }
+              }
+            }
+          }
+        }
+        tc_fence_before();
+      }
+      if (fail && tid == 0) report(a.status, SPEC_ERR_TIMEOUT);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tmem_free(tm, C::kCols);
+}
+
+}  // namespace spec_kv_detail

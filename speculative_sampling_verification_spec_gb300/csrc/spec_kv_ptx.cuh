@@ -1,0 +1,155 @@
+#pragma once
+// spec_kv_ptx.cuh -- wrappers of the PTX the tensor-core attention kernel is made
+// of: mbarriers with bounded waits, tensor-map copies, tensor memory and the
+// fifth-generation matrix instruction with its descriptors.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace spec_kv_detail {
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// ---- mbarriers -------------------------------------------------------------
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits at most about two seconds, and no longer than until *gave_up is set (by
+// whichever wait of the CTA ran out first, so that all of them end).  False: gave up.
+static __device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatile int* gave_up) {
+  const uint64_t t0 = now_ns();
+  for (uint32_t i = 0; i < 100000u; ++i) {
+    if (bar_try(b, parity)) return true;
+    if (*gave_up || now_ns() - t0 > 2000000000ull) break;
+  }
+  *gave_up = 1;
+  return false;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* gave_up) {
+  if (bar_try(b, parity)) return true;
+  return bar_wait_slow(b, parity, gave_up);
+}
+
+__device__ __forceinline__ void fence_bar_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+// orders this thread's plain accesses of shared memory before later asynchronous ones
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ---- tensor-map copies -----------------------------------------------------
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// ---- tensor memory ---------------------------------------------------------
+// allocation, release: one whole warp; columns a power of two from 32
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+// 16 consecutive columns of the thread's lane
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const float* x) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// waits for the thread's loads; the 16 values pass through, so that nothing that uses them moves ahead of the wait
+__device__ __forceinline__ void tmem_wait_ld(float* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]),
+                 "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15])
+               :
+               : "memory");
+}
+// the same for N values loaded 16 at a time, with one wait
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld_all(float* x) {
+  tmem_wait_ld(x);
+#pragma unroll
+  for (int c = 16; c < N; c += 16)
+    asm volatile(""
+                 : "+f"(x[c]), "+f"(x[c + 1]), "+f"(x[c + 2]), "+f"(x[c + 3]), "+f"(x[c + 4]), "+f"(x[c + 5]),
+                   "+f"(x[c + 6]), "+f"(x[c + 7]), "+f"(x[c + 8]), "+f"(x[c + 9]), "+f"(x[c + 10]), "+f"(x[c + 11]),
+                   "+f"(x[c + 12]), "+f"(x[c + 13]), "+f"(x[c + 14]), "+f"(x[c + 15]));
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// ---- the matrix instruction ------------------------------------------------
+// Shared-memory operand descriptor: start address, leading and stride byte offsets
+// (all in 16-byte units), the fixed bit of this generation, the swizzle.
+enum { kSwizzleNone = 0, kSwizzle128 = 2, kSwizzle64 = 4 };
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead_bytes, uint32_t stride_bytes, int swizzle) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>((lead_bytes >> 4) & 0x3fffu) << 16) |
+         (static_cast<uint64_t>((stride_bytes >> 4) & 0x3fffu) << 32) | (uint64_t(1) << 46) |
+         (static_cast<uint64_t>(swizzle) << 61);
+}
+// Instruction descriptor: e4m3 operands, float accumulators, M x N; an operand is
+// K-major (its K runs along the contiguous bytes) or else transposed.
+__host__ __device__ constexpr uint32_t instr_desc(int M, int N, bool a_transposed, bool b_transposed) {
+  return (1u << 4) | ((a_transposed ? 1u : 0u) << 15) | ((b_transposed ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D (+)= A B, 32 of K at a time; one thread issues it
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// arrives on the barrier when all matrix instructions issued before are complete
+__device__ __forceinline__ void mma_commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(b))
+               : "memory");
+}
+
+}  // namespace spec_kv_detail
