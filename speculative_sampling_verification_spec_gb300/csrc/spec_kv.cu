@@ -95,6 +95,11 @@ const void* append_fn(bool vec, bool warp) {
              : (warp ? append_ptr<E, 1, true>() : append_ptr<E, 1, false>());
 }
 
+template <typename E, bool CTA>
+const void* join_ptr() {
+  return reinterpret_cast<const void*>(&spec_kv_join_kernel<E, CTA>);
+}
+
 // How the attention's work is cut; a function of B, T, Hq, Hkv, D and the kernel.
 struct AttnPlan {
   int rows = 0, nrt = 0, nranges = 0, slot_rows = 0;
@@ -348,13 +353,15 @@ spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+  // with few rows beside the ranges, a row can be cut into many parts: a CTA for each
+  const bool wide = rows <= 4 * kSMs * 16 && pl.nranges > 8 * static_cast<int64_t>(a.B) * a.Hkv;
+  cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + kJoinWarps - 1) / kJoinWarps));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const void* jn = f32 ? reinterpret_cast<const void*>(&spec_kv_join_kernel<float>)
-                       : reinterpret_cast<const void*>(&spec_kv_join_kernel<__nv_bfloat16>);
+  const void* jn = f32 ? (wide ? join_ptr<float, true>() : join_ptr<float, false>())
+                       : (wide ? join_ptr<__nv_bfloat16, true>() : join_ptr<__nv_bfloat16, false>());
   if (cudaLaunchKernelExC(&cfg, jn, args) != cudaSuccess) return SPEC_ERR_CUDA;
   specv_units::count_launches(2);
   return SPEC_OK;

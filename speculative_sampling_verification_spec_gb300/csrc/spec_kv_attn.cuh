@@ -225,9 +225,11 @@ __global__ void __launch_bounds__(kGenThreads) spec_kv_attention_kernel(const __
   }
 }
 
-// One warp a row (sequence, token, query head): rows shared by several ranges are
-// added up in the order of the ranges; rows with nothing to attend are zero, rows
-// of a sequence with bad lengths NaN; the others are written already.
+// Rows (sequence, token, query head) shared by several ranges are added up in the
+// order of the ranges; rows with nothing to attend are zero, rows of a sequence
+// with bad lengths NaN; the others are written already.  A row is a warp's, or,
+// where rows are cut into many parts, a CTA's, whose warps take every fourth part
+// (the order of the sum is then fixed too).
 constexpr int kJoinWarps = 4;
 
 template <typename E>
@@ -251,11 +253,13 @@ __device__ __forceinline__ void store4(const KvArgs& a, E* o, float4 x) {
   from_float(x.w, o + 3);
 }
 
-template <typename E>
+template <typename E, bool CTA>
 __global__ void __launch_bounds__(32 * kJoinWarps) spec_kv_join_kernel(const __grid_constant__ KvArgs a) {
-  const int lane = threadIdx.x & 31;
+  __shared__ __align__(16) float4 part_o[CTA ? kJoinWarps : 1][64];
+  __shared__ float part_l[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
-  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  const int64_t mine = CTA ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
   const int64_t row = mine < rows ? mine : rows - 1;
   const int hq = static_cast<int>(row % a.Hq);
   const int64_t bt = row / a.Hq;
@@ -265,6 +269,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) spec_kv_join_kernel(const __g
   if (mine >= rows) return;
   E* o = static_cast<E*>(a.out) + b * a.o_seq + t * a.o_tok + hq * a.o_head;
   if (s.bad || t >= s.n) {
+    if (CTA && warp > 0) return;
     const float x = s.bad ? __uint_as_float(0x7fc00000u) : 0.0f;
     for (int d = lane * 4; d < a.D; d += 128) store4(a, o + d, make_float4(x, x, x, x));
     if (lane == 0) {
@@ -284,41 +289,53 @@ __global__ void __launch_bounds__(32 * kJoinWarps) spec_kv_join_kernel(const __g
     return static_cast<int64_t>(2 * (c * a.nrt + rt) + (c == c0 ? 1 : 0)) * a.slot_rows + r;
   };
   float top = kNoRef;
-  for (int c = c0 + lane; c <= c1; c += 32) {
-    const float2 ml = a.part_ml[slot_row(c)];
-    top = fmaxf(top, ml.x);
-  }
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, a.part_ml[slot_row(c)].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
   float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
   float l = 0.0f;
-  for (int cb = c0; cb <= c1; cb += 32) {
-    // weights of up to 32 parts, one a lane
+  constexpr int kStep = CTA ? kJoinWarps : 1;
+  for (int cb = c0 + (CTA ? warp : 0); cb <= c1; cb += 32 * kStep) {
+    // weights of up to 32 parts, one a lane; a part without tokens for this row left no output
     float wl = 0.0f, ll = 0.0f;
-    if (cb + lane <= c1) {
-      const float2 ml = a.part_ml[slot_row(cb + lane)];
-      if (!(ml.y == 0.0f)) {  // a part without tokens for this row left no output
-        wl = exp2f(ml.x - top);
-        ll = ml.y;
-      }
+    if (cb + lane * kStep <= c1) {
+      const float2 ml = a.part_ml[slot_row(cb + lane * kStep)];
+      ll = ml.y;
+      wl = exp2f(ml.x - top);
     }
-    const int m = min(32, c1 - cb + 1);
-#pragma unroll 4
+    const int m = min(32, (c1 - cb) / kStep + 1);
+#pragma unroll 8
     for (int i = 0; i < m; ++i) {
       const float w = __shfl_sync(kFull, wl, i), li = __shfl_sync(kFull, ll, i);
-      if (li == 0.0f) continue;
-      l = fmaf(w, li, l);
-      const float* po = a.part_o + slot_row(cb + i) * a.D;
+      const bool none = li == 0.0f;
+      const float* po = a.part_o + slot_row(cb + i * kStep) * a.D;
+      l = none ? l : fmaf(w, li, l);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int d = lane * 4 + k * 128;
         if (d < a.D) {
           const float4 x = *reinterpret_cast<const float4*>(po + d);
-          acc[k].x = fmaf(w, x.x, acc[k].x);
-          acc[k].y = fmaf(w, x.y, acc[k].y);
-          acc[k].z = fmaf(w, x.z, acc[k].z);
-          acc[k].w = fmaf(w, x.w, acc[k].w);
+          acc[k].x = none ? acc[k].x : fmaf(w, x.x, acc[k].x);
+          acc[k].y = none ? acc[k].y : fmaf(w, x.y, acc[k].y);
+          acc[k].z = none ? acc[k].z : fmaf(w, x.z, acc[k].z);
+          acc[k].w = none ? acc[k].w : fmaf(w, x.w, acc[k].w);
         }
+      }
+    }
+  }
+  if constexpr (CTA) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) part_o[warp][lane + 32 * k] = acc[k];
+    if (lane == 0) part_l[warp] = l;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) {
+      l += part_l[w];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 x = part_o[w][lane + 32 * k];
+        acc[k] = make_float4(acc[k].x + x.x, acc[k].y + x.y, acc[k].z + x.z, acc[k].w + x.w);
       }
     }
   }

@@ -27,9 +27,10 @@
 // reference that keeps p within the 8-bit range, so it is raised (and the
 // accumulators rescaled) only when a score passes it by more than 2^kSlack.
 //
-// Roles: warps 0-3 softmax and epilogue, warp 4 loads, one thread of warp 5
-// issues the products.  Scores are double-buffered, so the products of the next
-// tile run under the softmax of this one.  Two CTAs share an SM.
+// Roles: warps 0-3 and 4-7 softmax and epilogue, each four warps for half of the
+// rows; warp 8 loads; one thread of warp 9 issues the products.  Scores are
+// double-buffered, so the products of the next tile run under the softmax of this
+// one.  Two CTAs share an SM.
 #include <cuda_fp16.h>
 
 #include "spec_kv_attn.cuh"
@@ -38,7 +39,8 @@
 
 namespace spec_kv_detail {
 
-constexpr int kMmaThreads = 192;
+constexpr int kMmaThreads = 320;
+constexpr int kSoftThreads = 256;  // two groups of 128, a token a thread
 constexpr int kScaleRing = 8;       // tiles of scales; a loader is never this far ahead of the softmax
 constexpr int kSlack = 3;           // log2 of how far weights may pass the reference
 constexpr float kShift = 8 - kSlack;  // a raised reference is kShift below the largest score: weights stay within 2^8 < 448
@@ -66,9 +68,11 @@ struct MmaSmall {
   uint64_t k_full[C::KS], k_empty[C::KS], v_full[C::VS], v_empty[C::VS];
   uint64_t s_full[2], p_full[C::PB], pv_done[C::PB], sc_full[kScaleRing], q_full, drain;
   float4 rowtab[NR / 2];  // of two rows: factors of the scores, negated references
-  float2 scales[kScaleRing][kTile / 16];
-  float fac[NR];
-  float red[4][NR];
+  float4 scales[kScaleRing][kTile / 16];  // of a page: key scale; value scale's log2 and reciprocal
+  int64_t out_at[NR];     // element of the output (of lse for `lse_at`) where a row begins
+  int64_t lse_at[NR];
+  alignas(16) float fac[NR];
+  alignas(16) float red[4][NR];
   int pos[NR];
   RangePlan plan;
   int scratch[kMmaThreads / 32];
@@ -111,14 +115,43 @@ __device__ __forceinline__ u64 add2(u64 a, u64 b) {
   return r;
 }
 
-// barrier 1: the four softmax warps
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// barriers 1 and 2: a group of four softmax warps; barrier 3: both groups
+// (constant numbers: with a computed one the CTA would claim all sixteen)
+__device__ __forceinline__ void group_sync(int group) {
+  if (group == 0)
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+  else
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ bool group_any(int group, bool x) {
+  uint32_t r;
+  if (group == 0)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(x ? 1u : 0u)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(x ? 1u : 0u)
+        : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ bool soft_any(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "bar.red.or.pred q, 3, 256, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(x ? 1u : 0u)
@@ -133,14 +166,14 @@ __device__ __forceinline__ int order_of(float x) {
 }
 __device__ __forceinline__ float of_order(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
-// sums over the 32 lanes of 16 or 32 values each; lane r (mod the count) gets value r's
+// sums over the 32 lanes of N = 8, 16 or 32 values each; lane r (mod N) gets value r's
 template <int N>
 __device__ __forceinline__ float lane_sums(float* v) {
   const int lane = threadIdx.x & 31;
-  if constexpr (N == 16) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(kFull, v[i], 16);
-  }
+  for (int w = 16; w >= N; w >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], w);
 #pragma unroll
   for (int w = N / 2; w; w >>= 1) {
 #pragma unroll
@@ -151,6 +184,15 @@ __device__ __forceinline__ float lane_sums(float* v) {
     }
   }
   return v[0];
+}
+
+// the e4m3 codes of two floats' nearest halves, and of 16 times what they leave over
+__device__ __forceinline__ void two_pieces(float w0, float w1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(w0, w1);
+  hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+  const __half2 b(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3));
+  const __half2 d = __hmul2(__hsub2(h, b), __half2half2(__ushort_as_half(0x4c00)));  // x 16
+  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(d), __NV_SATFINITE, __NV_E4M3);
 }
 
 template <int D, int NR>
@@ -178,20 +220,20 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
     }
     for (int i = 0; i < 2; ++i) bar_init(&sm.s_full[i], 1);
     for (int i = 0; i < C::PB; ++i) {
-      bar_init(&sm.p_full[i], 4);
+      bar_init(&sm.p_full[i], kSoftThreads / 32);
       bar_init(&sm.pv_done[i], 1);
     }
     for (int i = 0; i < kScaleRing; ++i) bar_init(&sm.sc_full[i], 1);
-    bar_init(&sm.q_full, 4);
+    bar_init(&sm.q_full, 1);
     bar_init(&sm.drain, 1);
     sm.gave_up = 0;
     fence_bar_init();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == 8 && lane == 0) {
     tma_prefetch_map(&maps.k);
     tma_prefetch_map(&maps.v);
   }
-  if (warp == 5) tmem_alloc(&sm.tmem, C::kCols);
+  if (warp == 9) tmem_alloc(&sm.tmem, C::kCols);
   const int range = blockIdx.x / a.nrt, rt = blockIdx.x - range * a.nrt;
   asm volatile("griddepcontrol.launch_dependents;");
   tc_fence_before();
@@ -205,7 +247,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
     Piece p;
     int n = 0;  // tiles so far, over all pieces
 
-    if (warp == 4) {
+    if (warp == 8) {
       // ---------------------------------------------------------------- loads
       const int np = kTile >> a.log_page;  // pages a tile
       const uint32_t page_bytes = static_cast<uint32_t>(D) << a.log_page;
@@ -224,7 +266,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           return pid;
         };
         const auto scales = [&](int base, int pid) {
-          float2 s = make_float2(0.0f, 0.0f);
+          float2 s = make_float2(0.0f, 1.0f);
           if (base + lane < last) {
             if (pid < 0) {
               s.x = s.y = __uint_as_float(0x7fc00000u);
@@ -260,7 +302,10 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           ok = __all_sync(kFull, ok);
           if (!ok) break;
           if (lane == 0) bar_arrive_expect(&sm.k_full[ks], cnt * page_bytes);
-          if (mine >= 0 && mine < np) sm.scales[n % kScaleRing][mine] = sc;
+          if (mine >= 0 && mine < np) {
+            const float v = sc.y < 7.8886090522101181e-31f ? 7.8886090522101181e-31f : sc.y;  // 2^-100
+            sm.scales[n % kScaleRing][mine] = make_float4(sc.x, log2f(v), 1.0f / v, 0.0f);
+          }
           __syncwarp();
           if (has)
             tma_load_4d(sk + ks * C::kTileBytes + mine * page_bytes, &maps.k, 0, y, z, w, &sm.k_full[ks]);
@@ -287,7 +332,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         quiet = 0;
         for (int i = max(0, n - C::VS); i < n; ++i) bar_wait(&sm.v_full[i % C::VS], (i / C::VS) & 1, &quiet);
       }
-    } else if (warp == 5) {
+    } else if (warp == 9) {
       // ------------------------------------------------------------- products
       if (lane == 0) {
         const uint32_t q0 = smem_u32(sq), k0 = smem_u32(sk), v0 = smem_u32(sv), p0 = smem_u32(sp);
@@ -342,19 +387,31 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       __syncwarp();
     } else {
       // -------------------------------------------------------------- softmax
-      const uint32_t tl = tm + (static_cast<uint32_t>(warp * 32) << 16);  // this warp's lanes
-      const uint32_t tO = tl + 2 * NR;
+      constexpr int RT = NR / 2;                 // rows of a group
+      constexpr int CH = RT % 16 == 0 ? 16 : 8;  // rows at a time
+      constexpr bool kHold = RT <= 24;           // the scores of a tile stay in registers between max and weights
+      const int group = warp >> 2, token = tid & 127, r_base = group * RT;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;  // tensor memory lanes of this warp
+      const uint32_t tO = tm + lanes + 2 * NR + r_base;                     // first pieces; the second NR further
       bool fail = false;
       while (walk_next(a, walk, p)) {
         const int m = p.tile1 - p.tile0;
-        float l[NR];
+        float l[RT];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) l[r] = 0.0f;
+        for (int r = 0; r < RT; ++r) l[r] = 0.0f;
         soft_sync();  // the piece before has been written out
+        if (tid < NR) {
+          const bool row = tid < p.nrows;
+          const int gr = p.row0 + tid, t = gr / a.G, g = gr - t * a.G;
+          sm.pos[tid] = row ? p.L + t : -1;
+          sm.out_at[tid] = p.b * a.o_seq + t * a.o_tok + (p.h * a.G + g) * a.o_head;
+          sm.lse_at[tid] = (static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g;
+        }
         if (m > 0 && !fail) {
           // queries: 16 channels a thread
-          constexpr int kPer = D / 16;          // threads a row
-          constexpr int kStep = 128 / kPer;     // rows at a time
+          constexpr int kPer = D / 16;                 // threads a row
+          constexpr int kStep = kSoftThreads / kPer;   // rows at a time
+#pragma unroll 1
           for (int r0 = 0; r0 < NR; r0 += kStep) {
             const int r = r0 + tid / kPer, c = tid % kPer;
             float x[16];
@@ -379,7 +436,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             for (int d = kPer / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(kFull, top, d));
             const bool fin = top < 0x7f800000u;
             const float s = scale_for(__uint_as_float(top));
-            const float inv = 1.0f / s;
+            const float inv = fin ? 1.0f / s : 0.0f;
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -407,157 +464,182 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
                 // a row that is not there has a reference no score passes
                 tab[r & 1] = row ? (fin ? s * a.scale2 : __uint_as_float(0x7fc00000u)) : 0.0f;
                 tab[2 + (r & 1)] = row ? -kNoRef : kNoRef;
-                sm.pos[r] = row ? p.L + (p.row0 + r) / a.G : -1;
               }
             }
           }
           fence_async();
           soft_sync();
-          if (lane == 0) bar_arrive(&sm.q_full);
+          if (tid == 0) bar_arrive(&sm.q_full);
         }
         const int end = p.L + p.n;
         const int pos_lo = p.L + p.row0 / a.G, pos_hi = p.L + (p.row0 + p.nrows - 1) / a.G;
         for (int t = p.tile0; t < p.tile1; ++t, ++n) {
-          const int j = t * kTile + tid;
+          const int j = t * kTile + token;
           if (!fail) fail = !bar_wait(&sm.sc_full[n % kScaleRing], (n / kScaleRing) & 1, gave_up);
-          float2 sc = sm.scales[n % kScaleRing][tid >> a.log_page];
+          float4 sc = sm.scales[n % kScaleRing][token >> a.log_page];
           // tiles that some row sees only in part
           const bool edge = t * kTile + kTile - 1 > pos_lo || (a.window > 0 && t * kTile <= pos_hi - a.window);
-          const bool all_see = j <= pos_lo && (a.window <= 0 || j > pos_hi - a.window);
           bool poison = false;
-          if (edge && !all_see) {
+          if (edge) {
             // no row may be touched by what it does not see: values that are not to be read are
             // zero, NaN codes and scales of a token that some rows see go to those rows' sums
-            if (!fail) fail = !bar_wait(&sm.v_full[n % C::VS], (n / C::VS) & 1, gave_up);
-            uint8_t* row = sv + (n % C::VS) * C::kTileBytes + tid * D;  // whole rows: the swizzle stays inside
+            const bool all_see = j <= pos_lo && (a.window <= 0 || j > pos_hi - a.window);
             const bool gone = j >= end;
-            poison = !gone && !(sc.x == sc.x && sc.y == sc.y);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              uint4 w = make_uint4(0, 0, 0, 0);
-              bool write = gone;
-              if (!gone) {
-                w = *reinterpret_cast<const uint4*>(row + i * 16);
-                uint32_t* u = &w.x;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t nan = __vcmpeq4(u[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                  if (nan) {
-                    u[e] &= ~nan;
-                    write = true;
-                    poison = true;
-                  }
-                }
-              }
-              if (write) *reinterpret_cast<uint4*>(row + i * 16) = w;
+            const bool bad_scale = !(sc.x == sc.x && sc.z == sc.z);
+            uint8_t* row = sv + (n % C::VS) * C::kTileBytes + token * D;  // whole rows: the swizzle stays inside
+            if (!fail) fail = !bar_wait(&sm.v_full[n % C::VS], (n / C::VS) & 1, gave_up);
+            if (!all_see && !gone) {
+              uint32_t nan = 0;
+#pragma unroll 4
+              for (int i = 0; i < D / 4; ++i)
+                nan |= __vcmpeq4(reinterpret_cast<const uint32_t*>(row)[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              poison = nan != 0 || bad_scale;
             }
-            if (gone || !(sc.x == sc.x && sc.y == sc.y)) sc = make_float2(0.0f, 1.0f);
+            soft_sync();  // both groups have looked
+            if (gone || poison) {
+#pragma unroll 4
+              for (int i = 0; i < D / 16; ++i) reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
+              if (gone || bad_scale) sc = make_float4(0.0f, 0.0f, 1.0f, 0.0f);
+            }
           }
-          const float vs = sc.y < 7.8886090522101181e-31f ? 7.8886090522101181e-31f : sc.y;  // 2^-100
-          const float lv = log2f(vs), ivs = 1.0f / vs;
-          const u64 ks2 = pack2(sc.x, sc.x), lv2 = pack2(lv, lv), ivs2 = pack2(ivs, ivs);
-          const uint32_t tS = tl + (n & 1) * NR;
+          const u64 ks2 = pack2(sc.x, sc.x), lv2 = pack2(sc.y, sc.y), ivs2 = pack2(sc.z, sc.z);
+          const uint32_t tS = tm + lanes + (n & 1) * NR + r_base;
           if (!fail) fail = !bar_wait(&sm.s_full[n & 1], (n >> 1) & 1, gave_up);
           tc_fence_after();
-          float x[NR];
           const auto sees = [&](int r) {
-            const int q = sm.pos[r];
+            const int q = sm.pos[r_base + r];
             return j <= q && (a.window <= 0 || j > q - a.window);
           };
-          // scores in log2 units against the rows' references
-          const auto load_scores = [&]() {
+          // scores of rows c.. in log2 units against their references
+          const auto against_refs = [&](int c, float* x) {
 #pragma unroll
-            for (int c = 0; c < NR; c += 16) tmem_ld16(tS + c, &x[c]);
-            tmem_wait_ld_all<NR>(x);
-#pragma unroll
-            for (int r = 0; r < NR; r += 2) {
-              const float4 tab = sm.rowtab[r >> 1];
+            for (int i = 0; i < CH; i += 2) {
+              const float4 tab = sm.rowtab[(r_base + c + i) >> 1];
               const u64 f = mul2(ks2, pack2(tab.x, tab.y));
-              unpack2(fma2(pack2(x[r], x[r + 1]), f, add2(lv2, pack2(tab.z, tab.w))), x[r], x[r + 1]);
+              unpack2(fma2(pack2(x[i], x[i + 1]), f, add2(lv2, pack2(tab.z, tab.w))), x[i], x[i + 1]);
             }
             if (edge) {
 #pragma unroll
-              for (int r = 0; r < NR; ++r) x[r] = sees(r) ? x[r] : -INFINITY;
+              for (int i = 0; i < CH; ++i) x[i] = sees(c + i) ? x[i] : -INFINITY;
             }
           };
-          load_scores();
-          float top = x[0];
+          float x[kHold ? RT : CH];
+          while (true) {
+            float top = -INFINITY;
+            if constexpr (kHold) {
 #pragma unroll
-          for (int r = 1; r < NR; ++r) top = fmaxf(top, x[r]);
-          // would some weight leave the 8-bit range?
-          if (soft_any(top > 8.0f)) {
-            // raise the references to the largest score so far
-#pragma unroll
-            for (int c = 0; c < NR; c += 16) tmem_ld16(tS + c, &x[c]);
-            tmem_wait_ld_all<NR>(x);
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              const float* tab = reinterpret_cast<const float*>(&sm.rowtab[r >> 1]);
-              float u = fmaf(x[r], sc.x * tab[r & 1], lv);
-              if (edge && !sees(r)) u = -INFINITY;
-              u = u == u ? u : -INFINITY;
-              const float w = of_order(__reduce_max_sync(kFull, order_of(u)));
-              if (lane == 0) sm.red[warp][r] = w;
+              for (int c = 0; c < RT; c += CH) tmem_ld<CH>(tS + c, &x[c]);
+              tmem_wait_ld();
             }
-            soft_sync();
-            if (tid < NR) {
-              float* ref = reinterpret_cast<float*>(&sm.rowtab[tid >> 1]) + 2 + (tid & 1);
+#pragma unroll
+            for (int c = 0; c < RT; c += CH) {
+              float* y = &x[kHold ? c : 0];
+              if constexpr (!kHold) {
+                tmem_ld<CH>(tS + c, y);
+                tmem_wait_ld();
+              }
+              tmem_tie<CH>(y);
+              against_refs(c, y);
+#pragma unroll
+              for (int i = 0; i < CH; i += 2) top = fmaxf(top, fmaxf(y[i], y[i + 1]));
+            }
+            // would some weight leave the 8-bit range?
+            if (!group_any(group, top > 8.0f)) break;
+            // raise the references to the largest score so far
+#pragma unroll 1
+            for (int c = 0; c < RT; c += CH) {
+              float y[CH];
+              tmem_ld<CH>(tS + c, y);
+              tmem_wait_ld();
+              tmem_tie<CH>(y);
+              float mine = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < CH; ++i) {
+                const float* tab = reinterpret_cast<const float*>(&sm.rowtab[(r_base + c + i) >> 1]);
+                float u = fmaf(y[i], sc.x * tab[i & 1], sc.y);
+                if (edge && !sees(c + i)) u = -INFINITY;
+                u = u == u ? u : -INFINITY;
+                const float w = of_order(__reduce_max_sync(kFull, order_of(u)));
+                if (lane == i) mine = w;
+              }
+              if (lane < CH) sm.red[warp & 3][r_base + c + lane] = mine;
+            }
+            group_sync(group);
+            if (token < RT) {
+              const int r = r_base + token;
+              float* ref = reinterpret_cast<float*>(&sm.rowtab[r >> 1]) + 2 + (r & 1);
               const float before = -*ref;
-              const float now = fmaxf(before, fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]),
-                                                    fmaxf(sm.red[2][tid], sm.red[3][tid])) - kShift);
-              sm.fac[tid] = now == before ? 1.0f : ex2(before - now);
+              const float now =
+                  fmaxf(before, fmaxf(fmaxf(sm.red[0][r], sm.red[1][r]), fmaxf(sm.red[2][r], sm.red[3][r])) - kShift);
+              sm.fac[r] = now == before ? 1.0f : ex2(before - now);
               *ref = -now;
             }
-            soft_sync();
-#pragma unroll
-            for (int r = 0; r < NR; ++r) l[r] *= sm.fac[r];
+            group_sync(group);
             if (t > p.tile0) {
+#pragma unroll
+              for (int r = 0; r < RT; r += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&sm.fac[r_base + r]);
+                l[r] *= f.x;
+                l[r + 1] *= f.y;
+                l[r + 2] *= f.z;
+                l[r + 3] *= f.w;
+              }
               if (!fail) fail = !bar_wait(&sm.pv_done[(n - 1) % C::PB], ((n - 1) / C::PB) & 1, gave_up);
               tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < 2 * RT; c += CH) {
+                const int r = c < RT ? c : c - RT;
+                const uint32_t at = tO + r + (c < RT ? 0 : NR);
+                float o[CH];
+                tmem_ld<CH>(at, o);
+                tmem_wait_ld();
+                tmem_tie<CH>(o);
 #pragma unroll
-              for (int c = 0; c < 2 * NR; c += 16) {
-                float o[16];
-                tmem_ld16(tO + c, o);
-                tmem_wait_ld(o);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] *= sm.fac[(c + i) % NR];
-                tmem_st16(tO + c, o);
+                for (int i = 0; i < CH; ++i) o[i] *= sm.fac[r_base + r + i];
+                tmem_st<CH>(at, o);
               }
               tmem_wait_st();
             }
-            load_scores();
           }
           // weights: two 8-bit pieces each, 16 rows of a token side by side
           if (n >= C::PB && !fail) fail = !bar_wait(&sm.pv_done[n % C::PB], (n / C::PB - 1) & 1, gave_up);
-          uint8_t* dst = sp + (n % C::PB) * C::kPBytes + tid * 16;
+          uint8_t* dst = sp + (n % C::PB) * C::kPBytes + token * 16;
 #pragma unroll
-          for (int c = 0; c < NR; c += 16) {
-            uint32_t hi[4], lo[4];
+          for (int c = 0; c < RT; c += CH) {
+            float* y = &x[kHold ? c : 0];
+            if constexpr (!kHold) {
+              tmem_ld<CH>(tS + c, y);
+              tmem_wait_ld();
+              tmem_tie<CH>(y);
+              against_refs(c, y);
+            }
+            uint32_t hi[CH / 4], lo[CH / 4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t h4 = 0, l4 = 0;
+            for (int i = 0; i < CH; i += 4) {
+              uint32_t h[2], d[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int r = c + 4 * i + 2 * e;
-                const float w0 = ex2(x[r]), w1 = ex2(x[r + 1]);
+                const int r = c + i + 2 * e;
+                const float w0 = ex2(y[i + 2 * e]), w1 = ex2(y[i + 2 * e + 1]);
                 unpack2(fma2(pack2(w0, w1), ivs2, pack2(l[r], l[r + 1])), l[r], l[r + 1]);
-                const __half2 h = __floats2half2_rn(w0, w1);
-                const uint16_t ch = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
-                const __half2 b(__nv_cvt_fp8x2_to_halfraw2(ch, __NV_E4M3));
-                const __half2 d = __hmul2(__hsub2(h, b), __half2half2(__ushort_as_half(0x4c00)));  // x 16
-                const uint16_t cl = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(d), __NV_SATFINITE, __NV_E4M3);
-                h4 |= static_cast<uint32_t>(ch) << (16 * e);
-                l4 |= static_cast<uint32_t>(cl) << (16 * e);
+                two_pieces(w0, w1, h[e], d[e]);
               }
-              hi[i] = h4;
-              lo[i] = l4;
+              hi[i / 4] = h[0] | (h[1] << 16);
+              lo[i / 4] = d[0] | (d[1] << 16);
             }
-            *reinterpret_cast<uint4*>(dst + (c / 16) * (kTile * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dst + (c / 16 + NR / 16) * (kTile * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            const int r = r_base + c;
+            uint8_t* at = dst + (r / 16) * (kTile * 16) + (r % 16);
+            if constexpr (CH == 16) {
+              *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(at + (NR / 16) * (kTile * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+              *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(at + (NR / 16) * (kTile * 16)) = make_uint2(lo[0], lo[1]);
+            }
           }
           if (poison) {
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
+            for (int r = 0; r < RT; ++r)
               if (sees(r)) l[r] = __uint_as_float(0x7fc00000u);
           }
           fence_async();
@@ -570,44 +652,41 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         fail = soft_any(fail);
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c + 32 <= NR; c += 32) sm.red[warp][c + lane] = lane_sums<32>(l + c);
-        if constexpr (NR % 32 != 0) {
-          const float s = lane_sums<16>(l + NR / 32 * 32);
-          if (lane < 16) sm.red[warp][NR / 32 * 32 + lane] = s;
+        for (int c = 0; c < RT; c += CH) {
+          const float s = lane_sums<CH>(l + c);
+          if (lane < CH) sm.red[warp & 3][r_base + c + lane] = s;
         }
         soft_sync();
         if (tid < p.nrows) {
           const float ref = m > 0 ? -reinterpret_cast<const float*>(&sm.rowtab[tid >> 1])[2 + (tid & 1)] : kNoRef;
           float s = sm.red[0][tid] + sm.red[1][tid] + sm.red[2][tid] + sm.red[3][tid];
           if (fail) s = __uint_as_float(0x7fc00000u);
-          const int gr = p.row0 + tid, t = gr / a.G, g = gr - t * a.G;
           if (p.whole) {
-            if (a.lse) a.lse[(static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g] = lse_of(ref, s);
+            if (a.lse) a.lse[sm.lse_at[tid]] = lse_of(ref, s);
             sm.fac[tid] = 1.0f / s;
           } else {
             a.part_ml[static_cast<int64_t>(p.slot) * a.slot_rows + tid] = make_float2(ref, s);
           }
         }
         if (p.whole) soft_sync();
-        if (m > 0 && warp * 32 < D) {
+        if (m > 0 && (warp & 3) * 32 < D) {
+          float* part = a.part_o + (static_cast<int64_t>(p.slot) * a.slot_rows + r_base) * D + token;
+#pragma unroll 1
+          for (int c = 0; c < RT; c += 8) {
+            float o[16];  // both pieces of eight rows
+            tmem_ld<8>(tO + c, o);
+            tmem_ld<8>(tO + NR + c, o + 8);
+            tmem_wait_ld();
+            tmem_tie<16>(o);
 #pragma unroll
-          for (int c = 0; c < NR; c += 16) {
-            float o[32];  // both pieces
-            tmem_ld16(tO + c, o);
-            tmem_ld16(tO + NR + c, o + 16);
-            tmem_wait_ld_all<32>(o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = c + i;
+            for (int i = 0; i < 8; ++i) {
+              const int r = r_base + c + i;
               if (r < p.nrows) {
-                const float x = fmaf(o[16 + i], 0.0625f, o[i]);
-                if (p.whole) {
-                  const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
-                  from_float(x * sm.fac[r], static_cast<__nv_bfloat16*>(a.out) + p.b * a.o_seq + t * a.o_tok +
-                                                (p.h * a.G + g) * a.o_head + tid);
-                } else {
-                  a.part_o[(static_cast<int64_t>(p.slot) * a.slot_rows + r) * D + tid] = x;
-                }
+                const float y = fmaf(o[8 + i], 0.0625f, o[i]);
+                if (p.whole)
+                  from_float(y * sm.fac[r], static_cast<__nv_bfloat16*>(a.out) + sm.out_at[r] + token);
+                else
+                  part[(c + i) * D] = y;
               }
             }
           }
@@ -620,7 +699,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_free(tm, C::kCols);
+  if (warp == 9) tmem_free(tm, C::kCols);
 }
 
 }  // namespace spec_kv_detail

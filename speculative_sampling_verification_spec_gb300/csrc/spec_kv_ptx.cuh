@@ -81,43 +81,46 @@ __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
 }
-// 16 consecutive columns of the thread's lane
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float* x) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(x);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
+// N consecutive columns of the thread's lane
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float* x);
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t addr, const float* x);
+template <int N>
+__device__ __forceinline__ void tmem_tie(float* x);
+template <>
+__device__ __forceinline__ void tmem_ld<8>(uint32_t addr, float* x) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+               : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const float* x) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-// waits for the thread's loads; the 16 values pass through, so that nothing that uses them moves ahead of the wait
-__device__ __forceinline__ void tmem_wait_ld(float* x) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]),
-                 "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15])
-               :
+template <>
+__device__ __forceinline__ void tmem_st<8>(uint32_t addr, const float* x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
                : "memory");
 }
-// the same for N values loaded 16 at a time, with one wait
-template <int N>
-__device__ __forceinline__ void tmem_wait_ld_all(float* x) {
-  tmem_wait_ld(x);
-#pragma unroll
-  for (int c = 16; c < N; c += 16)
-    asm volatile(""
-                 : "+f"(x[c]), "+f"(x[c + 1]), "+f"(x[c + 2]), "+f"(x[c + 3]), "+f"(x[c + 4]), "+f"(x[c + 5]),
-                   "+f"(x[c + 6]), "+f"(x[c + 7]), "+f"(x[c + 8]), "+f"(x[c + 9]), "+f"(x[c + 10]), "+f"(x[c + 11]),
-                   "+f"(x[c + 12]), "+f"(x[c + 13]), "+f"(x[c + 14]), "+f"(x[c + 15]));
+// nothing that uses these values moves ahead of the wait before it
+template <>
+__device__ __forceinline__ void tmem_tie<8>(float* x) {
+  asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]));
 }
+template <>
+__device__ __forceinline__ void tmem_ld<16>(uint32_t addr, float* x) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+               : "r"(addr));
+}
+template <>
+__device__ __forceinline__ void tmem_st<16>(uint32_t addr, const float* x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(x[8]), "f"(x[9]), "f"(x[10]), "f"(x[11]), "f"(x[12]), "f"(x[13]), "f"(x[14]), "f"(x[15])
+               : "memory");
+}
+// nothing that uses these values moves ahead of the wait before it
+template <>
+__device__ __forceinline__ void tmem_tie<16>(float* x) {
+  asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]), "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
