@@ -72,7 +72,7 @@ typedef struct {
   int64_t o_seq_stride, o_tok_stride, o_head_stride;   /* append: q_out; attention: out */
   void* stream;              /* cudaStream_t */
   int32_t* status;           /* optional device int32[1]: first device-detected error */
-  void* workspace;           /* attention: device, 256-byte aligned; needs no clearing */
+  void* workspace;           /* attention: device, 256-byte aligned, zero-filled before first use */
   size_t workspace_bytes;
 } spec_kv_params;
 
@@ -101,7 +101,11 @@ spec_status spec_kv_append(const void* q, const void* k, const void* v, const fl
                            const spec_kv_cache* cache, const spec_kv_params* params, void* q_out);
 
 /* Workspace bytes spec_kv_attention needs (0 if the parameters are invalid);
- * a function of B, T, Hq, Hkv, D and dtype alone. */
+ * a function of B, T, Hq, Hkv, D and dtype alone.  A workspace is zero-filled once
+ * before its first use.  Its first 64 KB hold counters that every call leaves at
+ * zero again, so it is reused across calls of any shape without clearing (but not
+ * with spec_verify's; and after a SPEC_ERR_TIMEOUT it is cleared).  Calls that
+ * share one must not overlap in time on the GPU. */
 size_t spec_kv_attention_workspace_size(const spec_kv_cache* cache, const spec_kv_params* params);
 
 /* Attention of the new tokens' queries over the cache.  The new tokens' keys and
@@ -119,7 +123,8 @@ size_t spec_kv_attention_workspace_size(const spec_kv_cache* cache, const spec_k
  * sees makes its output NaN (a value: in the affected channels at least).
  * Device errors: a sequence whose lengths are out of range gets NaN, and so does
  * a row that reads a page outside [0, num_pages); both store
- * SPEC_ERR_CACHE_RANGE in *status. */
+ * SPEC_ERR_CACHE_RANGE in *status.  A bounded wait that runs out (about two
+ * seconds) gives NaN and SPEC_ERR_TIMEOUT. */
 spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const spec_kv_params* params, void* out,
                               float* lse);
 

@@ -20,6 +20,9 @@ using namespace spec_kv_detail;
 constexpr int kSMs = 152;
 constexpr int kGenCtas = kSMs * 4;
 constexpr int kMmaCtas = kSMs * 2;
+// What an item costs beside its tiles, in tiles.
+constexpr int kGenOverhead = 1;
+constexpr int kMmaOverhead = 3;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -46,7 +49,7 @@ spec_status check_cache(const spec_kv_cache* c, const spec_kv_params* p) {
   const int64_t tiles = (static_cast<int64_t>(p->max_pages) * c->page_size + kTile - 1) / kTile;
   // positions, and tiles of the whole call, are counted in 32 bits
   if (static_cast<int64_t>(p->max_pages) * c->page_size > INT_MAX - kTile) return SPEC_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(std::max(1, p->B)) * c->Hkv > (int64_t(1) << 30) / tiles) return SPEC_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(std::max(1, p->B)) * c->Hkv > (int64_t(1) << 30) / (tiles + kMmaOverhead)) return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
 }
 
@@ -95,16 +98,17 @@ const void* append_fn(bool vec, bool warp) {
              : (warp ? append_ptr<E, 1, true>() : append_ptr<E, 1, false>());
 }
 
-template <typename E, bool CTA>
-const void* join_ptr() {
-  return reinterpret_cast<const void*>(&spec_kv_join_kernel<E, CTA>);
-}
-
 // How the attention's work is cut; a function of B, T, Hq, Hkv, D and the kernel.
 struct AttnPlan {
   int rows = 0, nrt = 0, nranges = 0, slot_rows = 0;
-  size_t off_ml = 0, off_o = 0, ws_bytes = 0;
+  bool join_here = false, clear = false;
+  size_t off_prefix = 0, off_ml = 0, off_o = 0, ws_bytes = 0;
 };
+
+// Parts of an item that one CTA joins, in bytes.
+constexpr int64_t kJoinBytes = 256 << 10;
+// Workspace bytes kept zero between calls: counters of the items' parts.
+constexpr size_t kPartCounters = 64 * 1024;
 
 AttnPlan plan_attention(const spec_kv_cache* c, const spec_kv_params* p, bool mma) {
   AttnPlan pl;
@@ -117,7 +121,15 @@ AttnPlan plan_attention(const spec_kv_cache* c, const spec_kv_params* p, bool mm
   pl.nranges = std::max(1, (mma ? kMmaCtas : kGenCtas) / pl.nrt);
   // with one range nothing is shared, so no partial results
   const size_t slots = pl.nranges > 1 ? static_cast<size_t>(2) * pl.nranges * pl.nrt : 0;
-  pl.off_ml = round_up((static_cast<size_t>(p->B) + 1) * sizeof(int32_t), 256);
+  // The last CTA of an item adds up its parts where that is little to read (the
+  // parts of one item, if all sequences are alike); else a kernel over all rows.
+  const int64_t items = static_cast<int64_t>(std::max(1, p->B)) * c->Hkv;
+  const int64_t parts = (pl.nranges + items - 1) / items;
+  pl.join_here = parts * pl.rows * c->D * 4 <= kJoinBytes;
+  const size_t counters = round_up(static_cast<size_t>(p->B) * c->Hkv * pl.nrt * sizeof(int32_t), 256);
+  pl.clear = pl.join_here && pl.nranges > 1 && counters > kPartCounters;
+  pl.off_prefix = std::max(kPartCounters, counters);
+  pl.off_ml = pl.off_prefix + round_up((static_cast<size_t>(p->B) + 1) * sizeof(int32_t), 256);
   pl.off_o = pl.off_ml + round_up(slots * pl.slot_rows * sizeof(float2), 256);
   pl.ws_bytes = pl.off_o + round_up(slots * pl.slot_rows * c->D * sizeof(float), 256);
   return pl;
@@ -332,38 +344,41 @@ spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const s
   a.rows = pl.rows;
   a.nrt = pl.nrt;
   a.nranges = pl.nranges;
+  a.overhead = mma ? kMmaOverhead : kGenOverhead;
+  a.join_here = pl.join_here;
   a.slot_rows = pl.slot_rows;
   a.q_vec = aligned(q, 16) && a.q_seq % 8 == 0 && a.q_tok % 8 == 0 && a.q_head % 8 == 0;
   const int64_t ob = 4 * (p->dtype == SPEC_F32 ? 4 : 2);  // bytes of four channels
   a.o_vec = aligned(out, static_cast<uintptr_t>(ob)) && a.o_seq % 4 == 0 && a.o_tok % 4 == 0 && a.o_head % 4 == 0;
   char* ws = static_cast<char*>(p->workspace);
-  a.prefix = reinterpret_cast<int32_t*>(ws);
+  a.arrived = reinterpret_cast<int32_t*>(ws);
+  a.prefix = reinterpret_cast<int32_t*>(ws + pl.off_prefix);
   a.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
   a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
   const bool f32 = p->dtype == SPEC_F32;
   cudaStream_t st = static_cast<cudaStream_t>(p->stream);
+  if (pl.clear && cudaMemsetAsync(ws, 0, pl.off_prefix, st) != cudaSuccess) return SPEC_ERR_CUDA;
   const int grid = pl.nranges * pl.nrt;
   s = mma ? launch_mma(a, cache, order, grid, st) : launch_general(a, f32, grid, st);
   if (s != SPEC_OK) return s;
-  void* args[] = {&a};
+  specv_units::count_launches(1);
+  if (pl.join_here || pl.nranges == 1) return SPEC_OK;
   // the join kernel is a programmatic dependent launch: it may be scheduled while
   // the last ranges finish, and waits before it reads or writes
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
-  // with few rows beside the ranges, a row can be cut into many parts: a CTA for each
-  const bool wide = rows <= 4 * kSMs * 16 && pl.nranges > 8 * static_cast<int64_t>(a.B) * a.Hkv;
-  cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.T * a.Hq));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const void* jn = f32 ? (wide ? join_ptr<float, true>() : join_ptr<float, false>())
-                       : (wide ? join_ptr<__nv_bfloat16, true>() : join_ptr<__nv_bfloat16, false>());
+  void* args[] = {&a};
+  const void* jn = f32 ? reinterpret_cast<const void*>(&spec_kv_join_kernel<float>)
+                       : reinterpret_cast<const void*>(&spec_kv_join_kernel<__nv_bfloat16>);
   if (cudaLaunchKernelExC(&cfg, jn, args) != cudaSuccess) return SPEC_ERR_CUDA;
-  specv_units::count_launches(2);
+  specv_units::count_launches(1);
   return SPEC_OK;
 }
 

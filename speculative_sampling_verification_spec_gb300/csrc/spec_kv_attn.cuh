@@ -19,6 +19,134 @@ __device__ __forceinline__ float ex2(float x) {
 // reference and sum -> natural logarithm of the sum of the weights
 __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.69314718055994531f; }
 
+template <typename E>
+__device__ __forceinline__ void store4(const KvArgs& a, E* o, float4 x) {
+  if constexpr (sizeof(E) == 4) {
+    if (a.o_vec) {
+      *reinterpret_cast<float4*>(o) = x;
+      return;
+    }
+  } else {
+    if (a.o_vec) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+      *reinterpret_cast<uint2*>(o) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      return;
+    }
+  }
+  from_float(x.x, o);
+  from_float(x.y, o + 1);
+  from_float(x.z, o + 2);
+  from_float(x.w, o + 3);
+}
+
+// Adds up the parts c0 .. c1 of one row, in order, `step` apart from `from`: lane
+// by lane four channels (and four more from 128 on).  `top` is the largest
+// reference of all parts.
+__device__ __forceinline__ void add_parts(const KvArgs& a, int rt, int r, int c0, int c1, int from, int step, float top,
+                                          float4* acc, float& l) {
+  const int lane = threadIdx.x & 31;
+  const auto slot_row = [&](int c) { return static_cast<int64_t>(part_slot(a, c, c0, rt)) * a.slot_rows + r; };
+  for (int cb = from; cb <= c1; cb += 32 * step) {
+    // weights of up to 32 parts, one a lane; a part without tokens for this row left no output
+    float wl = 0.0f, ll = 0.0f;
+    if (cb + lane * step <= c1) {
+      const float2 ml = __ldcg(&a.part_ml[slot_row(cb + lane * step)]);
+      ll = ml.y;
+      wl = exp2f(ml.x - top);
+    }
+    const int m = min(32, (c1 - cb) / step + 1);
+#pragma unroll 8
+    for (int i = 0; i < m; ++i) {
+      const float w = __shfl_sync(kFull, wl, i), li = __shfl_sync(kFull, ll, i);
+      const bool none = li == 0.0f;
+      const float* po = a.part_o + slot_row(cb + i * step) * a.D;
+      l = none ? l : fmaf(w, li, l);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int d = lane * 4 + k * 128;
+        if (d < a.D) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(po + d));
+          acc[k].x = none ? acc[k].x : fmaf(w, x.x, acc[k].x);
+          acc[k].y = none ? acc[k].y : fmaf(w, x.y, acc[k].y);
+          acc[k].z = none ? acc[k].z : fmaf(w, x.z, acc[k].z);
+          acc[k].w = none ? acc[k].w : fmaf(w, x.w, acc[k].w);
+        }
+      }
+    }
+  }
+}
+
+// The largest reference of a row's parts, in every lane.
+__device__ __forceinline__ float top_of_parts(const KvArgs& a, int rt, int r, int c0, int c1) {
+  float top = kNoRef;
+  for (int c = c0 + (threadIdx.x & 31); c <= c1; c += 32)
+    top = fmaxf(top, __ldcg(&a.part_ml[static_cast<int64_t>(part_slot(a, c, c0, rt)) * a.slot_rows + r]).x);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+  return top;
+}
+
+// A joined row's output and lse, by one warp.
+template <typename E>
+__device__ __forceinline__ void store_row(const KvArgs& a, int b, int t, int hq, const float4* acc, float top, float l) {
+  const int lane = threadIdx.x & 31;
+  E* o = static_cast<E*>(a.out) + b * a.o_seq + t * a.o_tok + hq * a.o_head;
+  const float inv = 1.0f / l;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int d = lane * 4 + k * 128;
+    if (d < a.D) store4(a, o + d, make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
+  }
+  if (lane == 0 && a.lse) a.lse[(static_cast<int64_t>(b) * a.T + t) * a.Hq + hq] = lse_of(top, l);
+}
+
+// Whether this CTA is the last of its item to leave its part (all parts can then
+// be read).  Called by one thread after the CTA's stores and a barrier.
+__device__ __forceinline__ bool last_of_item(const KvArgs& a, const Piece& p, int rt) {
+  int32_t* count = a.arrived + (static_cast<int64_t>(p.b) * a.Hkv + p.h) * a.nrt + rt;
+  __threadfence();
+  const bool last = atomicAdd(count, 1) == p.c1 - p.c0;
+  if (last) {
+    *count = 0;  // for the next call
+    __threadfence();
+  }
+  return last;
+}
+
+// Joins an item's rows, by `warps` warps: a row is a warp's.
+template <typename E>
+__device__ __forceinline__ void join_item(const KvArgs& a, const Piece& p, int rt, int warp, int warps) {
+  for (int r = warp; r < p.nrows; r += warps) {
+    const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
+    const float top = top_of_parts(a, rt, r, p.c0, p.c1);
+    float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+    float l = 0.0f;
+    add_parts(a, rt, r, p.c0, p.c1, p.c0, 1, top, acc, l);
+    store_row<E>(a, p.b, t, p.h * a.G + g, acc, top, l);
+  }
+}
+
+// Slots without a new token are zero, those of a sequence with bad lengths NaN;
+// (sequence, slot) pairs are spread over the grid's CTAs.
+template <typename E>
+__device__ __forceinline__ void fill_empty(const KvArgs& a, int tid, int threads) {
+  const int64_t pairs = static_cast<int64_t>(a.B) * a.T;
+  for (int64_t i = blockIdx.x; i < pairs; i += gridDim.x) {
+    const int b = static_cast<int>(i / a.T), t = static_cast<int>(i - static_cast<int64_t>(b) * a.T);
+    const SeqSpan s = seq_span(a, b);
+    if (!s.bad && t < s.n) continue;
+    const float x = s.bad ? __uint_as_float(0x7fc00000u) : 0.0f;
+    if (s.bad && tid == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+    const int quads = a.D / 4;
+    for (int e = tid; e < a.Hq * quads; e += threads) {
+      const int h = e / quads, d = (e - h * quads) * 4;
+      store4(a, static_cast<E*>(a.out) + b * a.o_seq + t * a.o_tok + h * a.o_head + d, make_float4(x, x, x, x));
+      if (d == 0 && a.lse) a.lse[i * a.Hq + h] = s.bad ? x : -INFINITY;
+    }
+  }
+}
+
 constexpr int kGenThreads = 128;
 constexpr int kGenRows = 8;    // rows of a row tile
 constexpr int kGenSub = 32;    // tokens staged at a time: a lane's token in the scores
@@ -40,6 +168,7 @@ __global__ void __launch_bounds__(kGenThreads) spec_kv_attention_kernel(const __
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int range = blockIdx.x / a.nrt, rt = blockIdx.x - range * a.nrt;
   make_plan_range<kGenThreads>(a, range, &plan, scratch, blockIdx.x == 0 ? a.prefix : nullptr);
+  fill_empty<E>(a, tid, kGenThreads);
   if (plan.w0 >= plan.w1) return;
   const int D = a.D, kst = D + 4, dv = D / 16;
   float* sq = reinterpret_cast<float*>(dyn);  // [kGenRows][D]
@@ -204,7 +333,7 @@ __global__ void __launch_bounds__(kGenThreads) spec_kv_attention_kernel(const __
 #pragma unroll
         for (int r = 0; r < kGenRows; ++r) {
           if (r >= p.nrows) continue;
-          if (p.whole) {
+          if (p.whole()) {
             const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
             from_float(acc[i][r] / sl[r], static_cast<E*>(a.out) + p.b * a.o_seq + t * a.o_tok + (p.h * a.G + g) * a.o_head + d);
           } else {
@@ -215,137 +344,63 @@ __global__ void __launch_bounds__(kGenThreads) spec_kv_attention_kernel(const __
     }
     if (tid < p.nrows) {
       const int gr = p.row0 + tid, t = gr / a.G, g = gr - t * a.G;
-      if (p.whole) {
+      if (p.whole()) {
         if (a.lse) a.lse[(static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g] = lse_of(sm[tid], sl[tid]);
       } else {
         a.part_ml[static_cast<int64_t>(p.slot) * a.slot_rows + tid] = make_float2(sm[tid], sl[tid]);
       }
     }
     __syncthreads();  // queries and statistics are rewritten by the next piece
+    if (a.join_here && !p.whole()) {
+      if (tid == 0) scratch[0] = last_of_item(a, p, rt);
+      __syncthreads();
+      if (scratch[0]) join_item<E>(a, p, rt, warp, kGenThreads / 32);
+    }
   }
 }
 
-// Rows (sequence, token, query head) shared by several ranges are added up in the
-// order of the ranges; rows with nothing to attend are zero, rows of a sequence
-// with bad lengths NaN; the others are written already.  A row is a warp's, or,
-// where rows are cut into many parts, a CTA's, whose warps take every fourth part
-// (the order of the sum is then fixed too).
+// The join kernel, for items of many rows and parts: a row (sequence, token, query
+// head) is a CTA's, whose warps take every fourth part (the order of the sum is
+// fixed too).
 constexpr int kJoinWarps = 4;
 
 template <typename E>
-__device__ __forceinline__ void store4(const KvArgs& a, E* o, float4 x) {
-  if constexpr (sizeof(E) == 4) {
-    if (a.o_vec) {
-      *reinterpret_cast<float4*>(o) = x;
-      return;
-    }
-  } else {
-    if (a.o_vec) {
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
-      *reinterpret_cast<uint2*>(o) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-      return;
-    }
-  }
-  from_float(x.x, o);
-  from_float(x.y, o + 1);
-  from_float(x.z, o + 2);
-  from_float(x.w, o + 3);
-}
-
-template <typename E, bool CTA>
 __global__ void __launch_bounds__(32 * kJoinWarps) spec_kv_join_kernel(const __grid_constant__ KvArgs a) {
-  __shared__ __align__(16) float4 part_o[CTA ? kJoinWarps : 1][64];
+  __shared__ __align__(16) float4 part_o[kJoinWarps][64];
   __shared__ float part_l[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
-  const int64_t mine = CTA ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
-  const int64_t row = mine < rows ? mine : rows - 1;
+  const int64_t row = blockIdx.x;
   const int hq = static_cast<int>(row % a.Hq);
   const int64_t bt = row / a.Hq;
   const int b = static_cast<int>(bt / a.T), t = static_cast<int>(bt - static_cast<int64_t>(b) * a.T);
-  const SeqSpan s = seq_span(a, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the ranges' results are complete
-  if (mine >= rows) return;
-  E* o = static_cast<E*>(a.out) + b * a.o_seq + t * a.o_tok + hq * a.o_head;
-  if (s.bad || t >= s.n) {
-    if (CTA && warp > 0) return;
-    const float x = s.bad ? __uint_as_float(0x7fc00000u) : 0.0f;
-    for (int d = lane * 4; d < a.D; d += 128) store4(a, o + d, make_float4(x, x, x, x));
-    if (lane == 0) {
-      if (a.lse) a.lse[row] = s.bad ? x : -INFINITY;
-      if (s.bad) report(a.status, SPEC_ERR_CACHE_RANGE);
-    }
-    return;
-  }
-  const int total = a.prefix[a.B];
-  const int per = max(1, (total + a.nranges - 1) / a.nranges);
+  const SeqSpan s = seq_span(a, b);
+  if (s.bad || t >= s.n) return;
+  const int per = max(1, (a.prefix[a.B] + a.nranges - 1) / a.nranges);
   const int h = hq / a.G, g = hq - h * a.G;
-  const int wb = a.prefix[b] + h * s.nt;
-  const int c0 = wb / per, c1 = (wb + s.nt - 1) / per;
+  const int first = a.prefix[b] + h * s.places + a.overhead;
+  const int c0 = first / per, c1 = (first + s.nt - 1) / per;
   if (c0 == c1) return;
   const int gr = t * a.G + g, rt = gr / a.rows, r = gr - rt * a.rows;
-  const auto slot_row = [&](int c) {
-    return static_cast<int64_t>(2 * (c * a.nrt + rt) + (c == c0 ? 1 : 0)) * a.slot_rows + r;
-  };
-  float top = kNoRef;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, a.part_ml[slot_row(c)].x);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+  const float top = top_of_parts(a, rt, r, c0, c1);
   float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
   float l = 0.0f;
-  constexpr int kStep = CTA ? kJoinWarps : 1;
-  for (int cb = c0 + (CTA ? warp : 0); cb <= c1; cb += 32 * kStep) {
-    // weights of up to 32 parts, one a lane; a part without tokens for this row left no output
-    float wl = 0.0f, ll = 0.0f;
-    if (cb + lane * kStep <= c1) {
-      const float2 ml = a.part_ml[slot_row(cb + lane * kStep)];
-      ll = ml.y;
-      wl = exp2f(ml.x - top);
-    }
-    const int m = min(32, (c1 - cb) / kStep + 1);
-#pragma unroll 8
-    for (int i = 0; i < m; ++i) {
-      const float w = __shfl_sync(kFull, wl, i), li = __shfl_sync(kFull, ll, i);
-      const bool none = li == 0.0f;
-      const float* po = a.part_o + slot_row(cb + i * kStep) * a.D;
-      l = none ? l : fmaf(w, li, l);
+  add_parts(a, rt, r, c0, c1, c0 + warp, kJoinWarps, top, acc, l);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int d = lane * 4 + k * 128;
-        if (d < a.D) {
-          const float4 x = *reinterpret_cast<const float4*>(po + d);
-          acc[k].x = none ? acc[k].x : fmaf(w, x.x, acc[k].x);
-          acc[k].y = none ? acc[k].y : fmaf(w, x.y, acc[k].y);
-          acc[k].z = none ? acc[k].z : fmaf(w, x.z, acc[k].z);
-          acc[k].w = none ? acc[k].w : fmaf(w, x.w, acc[k].w);
-        }
-      }
+  for (int k = 0; k < 2; ++k) part_o[warp][lane + 32 * k] = acc[k];
+  if (lane == 0) part_l[warp] = l;
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) {
+    l += part_l[w];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float4 x = part_o[w][lane + 32 * k];
+      acc[k] = make_float4(acc[k].x + x.x, acc[k].y + x.y, acc[k].z + x.z, acc[k].w + x.w);
     }
   }
-  if constexpr (CTA) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) part_o[warp][lane + 32 * k] = acc[k];
-    if (lane == 0) part_l[warp] = l;
-    __syncthreads();
-    if (warp > 0) return;
-#pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) {
-      l += part_l[w];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float4 x = part_o[w][lane + 32 * k];
-        acc[k] = make_float4(acc[k].x + x.x, acc[k].y + x.y, acc[k].z + x.z, acc[k].w + x.w);
-      }
-    }
-  }
-  const float inv = 1.0f / l;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int d = lane * 4 + k * 128;
-    if (d < a.D) store4(a, o + d, make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
-  }
-  if (lane == 0 && a.lse) a.lse[row] = lse_of(top, l);
+  store_row<E>(a, b, t, hq, acc, top, l);
 }
 
 }  // namespace spec_kv_detail

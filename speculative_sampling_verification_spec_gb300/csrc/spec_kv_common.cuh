@@ -4,12 +4,14 @@
 //
 // The attention's work is a list of tiles of kTile tokens: sequence after
 // sequence, within a sequence head after head, within a head in order of
-// position.  The list is cut into `nranges` equal ranges (from the lengths on
-// the device, so a batch of unequal sequences is spread evenly and no length
-// crosses to the host); a range is walked by one CTA for one row tile.  A (head,
-// row tile) that lies in one range is finished there; one that several ranges
-// share leaves a partial result (unnormalised output, reference, sum) per range
-// in the workspace, and the join kernel adds them in order.
+// position.  Before each head's tiles come `overhead` places without one, for what
+// it costs to take up a head.  The list is cut into `nranges` equal ranges (from
+// the lengths on the device, so a batch of unequal sequences is spread evenly and
+// no length crosses to the host); a range is walked by one CTA for one row tile.
+// An item (sequence, head, row tile) that lies in one range is finished there; one
+// that several ranges share leaves a partial result (unnormalised output,
+// reference, sum) per range in the workspace.  They are added up in the order of
+// the ranges, by the CTA that arrives last or by the join kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -49,10 +51,13 @@ struct KvArgs {
   int32_t rows;       // rows of a row tile (row = t * G + head in group)
   int32_t nrt;        // row tiles of a sequence
   int32_t nranges;    // ranges of the tile list
+  int32_t overhead;   // places of the list before a head's tiles
+  int32_t join_here;  // the last CTA of an item joins it, else the join kernel
   int32_t q_vec;      // queries may be loaded 16 bytes at a time
   int32_t o_vec;      // outputs may be stored four channels at a time
   int32_t slot_rows;  // rows a partial slot has room for
-  int32_t* prefix;    // workspace: [B + 1] tiles before each sequence
+  int32_t* arrived;   // workspace: [B][Hkv][nrt] ranges that have left their part; zero between calls
+  int32_t* prefix;    // workspace: [B + 1] places of the list before each sequence
   float* part_o;      // workspace: [slots][slot_rows][D]
   float2* part_ml;    // workspace: [slots][slot_rows] (reference, sum)
 };
@@ -76,6 +81,7 @@ __device__ __forceinline__ float2 codes2_to_float2(uint16_t c) {
 // L + n).  No tiles when it has no new token or its lengths are out of range.
 struct SeqSpan {
   int L, n, t0, nt;
+  int places;  // a head's in the list
   bool bad;
 };
 __device__ __forceinline__ SeqSpan seq_span(const KvArgs& a, int b) {
@@ -86,29 +92,31 @@ __device__ __forceinline__ SeqSpan seq_span(const KvArgs& a, int b) {
   s.bad = s.L < 0 || s.n < 0 || s.n > a.T || static_cast<int64_t>(s.L) + s.n > cap;
   s.t0 = 0;
   s.nt = 0;
+  s.places = 0;
   if (!s.bad && s.n > 0) {
     const int first = (a.window > 0 && s.L + 1 > a.window) ? s.L + 1 - a.window : 0;
     s.t0 = first / kTile;
     s.nt = (s.L + s.n + kTile - 1) / kTile - s.t0;
+    s.places = s.nt + a.overhead;
   }
   return s;
 }
 
-// A CTA's view of the tile list: the range [w0, w1), and where w0 lies.
+// A CTA's view of the list: the range [w0, w1), and where w0 lies.
 struct RangePlan {
   int per, w0, w1;
-  int b, off;  // sequence that holds w0, and w0's offset in its tiles (all heads)
+  int b, off;  // sequence that holds w0, and w0's offset in its places (all heads)
 };
 
 // All threads of the CTA (NT of them) take part; `plan` and `scratch` are in
-// shared memory.  When prefix is given, it gets the tiles before each sequence.
+// shared memory.  When prefix is given, it gets the places before each sequence.
 template <int NT>
 __device__ void make_plan_range(const KvArgs& a, int range, RangePlan* plan, int* scratch, int32_t* prefix) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = (a.B + NT - 1) / NT;
   const int b0 = min(a.B, tid * c), b1 = min(a.B, b0 + c);
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_span(a, b).nt * a.Hkv;
+  for (int b = b0; b < b1; ++b) mine += seq_span(a, b).places * a.Hkv;
   int inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -137,7 +145,7 @@ __device__ void make_plan_range(const KvArgs& a, int range, RangePlan* plan, int
   if (w0 < w1 && before <= w0 && w0 < before + mine) {
     int at = before;
     for (int b = b0; b < b1; ++b) {
-      const int k = seq_span(a, b).nt * a.Hkv;
+      const int k = seq_span(a, b).places * a.Hkv;
       if (w0 < at + k) {
         plan->b = b;
         plan->off = w0 - at;
@@ -150,7 +158,7 @@ __device__ void make_plan_range(const KvArgs& a, int range, RangePlan* plan, int
     int at = before;
     for (int b = b0; b < b1; ++b) {
       prefix[b] = at;
-      at += seq_span(a, b).nt * a.Hkv;
+      at += seq_span(a, b).places * a.Hkv;
     }
   }
   __syncthreads();
@@ -163,19 +171,19 @@ struct Piece {
   int L, n;          // tokens before the new ones; new tokens
   int row0, nrows;   // rows of this row tile
   int tile0, tile1;  // absolute tiles [tile0, tile1); may be empty
-  bool whole;        // the item lies in this range alone
-  int slot;          // else: where its partial result goes
+  int c0, c1;        // first and last range that hold tiles of the item
+  int slot;          // where a partial result goes, when these differ
+  __device__ bool whole() const { return c0 == c1; }
 };
 
 struct Walk {
-  int w, w1, b, off;  // next tile of the list; sequence and offset in it
-  int per, w0, range, rt;
+  int w, w1, b, off;  // next place of the list; sequence and offset in it
+  int per, range, rt;
 };
 
 __device__ __forceinline__ Walk walk_begin(const RangePlan& p, int range, int rt) {
   Walk k;
   k.w = p.w0;
-  k.w0 = p.w0;
   k.w1 = p.w1;
   k.b = p.b;
   k.off = p.off;
@@ -185,21 +193,28 @@ __device__ __forceinline__ Walk walk_begin(const RangePlan& p, int range, int rt
   return k;
 }
 
+// The slot of range c's part of an item that begins in range c0: a range holds at
+// most one item that began before it and one that goes on after it.
+__device__ __forceinline__ int part_slot(const KvArgs& a, int c, int c0, int rt) {
+  return 2 * (c * a.nrt + rt) + (c == c0 ? 1 : 0);
+}
+
 // The next piece that has rows; false at the range's end.
 __device__ __forceinline__ bool walk_next(const KvArgs& a, Walk& k, Piece& p) {
   while (k.w < k.w1) {
     const SeqSpan s = seq_span(a, k.b);
-    const int all = s.nt * a.Hkv;
-    if (k.off >= all) {  // on to the next sequence
+    if (k.off >= s.places * a.Hkv) {  // on to the next sequence
       ++k.b;
       k.off = 0;
       continue;
     }
-    const int h = k.off / s.nt, t = k.off - h * s.nt;
-    const int take = min(s.nt - t, k.w1 - k.w);
-    const int wb = k.w - t;  // list index of the item's first tile
-    p.whole = wb / k.per == (wb + s.nt - 1) / k.per;
-    p.slot = 2 * (k.range * a.nrt + k.rt) + (wb >= k.w0 ? 1 : 0);
+    const int h = k.off / s.places, at = k.off - h * s.places;
+    const int take = min(s.places - at, k.w1 - k.w);
+    const int first = k.w - at + a.overhead;  // place of the item's first tile
+    const int t0 = max(at - a.overhead, 0), t1 = at + take - a.overhead;
+    p.c0 = first / k.per;
+    p.c1 = (first + s.nt - 1) / k.per;
+    p.slot = part_slot(a, k.range, p.c0, k.rt);
     k.w += take;
     k.off += take;
     p.b = k.b;
@@ -208,13 +223,13 @@ __device__ __forceinline__ bool walk_next(const KvArgs& a, Walk& k, Piece& p) {
     p.n = s.n;
     p.row0 = k.rt * a.rows;
     p.nrows = min(a.rows, s.n * a.G - p.row0);
-    if (p.nrows <= 0) continue;
+    if (p.nrows <= 0 || t1 <= 0) continue;
     // tiles that some row of this row tile sees
     const int t_first = p.row0 / a.G, t_last = (p.row0 + p.nrows - 1) / a.G;
     const int hi = (s.L + t_last) / kTile + 1;
-    const int first = (a.window > 0 && s.L + t_first + 1 > a.window) ? s.L + t_first + 1 - a.window : 0;
-    p.tile0 = max(s.t0 + t, first / kTile);
-    p.tile1 = min(s.t0 + t + take, hi);
+    const int lo = (a.window > 0 && s.L + t_first + 1 > a.window) ? s.L + t_first + 1 - a.window : 0;
+    p.tile0 = max(s.t0 + t0, lo / kTile);
+    p.tile1 = min(s.t0 + t1, hi);
     if (p.tile1 < p.tile0) p.tile1 = p.tile0;
     return true;
   }

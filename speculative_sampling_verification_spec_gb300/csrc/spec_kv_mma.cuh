@@ -77,7 +77,7 @@ struct MmaSmall {
   RangePlan plan;
   int scratch[kMmaThreads / 32];
   uint32_t tmem;
-  int gave_up;
+  int gave_up, last;
 };
 
 template <int D, int NR>
@@ -661,14 +661,14 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           const float ref = m > 0 ? -reinterpret_cast<const float*>(&sm.rowtab[tid >> 1])[2 + (tid & 1)] : kNoRef;
           float s = sm.red[0][tid] + sm.red[1][tid] + sm.red[2][tid] + sm.red[3][tid];
           if (fail) s = __uint_as_float(0x7fc00000u);
-          if (p.whole) {
+          if (p.whole()) {
             if (a.lse) a.lse[sm.lse_at[tid]] = lse_of(ref, s);
             sm.fac[tid] = 1.0f / s;
           } else {
             a.part_ml[static_cast<int64_t>(p.slot) * a.slot_rows + tid] = make_float2(ref, s);
           }
         }
-        if (p.whole) soft_sync();
+        if (p.whole()) soft_sync();
         if (m > 0 && (warp & 3) * 32 < D) {
           float* part = a.part_o + (static_cast<int64_t>(p.slot) * a.slot_rows + r_base) * D + token;
 #pragma unroll 1
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
               const int r = r_base + c + i;
               if (r < p.nrows) {
                 const float y = fmaf(o[8 + i], 0.0625f, o[i]);
-                if (p.whole)
+                if (p.whole())
                   from_float(y * sm.fac[r], static_cast<__nv_bfloat16*>(a.out) + sm.out_at[r] + token);
                 else
                   part[(c + i) * D] = y;
@@ -692,10 +692,17 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           }
         }
         tc_fence_before();
+        if (a.join_here && !p.whole()) {
+          soft_sync();  // the part is written
+          if (tid == 0) sm.last = last_of_item(a, p, rt);
+          soft_sync();
+          if (sm.last) join_item<__nv_bfloat16>(a, p, rt, warp, kSoftThreads / 32);
+        }
       }
       if (fail && tid == 0) report(a.status, SPEC_ERR_TIMEOUT);
     }
   }
+  fill_empty<__nv_bfloat16>(a, tid, kMmaThreads);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

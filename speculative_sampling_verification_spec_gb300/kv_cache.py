@@ -103,7 +103,7 @@ def _workspace(nbytes, device, stream):
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(stream):
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)  # counters that calls leave at zero
         _ws_cache[key] = ws
     return ws
 
@@ -190,7 +190,7 @@ def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=No
     new tokens.  scale: factor of the scores (1 / sqrt(D)); window > 0: a query sees that many tokens, its own
     included.  Returns out [B, T, Hq, D] (zero in slots past new_lens), or (out, lse) with lse [B, T, Hq] float32, the
     natural logarithm of the sum of the weights, when return_lse or lse is given.  ws: a workspace of
-    spec_kv_attention_workspace_size bytes (uint8, CUDA); by default one is kept for each stream."""
+    spec_kv_attention_workspace_size bytes (uint8, CUDA, zeroed once); by default one is kept for each stream."""
     if not q.is_cuda:
         raise ValueError("spec_* calls take CUDA tensors (copy host data to the GPU first)")
     dtype = _DTYPES.get(q.dtype)

@@ -568,9 +568,12 @@ def test_attention_strides_streams_and_workspaces(dtype):
         assert got[0] is out and got[1] is lse
         assert_attention(out, lse, want)
     n = sv.spec_kv_attention_workspace_size(cache, 3, 5, 8, DT[dtype])
-    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")      # needs no clearing
-    out, lse = sv.spec_kv_attention(q, cache, *s.idx(), scale=0.05, return_lse=True, ws=ws)
-    assert_attention(out, lse, want)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:65536] = 0      # the counters: calls leave them at zero, the rest needs no clearing
+    for _ in range(2):
+        out, lse = sv.spec_kv_attention(q, cache, *s.idx(), scale=0.05, return_lse=True, ws=ws)
+        assert_attention(out, lse, want)
+        assert not ws[:65536].any()
     with pytest.raises(sv.SpecError):
         sv.spec_kv_attention(q, cache, *s.idx(), ws=ws[:n - 256])
     # another stream than the current one, with the queries made there
@@ -582,6 +585,39 @@ def test_attention_strides_streams_and_workspaces(dtype):
     out2, lse2 = sv.spec_kv_attention(q2, cache, *idx, scale=0.05, return_lse=True, stream=side)
     side.synchronize()
     assert torch.equal(out2, out) and torch.equal(lse2, lse)
+
+
+@gpu
+def test_one_workspace_for_calls_of_many_shapes():
+    """Shapes whose items are joined by their last CTA, by a kernel of its own, or not at all, in turn on one workspace;
+    and more items than the workspace has standing counters for."""
+    import speculative_sampling_verification_spec_gb300 as sv
+    shapes = [(1, 1, 4, 1, [3000], "bf16"), (2, 40, 8, 2, [2000, 77], "bf16"), (1, 5, 8, 2, [5000], "f32"),
+              (1, 20, 4, 1, [4000], "f32"), (3, 3, 4, 4, [10, 500, 0], "bf16"), (1, 1, 4, 1, [3000], "bf16")]
+    runs = []
+    for i, (B, T, Hq, Hkv, seq, dtype) in enumerate(shapes):
+        s = Setup(60 + i, B, T, Hq, Hkv, 64, 16, seq, [T] * B, dtype)
+        cache = s.cache()
+        s.append(cache)
+        s.ref_append()
+        runs.append((s, cache, s.dev(s.q), s.idx(), s.ref_attention()))
+    ws = torch.zeros(max(sv.spec_kv_attention_workspace_size(c, s.B, s.T, s.Hq, DT[s.dtype]) for s, c, *_ in runs),
+                     dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for s, cache, q, idx, want in runs:
+            out, lse = sv.spec_kv_attention(q, cache, *idx, return_lse=True, ws=ws)
+            assert_attention(out, lse, want)
+    # 4500 sequences x 4 heads: a few long ones are shared by ranges
+    B = 4500
+    seq = np.where(np.arange(B) % 900 == 0, 3000, np.arange(B) % 7)
+    s = Setup(70, B, 1, 4, 4, 64, 16, seq, [1] * B, "bf16")
+    cache = s.cache()
+    s.append(cache)
+    s.ref_append()
+    want = s.ref_attention()
+    for _ in range(2):
+        out, lse = sv.spec_kv_attention(s.dev(s.q), cache, *s.idx(), return_lse=True)
+        assert_attention(out, lse, want)
 
 
 @gpu
