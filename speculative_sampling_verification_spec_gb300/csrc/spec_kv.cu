@@ -288,16 +288,26 @@ spec_status spec_kv_append(const void* q, const void* k, const void* v, const fl
                    (!q || (vec_ok(q, a.q_seq, a.q_tok, a.q_head) && vec_ok(q_out, a.o_seq, a.o_tok, a.o_head)));
   const int per_tok = cache->D / (vec ? 16 : 2);
   g.units_page = (p->T - 1 + S - 1) / S + 1;
-  const int64_t units = static_cast<int64_t>(p->B) * g.units_page * cache->Hkv * 2;
-  if (units > INT_MAX) return SPEC_ERR_UNSUPPORTED;
-  g.units = static_cast<int>(units);
   // a unit fits a warp's registers or takes a CTA
-  const bool warp = std::min(p->T, S) * per_tok <= 32 * kAppendIter;
+  const bool warp = per_tok <= 32 && std::min(p->T, S) <= 32 / per_tok * kAppendWarpIter;
   const int threads = warp ? kAppendWarpThreads : kAppendCtaThreads;
-  g.unit_blocks = warp ? (g.units + kAppendWarpThreads / 32 - 1) / (kAppendWarpThreads / 32) : g.units;
-  const int per_row = p->Hq * per_tok;
-  g.q_rows_block = std::max(1, 2 * threads / per_row);
+  // groups of units, as large as leaves several for every warp or CTA that can be resident
+  const int64_t pages = static_cast<int64_t>(p->B) * g.units_page;
+  const int64_t slots = warp ? kSMs * 4 * (2048 / 32) : kSMs * kAppendCtas * 4;
+  g.group_units = 1;
+  while (g.group_units < 2 * cache->Hkv && pages * 2 * cache->Hkv / (2 * g.group_units) >= slots) g.group_units *= 2;
+  g.group_units = std::min(g.group_units, 2 * cache->Hkv);
+  g.groups_page = (2 * cache->Hkv + g.group_units - 1) / g.group_units;
+  if (pages * g.groups_page > INT_MAX) return SPEC_ERR_UNSUPPORTED;
+  g.groups = static_cast<int>(pages * g.groups_page);
+  constexpr int kWarps = kAppendWarpThreads / 32;
+  g.unit_blocks = warp ? (g.groups + kWarps - 1) / kWarps : g.groups;
+  // a query thread takes several heads and rows where that leaves enough threads for all SMs
   const int64_t rows = static_cast<int64_t>(p->B) * p->T;
+  g.q_heads = p->Hq % kAppendHeads == 0 && rows * p->Hq * per_tok >= int64_t(4) * kAppendHeads * kSMs * 2048 ? kAppendHeads : 1;
+  const int64_t beside = std::max(1, threads / (p->Hq / g.q_heads * per_tok));
+  g.q_rows_block = static_cast<int>(
+      beside * std::max<int64_t>(1, std::min<int64_t>(kAppendQueryRows, rows / (beside * kSMs * 2048 / threads))));
   const int64_t q_blocks = q ? (rows + g.q_rows_block - 1) / g.q_rows_block : 0;
   if (g.unit_blocks + q_blocks > INT_MAX) return SPEC_ERR_UNSUPPORTED;
   const void* fn = p->dtype == SPEC_F32 ? append_fn<float>(vec, warp) : append_fn<__nv_bfloat16>(vec, warp);

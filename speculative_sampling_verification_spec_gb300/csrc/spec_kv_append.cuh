@@ -4,10 +4,13 @@
 //
 // A unit is what one call writes to one (page, key/value head) of the keys or of
 // the values: at most page_size tokens.  Its scale depends on all of them (the
-// largest magnitude), so a unit is read, rotated and kept in registers, reduced,
-// and only then written as codes: one pass over the inputs.  A unit with few
-// elements is a warp's, a larger one a CTA's.  The queries need no reduction and
-// go to CTAs of their own at the end of the grid.
+// largest magnitude), so a unit is read, kept in registers, reduced,
+// and only then written as codes: one pass over the inputs.  What is kept is the
+// input as it came (half the registers in bfloat16, so twice as much is under
+// way); keys are rotated once for the largest magnitude and again for the codes.  A unit with few
+// elements is a warp's, a larger one a CTA's; where there are many, a warp or CTA
+// takes several of one page.  The queries need no reduction and go to CTAs of
+// their own at the end of the grid.
 //
 // A thread handles chunks of PC rotation pairs, 2 * PC channels: PC = 8 moves 16
 // bytes at a time and more where everything is aligned, PC = 1 single channels.
@@ -23,33 +26,52 @@ struct AppendArgs {
   int64_t k_seq, k_tok, k_head, v_seq, v_tok, v_head;
   int32_t rot, rot_len, interleaved;
   int32_t units_page;    // pages a sequence can touch in this call
-  int32_t unit_blocks;   // blocks that take units; the rest take queries
-  int32_t units;         // B * units_page * Hkv * 2
+  int32_t group_units;   // units of a group: a warp's or a CTA's
+  int32_t groups_page;   // groups of a page's 2 * Hkv units
+  int32_t groups;        // B * units_page * groups_page
+  int32_t unit_blocks;   // blocks that take groups; the rest take queries
   int32_t q_rows_block;  // (sequence, token) rows a query block takes
+  int32_t q_heads;       // heads a query thread takes: 1 or kAppendHeads
 };
 
+// N consecutive elements as they are in memory: 8 of them in 16-byte words, or one
 template <typename E, int N>
-__device__ __forceinline__ void load_n(const E* p, float* x) {
-  if constexpr (N == 1) {
-    x[0] = to_float(*p);
-  } else if constexpr (sizeof(E) == 2) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+struct Raw {
+  uint4 w[sizeof(E) * N / 16 > 0 ? sizeof(E) * N / 16 : 1];
+  __device__ __forceinline__ void load(const E* p) {
+    if constexpr (N == 1) {
+      w[0].x = __float_as_uint(to_float(*p));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const float4 r = reinterpret_cast<const float4*>(p)[i];
-      x[4 * i] = r.x;
-      x[4 * i + 1] = r.y;
-      x[4 * i + 2] = r.z;
-      x[4 * i + 3] = r.w;
+      for (int i = 0; i < static_cast<int>(sizeof(E) * N / 16); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
     }
   }
+  __device__ __forceinline__ void values(float* x) const {
+    if constexpr (N == 1) {
+      x[0] = __uint_as_float(w[0].x);
+    } else if constexpr (sizeof(E) == 2) {
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        x[4 * i] = __uint_as_float(w[i].x);
+        x[4 * i + 1] = __uint_as_float(w[i].y);
+        x[4 * i + 2] = __uint_as_float(w[i].z);
+        x[4 * i + 3] = __uint_as_float(w[i].w);
+      }
+    }
+  }
+};
+template <typename E, int N>
+__device__ __forceinline__ void load_n(const E* p, float* x) {
+  Raw<E, N> r;
+  r.load(p);
+  r.values(x);
 }
 
 template <typename E, int N>
@@ -93,31 +115,53 @@ __device__ __forceinline__ ChunkAt chunk_at(const AppendArgs& g, int c) {
   return k;
 }
 
-// The values of a chunk in the order lo.., hi.., rotated where `turn`.  Products
-// and sums are rounded one by one, so the result does not depend on contraction.
+// (x1, x2) rotated by an angle; products and sums are rounded one by one, so the
+// result does not depend on contraction.
+__device__ __forceinline__ void turn(float& x1, float& x2, float co, float si) {
+  const float a = __fsub_rn(__fmul_rn(x1, co), __fmul_rn(x2, si));
+  const float b = __fadd_rn(__fmul_rn(x2, co), __fmul_rn(x1, si));
+  x1 = a;
+  x2 = b;
+}
+
+// A chunk as it is in memory, and its values in the order lo.., hi..
 template <typename E, int PC>
-__device__ __forceinline__ void load_chunk(const AppendArgs& g, const E* row, const float* cs, const ChunkAt& k,
-                                           float* y) {
-  load_n<E, PC>(row + k.lo, y);
-  load_n<E, PC>(row + k.hi, y + PC);
-  if (!cs || !k.turn) return;
+struct RawChunk {
+  Raw<E, PC> lo, hi;
+  __device__ __forceinline__ void load(const E* row, const ChunkAt& k) {
+    lo.load(row + k.lo);
+    hi.load(row + k.hi);
+  }
+  __device__ __forceinline__ void values(float* y) const {
+    lo.values(y);
+    hi.values(y + PC);
+  }
+};
+// The cosines and sines of a chunk's pairs, from the position's row of them, and
+// the rotation of a chunk.
+template <int PC>
+struct Angles {
   float co[PC], si[PC];
-  load_n<float, PC>(cs + k.angle, co);
-  load_n<float, PC>(cs + (g.rot >> 1) + k.angle, si);
-#pragma unroll
-  for (int i = 0; i < PC; ++i) {
-    // both forms are spelled out, so that the indices are constants
-    const float x1 = g.interleaved ? y[2 * i] : y[i], x2 = g.interleaved ? y[2 * i + 1] : y[PC + i];
-    const float a = __fsub_rn(__fmul_rn(x1, co[i]), __fmul_rn(x2, si[i]));
-    const float b = __fadd_rn(__fmul_rn(x2, co[i]), __fmul_rn(x1, si[i]));
+  __device__ __forceinline__ Angles(const AppendArgs& g, const float* cs, const ChunkAt& k) {
+    if (!k.turn) return;
+    load_n<float, PC>(cs + k.angle, co);
+    load_n<float, PC>(cs + (g.rot >> 1) + k.angle, si);
+  }
+  __device__ __forceinline__ void turn_all(const AppendArgs& g, const ChunkAt& k, float* y) const {
+    if (!k.turn) return;
     if (g.interleaved) {
-      y[2 * i] = a;
-      y[2 * i + 1] = b;
+#pragma unroll
+      for (int i = 0; i < PC; ++i) turn(y[2 * i], y[2 * i + 1], co[i], si[i]);
     } else {
-      y[i] = a;
-      y[PC + i] = b;
+#pragma unroll
+      for (int i = 0; i < PC; ++i) turn(y[i], y[PC + i], co[i], si[i]);
     }
   }
+};
+template <int PC>
+__device__ __forceinline__ void turn_chunk(const AppendArgs& g, const float* cs, const ChunkAt& k, float* y) {
+  const Angles<PC> at(g, cs, k);
+  at.turn_all(g, k, y);
 }
 
 __device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
@@ -142,22 +186,31 @@ struct Divider {
   __device__ __forceinline__ float operator()(float x) const { return exact ? x * inv : __fdiv_rn(x, scale); }
 };
 
-// two floats -> two e4m3 codes (low byte first); infinities become NaN codes
+// two floats -> two e4m3 codes (low byte first)
 __device__ __forceinline__ uint32_t to_codes2(float x, float y) {
-  if (!is_finite(x)) x = __uint_as_float(0x7fc00000u);
-  if (!is_finite(y)) y = __uint_as_float(0x7fc00000u);
   return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
+// infinities have no code (the conversion would take the largest one): NaN
+__device__ __forceinline__ float no_infinity(float x) { return is_finite(x) ? x : __uint_as_float(0x7fc00000u); }
 
+// N values of a chunk's half as codes: `plain`, all are finite and the scale is a power of two
 template <int N>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float* x, const Divider& d) {
+__device__ __forceinline__ void store_codes(uint8_t* p, const float* x, const Divider& d, bool plain) {
   if constexpr (N == 1) {
-    *p = static_cast<uint8_t>(to_codes2(d(x[0]), 0.0f) & 0xffu);
+    *p = static_cast<uint8_t>(to_codes2(no_infinity(d(x[0])), 0.0f) & 0xffu);
   } else {
     uint32_t w[2];
+    if (plain) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      w[i] = to_codes2(d(x[4 * i]), d(x[4 * i + 1])) | (to_codes2(d(x[4 * i + 2]), d(x[4 * i + 3])) << 16);
+      for (int i = 0; i < 2; ++i)
+        w[i] = to_codes2(x[4 * i] * d.inv, x[4 * i + 1] * d.inv) |
+               (to_codes2(x[4 * i + 2] * d.inv, x[4 * i + 3] * d.inv) << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        w[i] = to_codes2(no_infinity(d(x[4 * i])), no_infinity(d(x[4 * i + 1]))) |
+               (to_codes2(no_infinity(d(x[4 * i + 2])), no_infinity(d(x[4 * i + 3]))) << 16);
+    }
     *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   }
 }
@@ -172,17 +225,26 @@ __device__ __forceinline__ bool append_span(const AppendArgs& g, int b, int* L, 
   return !(*L < 0 || *n < 0 || *n > a.T || end > cap || (g.rot > 0 && *n > 0 && end > g.rot_len));
 }
 
-// ITER chunks a thread are kept in registers; a unit with more is read twice.
-constexpr int kAppendIter = 4;
+// Threads of a CTA, and chunks a thread keeps in registers (a unit with more is
+// read twice): units of a warp, four a CTA; units of a CTA.
+constexpr int kAppendWarpThreads = 128, kAppendWarpIter = 4;
+constexpr int kAppendCtaThreads = 256, kAppendCtas = 3;  // CTAs an SM
+template <typename E>
+constexpr int kAppendCtaIter = sizeof(E) == 2 ? 4 : 2;
+// Heads a query thread turns by one load of a position's angles, where the call is
+// large; chunks it has under way at once, and rows it takes in all.
+constexpr int kAppendHeads = 4, kAppendQueryRows = 16;
 
+// A group of units: `units` consecutive (head, keys or values) of one page of a
+// sequence, by a warp or a CTA.  What they share is worked out once.
 template <typename E, int PC, bool WARP>
-__device__ __forceinline__ void append_unit(const AppendArgs& g, int unit, int t, int nt, float* red) {
+__device__ __forceinline__ void append_group(const AppendArgs& g, int group, int t, uint32_t* red) {
+  constexpr int nt = WARP ? 32 : kAppendCtaThreads;
+  constexpr int ITER = WARP ? kAppendWarpIter : kAppendCtaIter<E>;
   const KvArgs& a = g.a;
-  const int kv = unit & 1;
-  int u = unit >> 1;
-  const int h = u % a.Hkv;
-  u /= a.Hkv;
-  const int pg = u % g.units_page, b = u / g.units_page;
+  const int of_page = group / g.groups_page;  // (sequence, page)
+  const int first = (group - of_page * g.groups_page) * g.group_units;
+  const int b = of_page / g.units_page, pg = of_page - b * g.units_page;
   int L, n;
   if (!append_span(g, b, &L, &n)) {
     if (t == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
@@ -193,129 +255,222 @@ __device__ __forceinline__ void append_unit(const AppendArgs& g, int unit, int t
   const int p0 = max(L, pi << a.log_page), p1 = min(L + n, (pi + 1) << a.log_page);
   if (p0 >= p1) return;
   const int page = page_of(a, b, pi);
-  if (page < 0) {
-    if (t == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
-    return;
-  }
-  const E* x = static_cast<const E*>(kv ? g.v : g.k) + b * (kv ? g.v_seq : g.k_seq) + h * (kv ? g.v_head : g.k_head);
-  const int64_t x_tok = kv ? g.v_tok : g.k_tok;
-  uint8_t* codes = (kv ? a.v_codes : a.k_codes) + page * a.page_stride + h * a.head_stride;
-  float* sp = (kv ? a.v_scale : a.k_scale) + page * a.scale_page_stride + h * a.scale_head_stride;
+  // a thread has one chunk of a token and every `step`th token, so that its chunk's
+  // place is worked out once (threads past the last whole token have nothing)
+  const int per_tok = a.D / (2 * PC), tokens = p1 - p0;
+  const int step = nt / per_tok, tok0 = t / per_tok;
+  const ChunkAt at = chunk_at<PC>(g, t - tok0 * per_tok);
+  const int mine = tok0 < step ? (tokens - tok0 + step - 1) / step : 0;  // this thread's tokens
+  const bool hold = tokens <= ITER * step;
   const int kept = p0 & (S - 1);  // earlier tokens of the sequence in this page
-  const float before = kept ? *sp : 0.0f;
-  const int per_tok = a.D / (2 * PC), total = (p1 - p0) * per_tok;
-  const bool turn = !kv && g.rot > 0;
-  const bool hold = total <= kAppendIter * nt;
-  float y[kAppendIter][2 * PC];
-  float amax = 0.0f;
-  for (int base = 0; base < total; base += kAppendIter * nt) {
+  const int cs_step = step * g.rot;
+  const float* const cs = g.cos_sin + (g.rot > 0 ? static_cast<int64_t>(p0 + tok0) * g.rot : 0);
+  const int64_t token = p0 - L + tok0;
+  const int last = min(first + g.group_units, 2 * a.Hkv);
+  for (int unit = first; unit < last; ++unit) {
+    const int kv = unit & 1, h = unit >> 1;
+    const int64_t x_tok = kv ? g.v_tok : g.k_tok, x_step = step * x_tok;
+    const E* const x = static_cast<const E*>(kv ? g.v : g.k) + b * (kv ? g.v_seq : g.k_seq) +
+                       h * (kv ? g.v_head : g.k_head) + token * x_tok;
+    const bool turned = !kv && g.rot > 0;
+    RawChunk<E, PC> raw[ITER];
+    const auto read = [&](int i0) {
 #pragma unroll
-    for (int it = 0; it < kAppendIter; ++it) {
-      const int i = base + it * nt + t;
-      if (i < total) {
-        const int tok = i / per_tok, c = i - tok * per_tok;
-        const ChunkAt at = chunk_at<PC>(g, c);
-        load_chunk<E, PC>(g, x + (p0 - L + tok) * x_tok, turn ? g.cos_sin + static_cast<int64_t>(p0 + tok) * g.rot : nullptr,
-                          at, y[it]);
+      for (int it = 0; it < ITER; ++it)
+        if (i0 + it < mine) raw[it].load(x + (i0 + it) * x_step, at);
+    };
+    const auto values = [&](int i0, int it, float* y) {
+      raw[it].values(y);
+      if (turned) turn_chunk<PC>(g, cs + static_cast<int64_t>(i0 + it) * cs_step, at, y);
+    };
+    const auto largest = [&](uint32_t v) {
+      v = __reduce_max_sync(kFull, v);
+      if constexpr (!WARP) {
+        __syncthreads();  // `red` has been read
+        if ((t & 31) == 0) red[t >> 5] = v;
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 2 * PC; ++j) {
-          const float m = fabsf(y[it][j]);
-          amax = (is_finite(m) && m > amax) ? m : amax;
+        for (int w = 0; w < nt / 32; w += 4) {
+          const uint4 r = *reinterpret_cast<const uint4*>(&red[w]);
+          v = max(max(v, max(r.x, r.y)), max(r.z, r.w));
         }
       }
-    }
-  }
-  // magnitudes are not negative: their bit patterns order them
-  uint32_t bits = __reduce_max_sync(kFull, __float_as_uint(amax));
-  if constexpr (!WARP) {
-    if ((t & 31) == 0) red[t >> 5] = __uint_as_float(bits);
-    __syncthreads();
-    for (int w = 0; w < nt / 32; ++w) bits = max(bits, __float_as_uint(red[w]));
-  }
-  const float need = scale_for(__uint_as_float(bits));
-  const float scale = before >= need ? before : need;
-  if (kept && scale != before) {
-    // the page's earlier codes at the grown scale
-    const float f = before / scale;
-    const int vec = a.D / 16;
-    for (int i = t; i < kept * vec; i += nt) {
-      const int tok = i / vec, c = i - tok * vec;
-      uint4* p = reinterpret_cast<uint4*>(codes + tok * a.token_stride + c * 16);
-      uint4 r = *p;
-      uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+      return v;
+    };
+    // bits of the largest magnitude: they order magnitudes, the infinities and NaN last
+    uint32_t top = 0;
+    int i0 = 0;
+    do {
+      read(i0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 lo = codes2_to_float2(static_cast<uint16_t>(w[j] & 0xffffu));
-        const float2 hi = codes2_to_float2(static_cast<uint16_t>(w[j] >> 16));
-        w[j] = to_codes2(lo.x * f, lo.y * f) | (to_codes2(hi.x * f, hi.y * f) << 16);
-      }
-      *p = r;
-    }
-  }
-  if (t == 0 && !(scale == before)) *sp = scale;
-  const Divider div(scale);
-  for (int base = 0; base < total; base += kAppendIter * nt) {
+      for (int it = 0; it < ITER; ++it) {
+        if (i0 + it < mine) {
+          float y[2 * PC];
+          values(i0, it, y);
 #pragma unroll
-    for (int it = 0; it < kAppendIter; ++it) {
-      const int i = base + it * nt + t;
-      if (i < total) {
-        const int tok = i / per_tok, c = i - tok * per_tok;
-        const ChunkAt at = chunk_at<PC>(g, c);
-        if (!hold)
-          load_chunk<E, PC>(g, x + (p0 - L + tok) * x_tok,
-                            turn ? g.cos_sin + static_cast<int64_t>(p0 + tok) * g.rot : nullptr, at, y[it]);
-        uint8_t* dst = codes + ((p0 + tok) & (S - 1)) * a.token_stride;
-        store_codes<PC>(dst + at.lo, y[it], div);
-        store_codes<PC>(dst + at.hi, y[it] + PC, div);
+          for (int j = 0; j < 2 * PC; ++j) top = max(top, __float_as_uint(y[j]) & 0x7fffffffu);
+        }
+      }
+      i0 += ITER;
+    } while (!hold && i0 < mine);
+    if (page < 0) {
+      if (t == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+      return;
+    }
+    uint8_t* const page_codes = (kv ? a.v_codes : a.k_codes) + page * a.page_stride + h * a.head_stride;
+    float* sp = (kv ? a.v_scale : a.k_scale) + page * a.scale_page_stride + h * a.scale_head_stride;
+    const float before = kept ? *sp : 0.0f;
+    top = largest(top);  // (all have read `before`)
+    bool plain = top < 0x7f800000u;
+    if (!plain) {  // NaN or infinities: the scale is that of the finite values
+      top = 0;
+      i0 = 0;
+      do {
+        if (!hold) read(i0);
+#pragma unroll
+        for (int it = 0; it < ITER; ++it) {
+          if (i0 + it < mine) {
+            float y[2 * PC];
+            values(i0, it, y);
+#pragma unroll
+            for (int j = 0; j < 2 * PC; ++j) {
+              const uint32_t m = __float_as_uint(y[j]) & 0x7fffffffu;
+              top = max(top, m < 0x7f800000u ? m : 0u);
+            }
+          }
+        }
+        i0 += ITER;
+      } while (!hold && i0 < mine);
+      top = largest(top);
+    }
+    const float need = scale_for(__uint_as_float(top));
+    const float scale = before >= need ? before : need;
+    if constexpr (WARP) __syncwarp();
+    if (kept && scale != before) {
+      // the page's earlier codes at the grown scale
+      const float f = before / scale;
+      const int vec = a.D / 16;
+#pragma unroll 1
+      for (int i = t; i < kept * vec; i += nt) {
+        const int tok = i / vec, c = i - tok * vec;
+        uint4* p = reinterpret_cast<uint4*>(page_codes + tok * a.token_stride + c * 16);
+        uint4 r = *p;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 lo = codes2_to_float2(static_cast<uint16_t>(w[j] & 0xffffu));
+          const float2 hi = codes2_to_float2(static_cast<uint16_t>(w[j] >> 16));
+          w[j] = to_codes2(no_infinity(lo.x * f), no_infinity(lo.y * f)) |
+                 (to_codes2(no_infinity(hi.x * f), no_infinity(hi.y * f)) << 16);
+        }
+        *p = r;
       }
     }
+    if (t == 0 && !(scale == before)) *sp = scale;
+    const Divider div(scale);
+    plain = plain && div.exact;
+    const int64_t code_step = step * a.token_stride;
+    uint8_t* const codes = page_codes + (kept + tok0) * a.token_stride;
+    i0 = 0;
+    do {
+      if (!hold) read(i0);
+#pragma unroll
+      for (int it = 0; it < ITER; ++it) {
+        if (i0 + it < mine) {
+          uint8_t* dst = codes + (i0 + it) * code_step;
+          float y[2 * PC];
+          values(i0, it, y);
+          store_codes<PC>(dst + at.lo, y, div, plain);
+          store_codes<PC>(dst + at.hi, y + PC, div, plain);
+        }
+      }
+      i0 += ITER;
+    } while (i0 < mine);
   }
 }
 
-constexpr int kAppendWarpThreads = 128;  // units of a warp: four a CTA
-constexpr int kAppendCtaThreads = 256;   // units of a CTA
-
 template <typename E, int PC, bool WARP>
-__global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads)
+__global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads, WARP ? 1 : kAppendCtas)
     spec_kv_append_kernel(const __grid_constant__ AppendArgs g) {
+  constexpr int nt = WARP ? kAppendWarpThreads : kAppendCtaThreads;
   const KvArgs& a = g.a;
   const int tid = threadIdx.x;
   if (blockIdx.x < static_cast<unsigned>(g.unit_blocks)) {
-    __shared__ float red[WARP ? 1 : kAppendCtaThreads / 32];
+    __shared__ __align__(16) uint32_t red[WARP ? 4 : kAppendCtaThreads / 32];
     if constexpr (WARP) {
-      const int unit = blockIdx.x * (kAppendWarpThreads / 32) + (tid >> 5);
-      if (unit < g.units) append_unit<E, PC, true>(g, unit, tid & 31, 32, red);
+      const int group = blockIdx.x * (kAppendWarpThreads / 32) + (tid >> 5);
+      if (group < g.groups) append_group<E, PC, true>(g, group, tid & 31, red);
     } else {
-      append_unit<E, PC, false>(g, blockIdx.x, tid, kAppendCtaThreads, red);
+      append_group<E, PC, false>(g, blockIdx.x, tid, red);
     }
     return;
   }
-  // queries
-  const int per_tok = a.D / (2 * PC), per_row = a.Hq * per_tok;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x - g.unit_blocks) * g.q_rows_block;
-  const int64_t nrows = static_cast<int64_t>(a.B) * a.T;
-  for (int i = tid; i < g.q_rows_block * per_row; i += blockDim.x) {
-    const int r = i / per_row, j = i - r * per_row;
-    const int64_t row = row0 + r;
-    if (row >= nrows) break;
-    const int b = static_cast<int>(row / a.T), tok = static_cast<int>(row - static_cast<int64_t>(b) * a.T);
-    const int h = j / per_tok, c = j - h * per_tok;
-    int L, n;
-    const bool ok = append_span(g, b, &L, &n);
-    float y[2 * PC];
-    const ChunkAt at = chunk_at<PC>(g, c);
-    if (!ok || tok >= n) {
-      const float fill = ok ? 0.0f : __uint_as_float(0x7fc00000u);
+  // queries: rows (sequence, token); as many side by side as the CTA has threads for
+  const int per_tok = a.D / (2 * PC), heads = a.Hq / g.q_heads, per_row = heads * per_tok;
+  const int beside = max(1, nt / per_row);
+  const int r0 = tid / per_row;  // this thread's row among those side by side
+  if (beside > 1 && r0 >= beside) return;
+  const int nrows = a.B * a.T;
+  const int row0 = static_cast<int>(blockIdx.x - g.unit_blocks) * g.q_rows_block;
+  const int first = row0 + (beside > 1 ? r0 : 0), last = min(nrows, row0 + g.q_rows_block);
+  for (int j = beside > 1 ? tid - r0 * per_row : tid; j < per_row; j += nt) {
+    const int h = j / per_tok;
+    const ChunkAt k = chunk_at<PC>(g, j - h * per_tok);
+    int b = first / a.T, tok = first - b * a.T;
+    for (int row = first; row < last;) {
+      // this sequence's rows among the CTA's: the new tokens, then the empty slots
+      int L, n;
+      const bool ok = append_span(g, b, &L, &n);
+      if (!ok && j == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+      const int rows = (min(last - row, a.T - tok) + beside - 1) / beside;
+      const int full = ok && tok < n ? min(rows, (n - tok + beside - 1) / beside) : 0;
+      const E* q = static_cast<const E*>(a.q) + b * a.q_seq + h * a.q_head + tok * a.q_tok;
+      E* o = static_cast<E*>(a.out) + b * a.o_seq + h * a.o_head + tok * a.o_tok;
+      const float* cs = g.cos_sin + (k.turn ? static_cast<int64_t>(L + tok) * g.rot : 0);
+      const int64_t q_step = beside * a.q_tok, o_step = beside * a.o_tok;
+      const int64_t q_heads = heads * a.q_head, o_heads = heads * a.o_head;
+      if (g.q_heads == 1) {
+        for (int i = 0; i < full; ++i, q += q_step, o += o_step, cs += beside * g.rot) {
+          float y[2 * PC];
+          RawChunk<E, PC> raw;
+          raw.load(q, k);
+          raw.values(y);
+          turn_chunk<PC>(g, cs, k, y);
+          store_n<E, PC>(o + k.lo, y);
+          store_n<E, PC>(o + k.hi, y + PC);
+        }
+      } else {
+        for (int i = 0; i < full; ++i, q += q_step, o += o_step, cs += beside * g.rot) {
+          RawChunk<E, PC> raw[kAppendHeads];
 #pragma unroll
-      for (int e = 0; e < 2 * PC; ++e) y[e] = fill;
-      if (!ok && i == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
-    } else {
-      load_chunk<E, PC>(g, static_cast<const E*>(a.q) + b * a.q_seq + tok * a.q_tok + h * a.q_head,
-                        g.rot > 0 ? g.cos_sin + static_cast<int64_t>(L + tok) * g.rot : nullptr, at, y);
+          for (int e = 0; e < kAppendHeads; ++e) raw[e].load(q + e * q_heads, k);
+          const Angles<PC> at(g, cs, k);
+#pragma unroll
+          for (int e = 0; e < kAppendHeads; ++e) {
+            float y[2 * PC];
+            raw[e].values(y);
+            at.turn_all(g, k, y);
+            store_n<E, PC>(o + e * o_heads + k.lo, y);
+            store_n<E, PC>(o + e * o_heads + k.hi, y + PC);
+          }
+        }
+      }
+      float fill[PC];
+#pragma unroll
+      for (int e = 0; e < PC; ++e) fill[e] = ok ? 0.0f : __uint_as_float(0x7fc00000u);
+      for (int i = full; i < rows; ++i, o += o_step) {
+        for (int e = 0; e < g.q_heads; ++e) {
+          store_n<E, PC>(o + e * o_heads + k.lo, fill);
+          store_n<E, PC>(o + e * o_heads + k.hi, fill);
+        }
+      }
+      row += rows * beside;
+      tok += rows * beside;
+      while (tok >= a.T) {
+        tok -= a.T;
+        ++b;
+      }
     }
-    E* o = static_cast<E*>(a.out) + b * a.o_seq + tok * a.o_tok + h * a.o_head;
-    store_n<E, PC>(o + at.lo, y);
-    store_n<E, PC>(o + at.hi, y + PC);
   }
 }
 
