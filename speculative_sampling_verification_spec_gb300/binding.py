@@ -17,6 +17,7 @@ import torch
 from . import _build
 
 SPEC_OK = 0
+SPEC_ERR_INVALID_ARG = 1
 SPEC_F32, SPEC_BF16 = 0, 1
 STATUS_NAMES = {0: "SPEC_OK", 1: "SPEC_ERR_INVALID_ARG", 2: "SPEC_ERR_CUDA", 3: "SPEC_ERR_NONFINITE",
                 4: "SPEC_ERR_TOKEN_RANGE", 5: "SPEC_ERR_TIMEOUT", 6: "SPEC_ERR_UNSUPPORTED",

@@ -23,19 +23,25 @@ _PARAMS = struct.Struct("@6if3i3P13q3PN")
 _F32, _BF16 = torch.float32, torch.bfloat16
 _DTYPES = {_F32: binding.SPEC_F32, _BF16: binding.SPEC_BF16}
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+_WS_LEAST = 1 << 20     # bytes of a stream's first workspace: most shapes' later calls need no other
+
+
+_loaded = None
 
 
 def _lib():
-    L = binding.lib()
-    if L.spec_kv_append.argtypes is None:
+    global _loaded
+    if _loaded is None:
+        L = binding.lib()
         P = ctypes.c_void_p
         L.spec_kv_attention_workspace_size.argtypes = [P, P]
         L.spec_kv_attention_workspace_size.restype = ctypes.c_size_t
         L.spec_kv_attention.argtypes = [P] * 5
         L.spec_kv_attention.restype = ctypes.c_int
-        L.spec_kv_append.restype = ctypes.c_int
         L.spec_kv_append.argtypes = [P] * 7
-    return L
+        L.spec_kv_append.restype = ctypes.c_int
+        _loaded = L
+    return _loaded
 
 
 class PagedKVCache:
@@ -79,8 +85,16 @@ class PagedKVCache:
         return sum(t.numel() * t.element_size() for t in (self.k_codes, self.v_codes, self.k_scale, self.v_scale))
 
 
+# the current stream's handle without building a Stream object, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_of(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _new(shape, dtype, device, stream):
@@ -97,35 +111,49 @@ def _new(shape, dtype, device, stream):
 _ws_cache = {}
 
 
-def _workspace(nbytes, device, stream):
+def _workspace(key, nbytes, device, stream):
     """The workspace of (device, stream): calls on different streams may overlap, so each stream has its own."""
-    key = (device.index, _stream_of(stream, device))
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(stream):
-            ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)  # counters that calls leave at zero
-        _ws_cache[key] = ws
+    with torch.cuda.stream(stream):
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)  # counters that calls leave at zero
+    _ws_cache[key] = ws
     return ws
 
 
 def _check_table(cache, B, page_table, seq_lens, new_lens, status):
+    dev = cache.device
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
             page_table.shape[1] < 1 or page_table.stride(1) != 1:
         raise ValueError("page_table must be int32 [B, max_pages], contiguous along the pages")
-    for t in (seq_lens, new_lens):
-        if t is not None and (t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous()):
-            raise ValueError("seq_lens and new_lens must be contiguous int32 [B]")
-    for t in (page_table, seq_lens, new_lens, status):
-        if t is not None and t.device != cache.device:
-            raise ValueError("page_table, lengths and status must be on the cache's device")
+    if seq_lens.dtype != torch.int32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be contiguous int32 [B]")
+    if new_lens is not None and (new_lens.dtype != torch.int32 or new_lens.shape != (B,) or
+                                 not new_lens.is_contiguous() or new_lens.device != dev):
+        raise ValueError("new_lens must be contiguous int32 [B] on the cache's device")
+    if page_table.device != dev or seq_lens.device != dev or (status is not None and status.device != dev):
+        raise ValueError("page_table, lengths and status must be on the cache's device")
 
 
-def _check_heads(name, t, shape, dtype, device):
+def _strides(name, t, shape, dtype, device):
+    """The strides of a [B, T, heads, head_dim] tensor, after checking it."""
     if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError("%s must be %s %s on %s, got %s %s on %s" % (name, dtype, tuple(shape), device, t.dtype,
                                                                      tuple(t.shape), t.device))
-    if t.stride(3) != 1:
+    st = t.stride()
+    if st[3] != 1:
         raise ValueError("%s must be contiguous along the channels" % name)
+    return st
+
+
+def _first_check(name, t, heads):
+    """Device, type and shape of the tensor that gives a call its sizes."""
+    if not t.is_cuda:
+        raise ValueError("spec_* calls take CUDA tensors (copy host data to the GPU first)")
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None:
+        raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    if t.dim() != 4:
+        raise ValueError("%s must be [B, T, %s, head_dim]" % (name, heads))
+    return dtype
 
 
 def spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens=None, *, cos_sin=None, interleaved=False,
@@ -138,19 +166,13 @@ def spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens=None, *, cos_s
     sines (None: no rotation); interleaved: pairs are neighbouring channels, else channels i and i + rot_dim / 2.
     Returns the rotated queries (q_out, or a new contiguous tensor; zero in slots past new_lens); q_out may be q.
     The cache is written in place."""
-    if not k.is_cuda:
-        raise ValueError("spec_* calls take CUDA tensors (copy host data to the GPU first)")
-    dtype = _DTYPES.get(k.dtype)
-    if dtype is None:
-        raise TypeError("keys must be float32 or bfloat16, got %s" % k.dtype)
-    if k.dim() != 4:
-        raise ValueError("k must be [B, T, kv_heads, head_dim]")
-    B, T, H, D = k.shape
-    if H != cache.kv_heads or D != cache.head_dim:
-        raise ValueError("k must be [B, T, %d, %d], got %s" % (cache.kv_heads, cache.head_dim, tuple(k.shape)))
-    dev = cache.device
-    _check_heads("k", k, k.shape, k.dtype, dev)
-    _check_heads("v", v, k.shape, k.dtype, dev)
+    dtype = _first_check("k", k, "kv_heads")
+    shape, dt, dev = k.shape, k.dtype, cache.device
+    B, T, hq, D = shape
+    if hq != cache.kv_heads or D != cache.head_dim:
+        raise ValueError("k must be [B, T, %d, %d], got %s" % (cache.kv_heads, cache.head_dim, tuple(shape)))
+    ks = _strides("k", k, shape, dt, dev)
+    vs = _strides("v", v, shape, dt, dev)
     _check_table(cache, B, page_table, seq_lens, new_lens, status)
     rot = rot_len = cs = 0
     if cos_sin is not None:
@@ -158,20 +180,21 @@ def spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens=None, *, cos_s
             raise ValueError("cos_sin must be contiguous float32 [positions, rot_dim] on the cache's device")
         rot_len, rot = cos_sin.shape
         cs = cos_sin.data_ptr()
-    hq, qs, os, qp, op = H, (0, 0, 0), (0, 0, 0), 0, 0
+    qs, os, qp, op = (0, 0, 0, 1), (0, 0, 0, 1), 0, 0
     if q is not None:
         if q.dim() != 4:
             raise ValueError("q must be [B, T, Hq, head_dim]")
         hq = q.shape[2]
-        _check_heads("q", q, (B, T, hq, D), k.dtype, dev)
+        shape = (B, T, hq, D)
+        qs = _strides("q", q, shape, dt, dev)
         if q_out is None:
-            q_out = _new((B, T, hq, D), q.dtype, dev, stream)
+            q_out = _new(shape, dt, dev, stream)
+            os = q_out.stride()
         else:
-            _check_heads("q_out", q_out, (B, T, hq, D), k.dtype, dev)
-        qs, os, qp, op = q.stride(), q_out.stride(), q.data_ptr(), q_out.data_ptr()
+            os = _strides("q_out", q_out, shape, dt, dev)
+        qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    ks, vs = k.stride(), v.stride()
     prm = _PARAMS.pack(B, T, hq, dtype, page_table.shape[1], 0, 0.0, rot, rot_len, 1 if interleaved else 0,
                        page_table.data_ptr(), seq_lens.data_ptr(), 0 if new_lens is None else new_lens.data_ptr(),
                        page_table.stride(0), qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], os[0],
@@ -191,43 +214,44 @@ def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=No
     included.  Returns out [B, T, Hq, D] (zero in slots past new_lens), or (out, lse) with lse [B, T, Hq] float32, the
     natural logarithm of the sum of the weights, when return_lse or lse is given.  ws: a workspace of
     spec_kv_attention_workspace_size bytes (uint8, CUDA, zeroed once); by default one is kept for each stream."""
-    if not q.is_cuda:
-        raise ValueError("spec_* calls take CUDA tensors (copy host data to the GPU first)")
-    dtype = _DTYPES.get(q.dtype)
-    if dtype is None:
-        raise TypeError("queries must be float32 or bfloat16, got %s" % q.dtype)
-    if q.dim() != 4:
-        raise ValueError("q must be [B, T, Hq, head_dim]")
-    B, T, hq, D = q.shape
-    dev = cache.device
-    _check_heads("q", q, (B, T, hq, cache.head_dim), q.dtype, dev)
+    dtype = _first_check("q", q, "Hq")
+    shape, dt, dev = q.shape, q.dtype, cache.device
+    B, T, hq, D = shape
+    if D != cache.head_dim:
+        raise ValueError("q must be [B, T, Hq, %d], got %s" % (cache.head_dim, tuple(shape)))
+    qs = _strides("q", q, shape, dt, dev)
     _check_table(cache, B, page_table, seq_lens, new_lens, status)
     if out is None:
-        out = _new((B, T, hq, D), q.dtype, dev, stream)
+        out = _new(shape, dt, dev, stream)
+        os = out.stride()
     else:
-        _check_heads("out", out, (B, T, hq, D), q.dtype, dev)
+        os = _strides("out", out, shape, dt, dev)
     if lse is not None:
-        if lse.dtype != _F32 or lse.shape != (B, T, hq) or not lse.is_contiguous() or lse.device != dev:
+        if lse.dtype != _F32 or lse.shape != shape[:3] or not lse.is_contiguous() or lse.device != dev:
             raise ValueError("lse must be contiguous float32 [B, T, Hq] on the cache's device")
     elif return_lse:
-        lse = _new((B, T, hq), _F32, dev, stream)
-    L = _lib()
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    qs, os = q.stride(), out.stride()
+        lse = _new(shape[:3], _F32, dev, stream)
     handle = _stream_of(stream, dev)
-
-    def pack(wp, wn):
-        return _PARAMS.pack(B, T, hq, dtype, page_table.shape[1], window, scale, 0, 0, 0, page_table.data_ptr(),
-                            seq_lens.data_ptr(), 0 if new_lens is None else new_lens.data_ptr(), page_table.stride(0),
-                            qs[0], qs[1], qs[2], 0, 0, 0, 0, 0, 0, os[0], os[1], os[2], handle,
-                            0 if status is None else status.data_ptr(), wp, wn)
-
+    key = (dev.index, handle)
     if ws is None:
-        nbytes = L.spec_kv_attention_workspace_size(cache._packed, pack(0, 0))
-        ws = _workspace(max(nbytes, 256), dev, stream)
-    code = L.spec_kv_attention(q.data_ptr(), cache._packed, pack(ws.data_ptr(), ws.numel()), out.data_ptr(),
-                               0 if lse is None else lse.data_ptr())
+        ws = _ws_cache.get(key)
+    fixed = (B, T, hq, dtype, page_table.shape[1], window, 1.0 / math.sqrt(D) if scale is None else scale, 0, 0, 0,
+             page_table.data_ptr(), seq_lens.data_ptr(), 0 if new_lens is None else new_lens.data_ptr(),
+             page_table.stride(0), qs[0], qs[1], qs[2], 0, 0, 0, 0, 0, 0, os[0], os[1], os[2], handle,
+             0 if status is None else status.data_ptr())
+    args = (q.data_ptr(), cache._packed, out.data_ptr(), 0 if lse is None else lse.data_ptr())
+    L = _lib()
+    if ws is None:
+        nbytes = L.spec_kv_attention_workspace_size(cache._packed, _PARAMS.pack(*fixed, 0, 0))
+        ws = _workspace(key, max(nbytes, _WS_LEAST), dev, stream)
+    code = L.spec_kv_attention(args[0], args[1], _PARAMS.pack(*fixed, ws.data_ptr(), ws.numel()), args[2], args[3])
+    if code == binding.SPEC_ERR_INVALID_ARG and ws is _ws_cache.get(key):
+        # the stream's workspace may be too small for this shape: a larger one is made, once
+        nbytes = L.spec_kv_attention_workspace_size(cache._packed, _PARAMS.pack(*fixed, 0, 0))
+        if nbytes > ws.numel():
+            ws = _workspace(key, nbytes, dev, stream)
+            code = L.spec_kv_attention(args[0], args[1], _PARAMS.pack(*fixed, ws.data_ptr(), ws.numel()), args[2],
+                                       args[3])
     if code != binding.SPEC_OK:
         raise binding.SpecError(code, "spec_kv_attention")
     return out if lse is None else (out, lse)
