@@ -11,7 +11,9 @@
 //
 // Tokens and channels are the instruction's 128 rows and the query rows its
 // columns, so its cost goes with the rows there are (from 16) and not with 128.
-// A row is a (new token, query head) of one key/value head.
+// A row is a (new token, query head) of one key/value head; the two softmax groups
+// take half of the rows each, four at a time, the first half in columns 0.. and
+// the second in columns NR / 2...
 //
 // What is not 8 bits is carried in two 8-bit pieces of 4 significant bits each:
 //   q / 2^e = hi + lo, two products into one accumulator (a bfloat16 has 8
@@ -45,12 +47,14 @@ constexpr int kScaleRing = 8;       // tiles of scales; a loader is never this f
 constexpr int kSlack = 3;           // log2 of how far weights may pass the reference
 constexpr float kShift = 8 - kSlack;  // a raised reference is kShift below the largest score: weights stay within 2^8 < 448
 
-// stages of keys and of values, buffers of weights: what two CTAs an SM leave room for
+// Stages of keys and of values, buffers of weights: what two CTAs an SM leave room
+// for.  Keys are used up two tiles ahead of the weights (the scores are
+// double-buffered), so values get the larger share.
 template <int D, int NR>
 struct MmaCfg {
   static constexpr int kTileBytes = kTile * D;
-  static constexpr int KS = D == 64 ? 4 : NR <= 32 ? 3 : NR == 48 ? 3 : 2;
-  static constexpr int VS = D == 64 ? 4 : NR == 16 ? 3 : 2;
+  static constexpr int KS = D == 64 ? 3 : 2;
+  static constexpr int VS = D == 64 ? 5 : NR == 16 ? 4 : NR <= 48 ? 3 : 2;
   static constexpr int PB = (D == 64 || NR <= 32) ? 2 : 1;
   static constexpr int kQBytes = NR * D;             // one piece
   static constexpr int kPBytes = kTile * 2 * NR;     // both pieces
@@ -387,22 +391,31 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       __syncwarp();
     } else {
       // -------------------------------------------------------------- softmax
-      constexpr int RT = NR / 2;                 // rows of a group
-      constexpr int CH = RT % 16 == 0 ? 16 : 8;  // rows at a time
-      constexpr bool kHold = RT <= 24;           // the scores of a tile stay in registers between max and weights
+      constexpr int RT = NR / 2;         // columns of a group
+      constexpr int CH = 4;              // rows at a time
+      constexpr bool kHold = RT <= 24;   // the scores of a tile stay in registers between max and weights
       const int group = warp >> 2, token = tid & 127, r_base = group * RT;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;  // tensor memory lanes of this warp
       const uint32_t tO = tm + lanes + 2 * NR + r_base;                     // first pieces; the second NR further
       bool fail = false;
       while (walk_next(a, walk, p)) {
         const int m = p.tile1 - p.tile0;
+        // rows of the first group (the second has the rest), and of this one in fours
+        const int half = min(RT, (p.nrows + 7) / 8 * 4);
+        const int mine = group == 0 ? min(half, p.nrows) : p.nrows - half;
+        const int fours = max(0, (mine + 3) / 4 * 4);
+        const auto row_of = [&](int col) {  // of a column: nrows and more for none
+          const int r = col < RT ? col : col - RT + half;
+          return col < RT ? (col < half ? r : p.nrows) : r;
+        };
         float l[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) l[r] = 0.0f;
         soft_sync();  // the piece before has been written out
         if (tid < NR) {
-          const bool row = tid < p.nrows;
-          const int gr = p.row0 + tid, t = gr / a.G, g = gr - t * a.G;
+          const int r = row_of(tid);
+          const bool row = r < p.nrows;
+          const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
           sm.pos[tid] = row ? p.L + t : -1;
           sm.out_at[tid] = p.b * a.o_seq + t * a.o_tok + (p.h * a.G + g) * a.o_head;
           sm.lse_at[tid] = (static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g;
@@ -413,11 +426,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           constexpr int kStep = kSoftThreads / kPer;   // rows at a time
 #pragma unroll 1
           for (int r0 = 0; r0 < NR; r0 += kStep) {
-            const int r = r0 + tid / kPer, c = tid % kPer;
+            const int col = r0 + tid / kPer, c = tid % kPer, r = row_of(col);
             float x[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-            if (r < p.nrows) {
+            if (col < NR && r < p.nrows) {
               const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
               const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + p.b * a.q_seq + t * a.q_tok +
                                          (p.h * a.G + g) * a.q_head + c * 16;
@@ -454,16 +467,16 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
               hi[i] = h4;
               lo[i] = l4;
             }
-            if (r < NR) {
-              uint8_t* dst = sq + c * (NR * 16) + r * 16;
+            if (col < NR) {
+              uint8_t* dst = sq + c * (NR * 16) + col * 16;
               *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
               *reinterpret_cast<uint4*>(dst + C::kQBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
               if (c == 0) {
                 const bool row = r < p.nrows;
-                float* tab = reinterpret_cast<float*>(&sm.rowtab[r >> 1]);
+                float* tab = reinterpret_cast<float*>(&sm.rowtab[col >> 1]);
                 // a row that is not there has a reference no score passes
-                tab[r & 1] = row ? (fin ? s * a.scale2 : __uint_as_float(0x7fc00000u)) : 0.0f;
-                tab[2 + (r & 1)] = row ? -kNoRef : kNoRef;
+                tab[col & 1] = row ? (fin ? s * a.scale2 : __uint_as_float(0x7fc00000u)) : 0.0f;
+                tab[2 + (col & 1)] = row ? -kNoRef : kNoRef;
               }
             }
           }
@@ -523,49 +536,65 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
               for (int i = 0; i < CH; ++i) x[i] = sees(c + i) ? x[i] : -INFINITY;
             }
           };
-          float x[kHold ? RT : CH];
+          float x[kHold ? RT : 16];
+          const auto load16 = [&](int c0, float* y) {
+            if constexpr (RT % 16 == 0) {
+              tmem_ld<16>(tS + c0, y);
+            } else {
+              tmem_ld<8>(tS + c0, y);
+              if (c0 + 8 < RT) tmem_ld<8>(tS + c0 + 8, y + 8);
+            }
+          };
           while (true) {
             float top = -INFINITY;
             if constexpr (kHold) {
 #pragma unroll
-              for (int c = 0; c < RT; c += CH) tmem_ld<CH>(tS + c, &x[c]);
+              for (int c = 0; c < RT; c += 16) load16(c, &x[c]);
               tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < RT; c += 8) tmem_tie<8>(&x[c]);
             }
 #pragma unroll
-            for (int c = 0; c < RT; c += CH) {
+            for (int c = 0; c < RT; c += 16) {
               float* y = &x[kHold ? c : 0];
+              constexpr int kLast = RT % 16 ? 8 : 16;
+              const int n16 = c + 16 <= RT ? 16 : kLast;
               if constexpr (!kHold) {
-                tmem_ld<CH>(tS + c, y);
+                load16(c, y);
                 tmem_wait_ld();
+                tmem_tie<16>(y);
               }
-              tmem_tie<CH>(y);
-              against_refs(c, y);
 #pragma unroll
-              for (int i = 0; i < CH; i += 2) top = fmaxf(top, fmaxf(y[i], y[i + 1]));
+              for (int i = 0; i < 16; i += CH) {
+                if (i < n16 && c + i < fours) {
+                  against_refs(c + i, y + i);
+                  top = fmaxf(fmaxf(top, fmaxf(y[i], y[i + 1])), fmaxf(y[i + 2], y[i + 3]));
+                }
+              }
             }
             // would some weight leave the 8-bit range?
             if (!group_any(group, top > 8.0f)) break;
             // raise the references to the largest score so far
 #pragma unroll 1
-            for (int c = 0; c < RT; c += CH) {
-              float y[CH];
-              tmem_ld<CH>(tS + c, y);
+            for (int c = 0; c < fours; c += 8) {
+              float y[8];
+              tmem_ld<8>(tS + c, y);
               tmem_wait_ld();
-              tmem_tie<CH>(y);
-              float mine = -INFINITY;
+              tmem_tie<8>(y);
+              float most = -INFINITY;
 #pragma unroll
-              for (int i = 0; i < CH; ++i) {
+              for (int i = 0; i < 8; ++i) {
                 const float* tab = reinterpret_cast<const float*>(&sm.rowtab[(r_base + c + i) >> 1]);
                 float u = fmaf(y[i], sc.x * tab[i & 1], sc.y);
                 if (edge && !sees(c + i)) u = -INFINITY;
                 u = u == u ? u : -INFINITY;
                 const float w = of_order(__reduce_max_sync(kFull, order_of(u)));
-                if (lane == i) mine = w;
+                if (lane == i) most = w;
               }
-              if (lane < CH) sm.red[warp & 3][r_base + c + lane] = mine;
+              if (lane < 8) sm.red[warp & 3][r_base + c + lane] = most;
             }
             group_sync(group);
-            if (token < RT) {
+            if (token < fours) {
               const int r = r_base + token;
               float* ref = reinterpret_cast<float*>(&sm.rowtab[r >> 1]) + 2 + (r & 1);
               const float before = -*ref;
@@ -578,25 +607,30 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             if (t > p.tile0) {
 #pragma unroll
               for (int r = 0; r < RT; r += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(&sm.fac[r_base + r]);
-                l[r] *= f.x;
-                l[r + 1] *= f.y;
-                l[r + 2] *= f.z;
-                l[r + 3] *= f.w;
+                if (r < fours) {
+                  const float4 f = *reinterpret_cast<const float4*>(&sm.fac[r_base + r]);
+                  l[r] *= f.x;
+                  l[r + 1] *= f.y;
+                  l[r + 2] *= f.z;
+                  l[r + 3] *= f.w;
+                }
               }
               if (!fail) fail = !bar_wait(&sm.pv_done[(n - 1) % C::PB], ((n - 1) / C::PB) & 1, gave_up);
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < 2 * RT; c += CH) {
-                const int r = c < RT ? c : c - RT;
-                const uint32_t at = tO + r + (c < RT ? 0 : NR);
-                float o[CH];
-                tmem_ld<CH>(at, o);
+              for (int c = 0; c < fours; c += 8) {  // (past the last row, what is there is not used)
+                float o[16];
+                tmem_ld<8>(tO + c, o);
+                tmem_ld<8>(tO + NR + c, o + 8);
                 tmem_wait_ld();
-                tmem_tie<CH>(o);
+                tmem_tie<16>(o);
 #pragma unroll
-                for (int i = 0; i < CH; ++i) o[i] *= sm.fac[r_base + r + i];
-                tmem_st<CH>(at, o);
+                for (int i = 0; i < 8; ++i) {
+                  o[i] *= sm.fac[r_base + c + i];
+                  o[8 + i] *= sm.fac[r_base + c + i];
+                }
+                tmem_st<8>(tO + c, o);
+                tmem_st<8>(tO + NR + c, o + 8);
               }
               tmem_wait_st();
             }
@@ -605,36 +639,46 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           if (n >= C::PB && !fail) fail = !bar_wait(&sm.pv_done[n % C::PB], (n / C::PB - 1) & 1, gave_up);
           uint8_t* dst = sp + (n % C::PB) * C::kPBytes + token * 16;
 #pragma unroll
-          for (int c = 0; c < RT; c += CH) {
+          for (int c = 0; c < RT; c += 16) {
             float* y = &x[kHold ? c : 0];
+            constexpr int kLast = RT % 16 ? 8 : 16;
+            const int n16 = c + 16 <= RT ? 16 : kLast;
             if constexpr (!kHold) {
-              tmem_ld<CH>(tS + c, y);
+              load16(c, y);
               tmem_wait_ld();
-              tmem_tie<CH>(y);
-              against_refs(c, y);
+              tmem_tie<16>(y);
             }
-            uint32_t hi[CH / 4], lo[CH / 4];
+            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < CH; i += 4) {
-              uint32_t h[2], d[2];
+            for (int i = 0; i < 16; i += CH) {
+              if (i < n16 && c + i < fours) {
+                if constexpr (!kHold) against_refs(c + i, y + i);
+                uint32_t h[2], d[2];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int r = c + i + 2 * e;
-                const float w0 = ex2(y[i + 2 * e]), w1 = ex2(y[i + 2 * e + 1]);
-                unpack2(fma2(pack2(w0, w1), ivs2, pack2(l[r], l[r + 1])), l[r], l[r + 1]);
-                two_pieces(w0, w1, h[e], d[e]);
+                for (int e = 0; e < 2; ++e) {
+                  const int r = c + i + 2 * e;
+                  const float w0 = ex2(y[i + 2 * e]), w1 = ex2(y[i + 2 * e + 1]);
+                  unpack2(fma2(pack2(w0, w1), ivs2, pack2(l[r], l[r + 1])), l[r], l[r + 1]);
+                  two_pieces(w0, w1, h[e], d[e]);
+                }
+                hi[i / 4] = h[0] | (h[1] << 16);
+                lo[i / 4] = d[0] | (d[1] << 16);
               }
-              hi[i / 4] = h[0] | (h[1] << 16);
-              lo[i / 4] = d[0] | (d[1] << 16);
             }
-            const int r = r_base + c;
-            uint8_t* at = dst + (r / 16) * (kTile * 16) + (r % 16);
-            if constexpr (CH == 16) {
+            const int col = r_base + c;
+            uint8_t* at = dst + (col / 16) * (kTile * 16) + (col % 16);
+            constexpr int kLoAt = (NR / 16) * (kTile * 16);
+            if (RT % 16 == 0) {
               *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(at + (NR / 16) * (kTile * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            } else {
+              *reinterpret_cast<uint4*>(at + kLoAt) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {  // eight columns at a time: a block of 16 may be shared with the other group
               *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(at + (NR / 16) * (kTile * 16)) = make_uint2(lo[0], lo[1]);
+              *reinterpret_cast<uint2*>(at + kLoAt) = make_uint2(lo[0], lo[1]);
+              if (n16 == 16) {
+                uint8_t* next = dst + ((col + 8) / 16) * (kTile * 16) + ((col + 8) % 16);
+                *reinterpret_cast<uint2*>(next) = make_uint2(hi[2], hi[3]);
+                *reinterpret_cast<uint2*>(next + kLoAt) = make_uint2(lo[2], lo[3]);
+              }
             }
           }
           if (poison) {
@@ -652,12 +696,14 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         fail = soft_any(fail);
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < RT; c += CH) {
-          const float s = lane_sums<CH>(l + c);
-          if (lane < CH) sm.red[warp & 3][r_base + c + lane] = s;
+        for (int c = 0; c < RT; c += 8) {
+          if (c < fours) {
+            const float s = lane_sums<8>(l + c);
+            if (lane < 8) sm.red[warp & 3][r_base + c + lane] = s;
+          }
         }
         soft_sync();
-        if (tid < p.nrows) {
+        if (tid < NR && row_of(tid) < p.nrows) {
           const float ref = m > 0 ? -reinterpret_cast<const float*>(&sm.rowtab[tid >> 1])[2 + (tid & 1)] : kNoRef;
           float s = sm.red[0][tid] + sm.red[1][tid] + sm.red[2][tid] + sm.red[3][tid];
           if (fail) s = __uint_as_float(0x7fc00000u);
@@ -665,14 +711,15 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             if (a.lse) a.lse[sm.lse_at[tid]] = lse_of(ref, s);
             sm.fac[tid] = 1.0f / s;
           } else {
-            a.part_ml[static_cast<int64_t>(p.slot) * a.slot_rows + tid] = make_float2(ref, s);
+            a.part_ml[static_cast<int64_t>(p.slot) * a.slot_rows + row_of(tid)] = make_float2(ref, s);
           }
         }
         if (p.whole()) soft_sync();
         if (m > 0 && (warp & 3) * 32 < D) {
-          float* part = a.part_o + (static_cast<int64_t>(p.slot) * a.slot_rows + r_base) * D + token;
+          const int row0 = group == 0 ? 0 : half;
+          float* part = a.part_o + (static_cast<int64_t>(p.slot) * a.slot_rows + row0) * D + token;
 #pragma unroll 1
-          for (int c = 0; c < RT; c += 8) {
+          for (int c = 0; c < fours; c += 8) {
             float o[16];  // both pieces of eight rows
             tmem_ld<8>(tO + c, o);
             tmem_ld<8>(tO + NR + c, o + 8);
@@ -681,7 +728,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int r = r_base + c + i;
-              if (r < p.nrows) {
+              if (c + i < mine) {
                 const float y = fmaf(o[8 + i], 0.0625f, o[i]);
                 if (p.whole())
                   from_float(y * sm.fac[r], static_cast<__nv_bfloat16*>(a.out) + sm.out_at[r] + token);
