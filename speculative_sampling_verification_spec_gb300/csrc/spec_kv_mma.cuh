@@ -17,7 +17,9 @@
 //
 // What is not 8 bits is carried in two 8-bit pieces of 4 significant bits each:
 //   q / 2^e = hi + lo, two products into one accumulator (a bfloat16 has 8
-//     significant bits: exact but for 2^-17 of the row's largest channel);
+//     significant bits: exact but for 2^-17 of the row's largest channel; rows
+//     within 2^kNear of each other share one e, for 2^-17 of the largest's, and
+//     one factor of the scores with it);
 //   p = hi + lo / 16, the pieces side by side as columns of one product and added
 //     at the end (a relative 2^-8 at most, 2^-10.6 on average; sums are of the
 //     float p).
@@ -44,6 +46,7 @@ namespace spec_kv_detail {
 constexpr int kMmaThreads = 320;
 constexpr int kSoftThreads = 256;  // two groups of 128, a token a thread
 constexpr int kScaleRing = 8;       // tiles of scales; a loader is never this far ahead of the softmax
+constexpr int kNear = 4;            // log2 of how far apart rows with one exponent may be
 constexpr int kSlack = 3;           // log2 of how far weights may pass the reference
 constexpr float kShift = 8 - kSlack;  // a raised reference is kShift below the largest score: weights stay within 2^8 < 448
 
@@ -70,8 +73,10 @@ template <int D, int NR>
 struct MmaSmall {
   using C = MmaCfg<D, NR>;
   uint64_t k_full[C::KS], k_empty[C::KS], v_full[C::VS], v_empty[C::VS];
-  uint64_t s_full[2], p_full[C::PB], pv_done[C::PB], sc_full[kScaleRing], q_full, drain;
-  float4 rowtab[NR / 2];  // of two rows: factors of the scores, negated references
+  uint64_t s_full[2], p_full[C::PB], pv_done[C::PB], q_full, drain;
+  alignas(16) float refs[NR];     // negated references of the rows
+  alignas(16) float factor[NR];   // of the scores, where rows have exponents of their own
+  uint32_t q_top, q_least;        // largest and least of the rows' largest magnitudes
   float4 scales[kScaleRing][kTile / 16];  // of a page: key scale; value scale's log2 and reciprocal
   int64_t out_at[NR];     // element of the output (of lse for `lse_at`) where a row begins
   int64_t lse_at[NR];
@@ -199,6 +204,18 @@ __device__ __forceinline__ void two_pieces(float w0, float w1, uint32_t& hi, uin
   lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(d), __NV_SATFINITE, __NV_E4M3);
 }
 
+// 16 channels of a row that is not aligned, as if loaded 16 bytes at a time
+static __device__ __noinline__ RawChunk<__nv_bfloat16, 8> gather16(const __nv_bfloat16* src) {
+  RawChunk<__nv_bfloat16, 8> r;
+  const unsigned short* s = reinterpret_cast<const unsigned short*>(src);
+  uint32_t u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = s[2 * i] | (static_cast<uint32_t>(s[2 * i + 1]) << 16);
+  r.lo.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+  r.hi.w[0] = make_uint4(u[4], u[5], u[6], u[7]);
+  return r;
+}
+
 template <int D, int NR>
 __global__ void __launch_bounds__(kMmaThreads, 2)
     spec_kv_attention_mma_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ MmaMaps maps) {
@@ -222,12 +239,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       bar_init(&sm.v_full[i], 1);
       bar_init(&sm.v_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) bar_init(&sm.s_full[i], 1);
+    for (int i = 0; i < 2; ++i) bar_init(&sm.s_full[i], 2);
     for (int i = 0; i < C::PB; ++i) {
       bar_init(&sm.p_full[i], kSoftThreads / 32);
       bar_init(&sm.pv_done[i], 1);
     }
-    for (int i = 0; i < kScaleRing; ++i) bar_init(&sm.sc_full[i], 1);
     bar_init(&sm.q_full, 1);
     bar_init(&sm.drain, 1);
     sm.gave_up = 0;
@@ -305,15 +321,15 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           if (n >= C::KS) ok = bar_wait(&sm.k_empty[ks], (n / C::KS - 1) & 1, gave_up);
           ok = __all_sync(kFull, ok);
           if (!ok) break;
-          if (lane == 0) bar_arrive_expect(&sm.k_full[ks], cnt * page_bytes);
           if (mine >= 0 && mine < np) {
             const float v = sc.y < 7.8886090522101181e-31f ? 7.8886090522101181e-31f : sc.y;  // 2^-100
             sm.scales[n % kScaleRing][mine] = make_float4(sc.x, log2f(v), 1.0f / v, 0.0f);
           }
+          __syncwarp();  // the scales are written: they come with the keys
+          if (lane == 0) bar_arrive_expect(&sm.k_full[ks], cnt * page_bytes);
           __syncwarp();
           if (has)
             tma_load_4d(sk + ks * C::kTileBytes + mine * page_bytes, &maps.k, 0, y, z, w, &sm.k_full[ks]);
-          if (lane == 0) bar_arrive(&sm.sc_full[n % kScaleRing]);
           if (n >= C::VS) ok = bar_wait(&sm.v_empty[vs], (n / C::VS - 1) & 1, gave_up);
           ok = __all_sync(kFull, ok);
           if (!ok) {
@@ -359,6 +375,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
                      half + k > 0);
           mma_commit(&sm.k_empty[st]);
           mma_commit(&sm.s_full[i & 1]);
+          bar_arrive(&sm.s_full[i & 1]);  // passes the loader's scales on, as a commit alone need not
         };
         while (ok && walk_next(a, walk, p)) {
           const int m = p.tile1 - p.tile0;
@@ -420,43 +437,80 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           sm.out_at[tid] = p.b * a.o_seq + t * a.o_tok + (p.h * a.G + g) * a.o_head;
           sm.lse_at[tid] = (static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g;
         }
+        if (tid == 0) {
+          sm.q_top = 0;
+          sm.q_least = 0x7f7fffffu;
+        }
+        bool one_factor = true;
+        float factor = 0.0f;
         if (m > 0 && !fail) {
           // queries: 16 channels a thread
           constexpr int kPer = D / 16;                 // threads a row
           constexpr int kStep = kSoftThreads / kPer;   // rows at a time
-#pragma unroll 1
-          for (int r0 = 0; r0 < NR; r0 += kStep) {
-            const int col = r0 + tid / kPer, c = tid % kPer, r = row_of(col);
-            float x[16];
+          constexpr int kTimes = (NR + kStep - 1) / kStep;
+          RawChunk<__nv_bfloat16, 8> raw[kTimes];
+          uint32_t tops[kTimes];  // bits of a row's largest magnitude (NaN above infinity)
+          soft_sync();            // q_top and q_least are set
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+          for (int i = 0; i < kTimes; ++i) {
+            const int col = i * kStep + tid / kPer, c = tid % kPer, r = row_of(col);
+            raw[i].lo.w[0] = raw[i].hi.w[0] = make_uint4(0, 0, 0, 0);
             if (col < NR && r < p.nrows) {
               const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
               const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + p.b * a.q_seq + t * a.q_tok +
                                          (p.h * a.G + g) * a.q_head + c * 16;
               if (a.q_vec) {
-                load_n<__nv_bfloat16, 8>(src, x);
-                load_n<__nv_bfloat16, 8>(src + 8, x + 8);
+                raw[i].lo.load(src);
+                raw[i].hi.load(src + 8);
               } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = to_float(src[i]);
+                raw[i] = gather16(src);
               }
             }
-            uint32_t top = 0;  // bits of the largest magnitude (NaN above infinity)
+          }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+          for (int i = 0; i < kTimes; ++i) {
+            float x[16];
+            raw[i].values(x);
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
 #pragma unroll
             for (int d = kPer / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(kFull, top, d));
-            const bool fin = top < 0x7f800000u;
-            const float s = scale_for(__uint_as_float(top));
-            const float inv = fin ? 1.0f / s : 0.0f;
+            tops[i] = top;
+            if (tid % kPer == 0 && top > 0 && top < 0x7f800000u) {
+              atomicMax(&sm.q_top, top);
+              atomicMin(&sm.q_least, top);
+            }
+          }
+          soft_sync();
+          const uint32_t q_top = sm.q_top;
+          const float common = scale_for(__uint_as_float(q_top));
+          one_factor = q_top < sm.q_least + (static_cast<uint32_t>(kNear) << 23);
+          factor = one_factor ? common * a.scale2 : a.scale2;
+#pragma unroll 1
+          for (int i = 0; i < kTimes; ++i) {
+            const int col = i * kStep + tid / kPer, c = tid % kPer;
+            RawChunk<__nv_bfloat16, 8> now = raw[0];
+            uint32_t top = tops[0];
+#pragma unroll
+            for (int e = 1; e < kTimes; ++e) {
+              if (i == e) {
+                now = raw[e];
+                top = tops[e];
+              }
+            }
+            float x[16];
+            now.values(x);
+            const bool fin = top < 0x7f800000u;  // a row that is not is NaN by its reference
+            const float s = one_factor ? common : fin ? scale_for(__uint_as_float(top)) : 1.0f;
+            const float inv = 1.0f / s;
             uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int e4 = 0; e4 < 4; ++e4) {
               uint32_t h4 = 0, l4 = 0;
 #pragma unroll
               for (int e = 0; e < 4; e += 2) {
-                const float2 y = make_float2(fin ? x[4 * i + e] * inv : 0.0f, fin ? x[4 * i + e + 1] * inv : 0.0f);
+                const float2 y = make_float2(fin ? x[4 * e4 + e] * inv : 0.0f, fin ? x[4 * e4 + e + 1] * inv : 0.0f);
                 const uint16_t ch = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
                 const float2 b = codes2_to_float2(ch);
                 const uint16_t cl =
@@ -464,19 +518,17 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
                 h4 |= static_cast<uint32_t>(ch) << (8 * e);
                 l4 |= static_cast<uint32_t>(cl) << (8 * e);
               }
-              hi[i] = h4;
-              lo[i] = l4;
+              hi[e4] = h4;
+              lo[e4] = l4;
             }
             if (col < NR) {
               uint8_t* dst = sq + c * (NR * 16) + col * 16;
               *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
               *reinterpret_cast<uint4*>(dst + C::kQBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
               if (c == 0) {
-                const bool row = r < p.nrows;
-                float* tab = reinterpret_cast<float*>(&sm.rowtab[col >> 1]);
                 // a row that is not there has a reference no score passes
-                tab[col & 1] = row ? (fin ? s * a.scale2 : __uint_as_float(0x7fc00000u)) : 0.0f;
-                tab[2 + (col & 1)] = row ? -kNoRef : kNoRef;
+                sm.refs[col] = row_of(col) >= p.nrows ? kNoRef : fin ? -kNoRef : __uint_as_float(0x7fc00000u);
+                sm.factor[col] = s;
               }
             }
           }
@@ -488,7 +540,10 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         const int pos_lo = p.L + p.row0 / a.G, pos_hi = p.L + (p.row0 + p.nrows - 1) / a.G;
         for (int t = p.tile0; t < p.tile1; ++t, ++n) {
           const int j = t * kTile + token;
-          if (!fail) fail = !bar_wait(&sm.sc_full[n % kScaleRing], (n / kScaleRing) & 1, gave_up);
+          // scores of this tile; they come with its scales, and with the end of the products two
+          // tiles back (issued before them): with two buffers of weights this one's is free
+          if (!fail) fail = !bar_wait(&sm.s_full[n & 1], (n >> 1) & 1, gave_up);
+          tc_fence_after();
           float4 sc = sm.scales[n % kScaleRing][token >> a.log_page];
           // tiles that some row sees only in part
           const bool edge = t * kTile + kTile - 1 > pos_lo || (a.window > 0 && t * kTile <= pos_hi - a.window);
@@ -515,22 +570,25 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
               if (gone || bad_scale) sc = make_float4(0.0f, 0.0f, 1.0f, 0.0f);
             }
           }
-          const u64 ks2 = pack2(sc.x, sc.x), lv2 = pack2(sc.y, sc.y), ivs2 = pack2(sc.z, sc.z);
+          const float ks = sc.x * factor;
+          const u64 ks2 = pack2(ks, ks), lv2 = pack2(sc.y, sc.y), ivs2 = pack2(sc.z, sc.z);
           const uint32_t tS = tm + lanes + (n & 1) * NR + r_base;
-          if (!fail) fail = !bar_wait(&sm.s_full[n & 1], (n >> 1) & 1, gave_up);
-          tc_fence_after();
           const auto sees = [&](int r) {
             const int q = sm.pos[r_base + r];
             return j <= q && (a.window <= 0 || j > q - a.window);
           };
           // scores of rows c.. in log2 units against their references
           const auto against_refs = [&](int c, float* x) {
-#pragma unroll
-            for (int i = 0; i < CH; i += 2) {
-              const float4 tab = sm.rowtab[(r_base + c + i) >> 1];
-              const u64 f = mul2(ks2, pack2(tab.x, tab.y));
-              unpack2(fma2(pack2(x[i], x[i + 1]), f, add2(lv2, pack2(tab.z, tab.w))), x[i], x[i + 1]);
+            if (!one_factor) {
+              const float4 f = *reinterpret_cast<const float4*>(&sm.factor[r_base + c]);
+              x[0] *= f.x;
+              x[1] *= f.y;
+              x[2] *= f.z;
+              x[3] *= f.w;
             }
+            const float4 ref = *reinterpret_cast<const float4*>(&sm.refs[r_base + c]);
+            unpack2(fma2(pack2(x[0], x[1]), ks2, add2(lv2, pack2(ref.x, ref.y))), x[0], x[1]);
+            unpack2(fma2(pack2(x[2], x[3]), ks2, add2(lv2, pack2(ref.z, ref.w))), x[2], x[3]);
             if (edge) {
 #pragma unroll
               for (int i = 0; i < CH; ++i) x[i] = sees(c + i) ? x[i] : -INFINITY;
@@ -584,8 +642,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
               float most = -INFINITY;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float* tab = reinterpret_cast<const float*>(&sm.rowtab[(r_base + c + i) >> 1]);
-                float u = fmaf(y[i], sc.x * tab[i & 1], sc.y);
+                float u = fmaf(one_factor ? y[i] : y[i] * sm.factor[r_base + c + i], ks, sc.y);
                 if (edge && !sees(c + i)) u = -INFINITY;
                 u = u == u ? u : -INFINITY;
                 const float w = of_order(__reduce_max_sync(kFull, order_of(u)));
@@ -596,12 +653,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             group_sync(group);
             if (token < fours) {
               const int r = r_base + token;
-              float* ref = reinterpret_cast<float*>(&sm.rowtab[r >> 1]) + 2 + (r & 1);
-              const float before = -*ref;
+              const float before = -sm.refs[r];
               const float now =
                   fmaxf(before, fmaxf(fmaxf(sm.red[0][r], sm.red[1][r]), fmaxf(sm.red[2][r], sm.red[3][r])) - kShift);
               sm.fac[r] = now == before ? 1.0f : ex2(before - now);
-              *ref = -now;
+              if (before == before) sm.refs[r] = -now;  // (a NaN row stays one)
             }
             group_sync(group);
             if (t > p.tile0) {
@@ -636,7 +692,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             }
           }
           // weights: two 8-bit pieces each, 16 rows of a token side by side
-          if (n >= C::PB && !fail) fail = !bar_wait(&sm.pv_done[n % C::PB], (n / C::PB - 1) & 1, gave_up);
+          if (C::PB == 1 && n > 0 && !fail) fail = !bar_wait(&sm.pv_done[0], (n - 1) & 1, gave_up);
           uint8_t* dst = sp + (n % C::PB) * C::kPBytes + token * 16;
 #pragma unroll
           for (int c = 0; c < RT; c += 16) {
@@ -704,7 +760,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         }
         soft_sync();
         if (tid < NR && row_of(tid) < p.nrows) {
-          const float ref = m > 0 ? -reinterpret_cast<const float*>(&sm.rowtab[tid >> 1])[2 + (tid & 1)] : kNoRef;
+          const float ref = m > 0 ? -sm.refs[tid] : kNoRef;
           float s = sm.red[0][tid] + sm.red[1][tid] + sm.red[2][tid] + sm.red[3][tid];
           if (fail) s = __uint_as_float(0x7fc00000u);
           if (p.whole()) {
