@@ -19,7 +19,7 @@ const void* stream_f32_k();
 const void* stream_bf16_k();
 
 // the tensor-core attention over the paged cache for head size D (64, 128) and up
-// to NR rows (16, 32, 48, 64), and its shared memory
+// to NR rows (16, 32, 48), and its shared memory
 const void* kv_mma(int D, int NR, int* smem_bytes);
 // adds n to the kernels that spec_launch_count reports (spec_verify.cu)
 void count_launches(int n);

@@ -22,7 +22,7 @@ constexpr int kGenCtas = kSMs * 4;
 constexpr int kMmaCtas = kSMs * 2;
 // What an item costs beside its tiles, in tiles.
 constexpr int kGenOverhead = 1;
-constexpr int kMmaOverhead = 3;
+constexpr int kMmaOverhead = 4;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -113,7 +113,7 @@ constexpr size_t kPartCounters = 64 * 1024;
 AttnPlan plan_attention(const spec_kv_cache* c, const spec_kv_params* p, bool mma) {
   AttnPlan pl;
   const int64_t rows = static_cast<int64_t>(p->T) * (p->Hq / c->Hkv);
-  const int most = mma ? 64 : kGenRows;
+  const int most = mma ? kMmaRows : kGenRows;
   pl.nrt = static_cast<int>((rows + most - 1) / most);
   // row tiles of equal size, rounded up to what the kernel takes
   pl.rows = mma ? static_cast<int>((rows + pl.nrt - 1) / pl.nrt + 15) / 16 * 16 : kGenRows;
@@ -232,7 +232,7 @@ spec_status launch_mma(const KvArgs& args, const spec_kv_cache* c, const MapOrde
   maps.at_page = order.at_page;
   int smem = 0;
   const void* fn = specv_units::kv_mma(a.D, a.rows, &smem);
-  if (!fn || !allow_smem(fn, (a.D == 128 ? 4 : 0) + a.rows / 16 - 1, smem)) return SPEC_ERR_CUDA;
+  if (!fn || !allow_smem(fn, (a.D == 128 ? 4 : 0) + a.rows / 16, smem)) return SPEC_ERR_CUDA;
   void* params[] = {&a, &maps};
   if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kMmaThreads), params, smem, st) != cudaSuccess)
     return SPEC_ERR_CUDA;

@@ -15,7 +15,6 @@ const void* of_rows(int NR, int* smem_bytes) {
     case 16: return entry<D, 16>(smem_bytes);
     case 32: return entry<D, 32>(smem_bytes);
     case 48: return entry<D, 48>(smem_bytes);
-    case 64: return entry<D, 64>(smem_bytes);
   }
   return nullptr;
 }
