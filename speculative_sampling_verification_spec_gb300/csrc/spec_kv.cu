@@ -88,6 +88,23 @@ void fill_cache(const spec_kv_cache* c, const spec_kv_params* p, KvArgs& a) {
   a.o_head = p->o_head_stride;
 }
 
+// All kernels of the cache are programmatic dependent launches: see start_dependents.
+spec_status launch(const void* fn, int64_t grid, int threads, int smem, void* stream, void** args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) return SPEC_ERR_CUDA;
+  specv_units::count_launches(1);
+  return SPEC_OK;
+}
+
 template <typename E, int PC, bool WARP>
 const void* append_ptr() {
   return reinterpret_cast<const void*>(&spec_kv_append_kernel<E, PC, WARP>);
@@ -217,9 +234,7 @@ spec_status launch_general(const KvArgs& args, bool f32, int grid, cudaStream_t 
                        : reinterpret_cast<const void*>(&spec_kv_attention_kernel<__nv_bfloat16>);
   const int smem = gen_smem_bytes(a.D);
   if (!allow_smem(fn, f32 ? 8 : 9, smem)) return SPEC_ERR_CUDA;
-  if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kGenThreads), params, smem, st) != cudaSuccess)
-    return SPEC_ERR_CUDA;
-  return SPEC_OK;
+  return launch(fn, grid, kGenThreads, smem, st, params);
 }
 
 spec_status launch_mma(const KvArgs& args, const spec_kv_cache* c, const MapOrder& order, int grid, cudaStream_t st) {
@@ -234,9 +249,7 @@ spec_status launch_mma(const KvArgs& args, const spec_kv_cache* c, const MapOrde
   const void* fn = specv_units::kv_mma(a.D, a.rows, &smem);
   if (!fn || !allow_smem(fn, (a.D == 128 ? 4 : 0) + a.rows / 16, smem)) return SPEC_ERR_CUDA;
   void* params[] = {&a, &maps};
-  if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kMmaThreads), params, smem, st) != cudaSuccess)
-    return SPEC_ERR_CUDA;
-  return SPEC_OK;
+  return launch(fn, grid, kMmaThreads, smem, st, params);
 }
 
 }  // namespace
@@ -312,11 +325,7 @@ spec_status spec_kv_append(const void* q, const void* k, const void* v, const fl
   if (g.unit_blocks + q_blocks > INT_MAX) return SPEC_ERR_UNSUPPORTED;
   const void* fn = p->dtype == SPEC_F32 ? append_fn<float>(vec, warp) : append_fn<__nv_bfloat16>(vec, warp);
   void* args[] = {&g};
-  if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(g.unit_blocks + q_blocks)), dim3(threads), args, 0,
-                       static_cast<cudaStream_t>(p->stream)) != cudaSuccess)
-    return SPEC_ERR_CUDA;
-  specv_units::count_launches(1);
-  return SPEC_OK;
+  return launch(fn, g.unit_blocks + q_blocks, threads, 0, p->stream, args);
 }
 
 size_t spec_kv_attention_workspace_size(const spec_kv_cache* cache, const spec_kv_params* params) {
@@ -371,25 +380,11 @@ spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const s
   const int grid = pl.nranges * pl.nrt;
   s = mma ? launch_mma(a, cache, order, grid, st) : launch_general(a, f32, grid, st);
   if (s != SPEC_OK) return s;
-  specv_units::count_launches(1);
   if (pl.join_here || pl.nranges == 1) return SPEC_OK;
-  // the join kernel is a programmatic dependent launch: it may be scheduled while
-  // the last ranges finish, and waits before it reads or writes
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.T * a.Hq));
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   void* args[] = {&a};
   const void* jn = f32 ? reinterpret_cast<const void*>(&spec_kv_join_kernel<float>)
                        : reinterpret_cast<const void*>(&spec_kv_join_kernel<__nv_bfloat16>);
-  if (cudaLaunchKernelExC(&cfg, jn, args) != cudaSuccess) return SPEC_ERR_CUDA;
-  specv_units::count_launches(1);
-  return SPEC_OK;
+  return launch(jn, static_cast<int64_t>(a.B) * a.T * a.Hq, 32 * kJoinWarps, 0, st, args);
 }
 
 }  // extern "C"

@@ -395,6 +395,8 @@ __global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads,
   constexpr int nt = WARP ? kAppendWarpThreads : kAppendCtaThreads;
   const KvArgs& a = g.a;
   const int tid = threadIdx.x;
+  start_dependents();
+  wait_for_grid();
   if (blockIdx.x < static_cast<unsigned>(g.unit_blocks)) {
     __shared__ __align__(16) uint32_t red[WARP ? 4 : kAppendCtaThreads / 32];
     if constexpr (WARP) {

@@ -167,6 +167,8 @@ __global__ void __launch_bounds__(kGenThreads) spec_kv_attention_kernel(const __
   __shared__ float sfac[kGenRows], sl[kGenRows], sm[kGenRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int range = blockIdx.x / a.nrt, rt = blockIdx.x - range * a.nrt;
+  start_dependents();
+  wait_for_grid();
   make_plan_range<kGenThreads>(a, range, &plan, scratch, blockIdx.x == 0 ? a.prefix : nullptr);
   fill_empty<E>(a, tid, kGenThreads);
   if (plan.w0 >= plan.w1) return;
@@ -373,7 +375,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) spec_kv_join_kernel(const __g
   const int hq = static_cast<int>(row % a.Hq);
   const int64_t bt = row / a.Hq;
   const int b = static_cast<int>(bt / a.T), t = static_cast<int>(bt - static_cast<int64_t>(b) * a.T);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the ranges' results are complete
+  start_dependents();
+  wait_for_grid();  // the ranges' results are complete
   const SeqSpan s = seq_span(a, b);
   if (s.bad || t >= s.n) return;
   const int per = max(1, (a.prefix[a.B] + a.nranges - 1) / a.nranges);

@@ -66,6 +66,13 @@ __device__ __forceinline__ void report(int32_t* status, int code) {
   if (status) atomicCAS(status, 0, code);
 }
 
+// Programmatic dependent launches.  A kernel of the cache may be scheduled while
+// the one before it in the stream runs out; nothing of global memory is read or
+// written before wait_for_grid (which every CTA passes), and the next such kernel
+// may be scheduled once every CTA has called start_dependents.
+__device__ __forceinline__ void start_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_float(float x, float* p) { *p = x; }
@@ -108,7 +115,7 @@ struct RangePlan {
   int b, off;  // sequence that holds w0, and w0's offset in its places (all heads)
 };
 
-// All threads of the CTA (NT of them) take part; `plan` and `scratch` are in
+// All threads of the CTA (NT of them) take part, once; `plan` and `scratch` are in
 // shared memory.  When prefix is given, it gets the places before each sequence.
 template <int NT>
 __device__ void make_plan_range(const KvArgs& a, int range, RangePlan* plan, int* scratch, int32_t* prefix) {
@@ -123,7 +130,6 @@ __device__ void make_plan_range(const KvArgs& a, int range, RangePlan* plan, int
     const int o = __shfl_up_sync(kFull, inc, d);
     if (lane >= d) inc += o;
   }
-  __syncthreads();  // the plan of the range before has been read
   if (lane == 31) scratch[warp] = inc;
   __syncthreads();
   int before = inc - mine, total = 0;

@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   }
   if (warp == 9) tmem_alloc(&sm.tmem, C::kCols);
   const int range = blockIdx.x / a.nrt, rt = blockIdx.x - range * a.nrt;
-  asm volatile("griddepcontrol.launch_dependents;");
+  start_dependents();
+  wait_for_grid();
   tc_fence_before();
   make_plan_range<kMmaThreads>(a, range, &sm.plan, sm.scratch, blockIdx.x == 0 ? a.prefix : nullptr);
   tc_fence_after();
@@ -325,15 +326,15 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           if (n >= C::KS) ok = bar_wait(&sm.k_empty[ks], (n / C::KS - 1) & 1, gave_up);
           ok = __all_sync(kFull, ok);
           if (!ok) break;
+          if (has)
+            tma_load_4d(sk + ks * C::kTileBytes + mine * page_bytes, &maps.k, 0, y, z, w, &sm.k_full[ks]);
+          // the tile's scales come with its keys: the arrival that the copies' bytes wait for is after them
           if (mine >= 0 && mine < np) {
             const float v = sc.y < 7.8886090522101181e-31f ? 7.8886090522101181e-31f : sc.y;  // 2^-100
             sm.scales[n % kScaleRing][mine] = make_float4(sc.x, log2f(v), 1.0f / v, 0.0f);
           }
-          __syncwarp();  // the scales are written: they come with the keys
-          if (lane == 0) bar_arrive_expect(&sm.k_full[ks], cnt * page_bytes);
           __syncwarp();
-          if (has)
-            tma_load_4d(sk + ks * C::kTileBytes + mine * page_bytes, &maps.k, 0, y, z, w, &sm.k_full[ks]);
+          if (lane == 0) bar_arrive_expect(&sm.k_full[ks], cnt * page_bytes);
           if (n >= C::VS) ok = bar_wait(&sm.v_empty[vs], (n / C::VS - 1) & 1, gave_up);
           ok = __all_sync(kFull, ok);
           if (!ok) {
