@@ -19,8 +19,8 @@ const void* stream_f32_k();
 const void* stream_bf16_k();
 
 // the tensor-core attention over the paged cache for head size D (64, 128) and up
-// to NR rows (16, 32, 48), and its shared memory
-const void* kv_mma(int D, int NR, int* smem_bytes);
+// to `rows` rows (at most 48) a row tile, and its shared memory
+const void* kv_mma(int D, int rows, int* smem_bytes);
 // adds n to the kernels that spec_launch_count reports (spec_verify.cu)
 void count_launches(int n);
 

@@ -132,8 +132,7 @@ AttnPlan plan_attention(const spec_kv_cache* c, const spec_kv_params* p, bool mm
   const int64_t rows = static_cast<int64_t>(p->T) * (p->Hq / c->Hkv);
   const int most = mma ? kMmaRows : kGenRows;
   pl.nrt = static_cast<int>((rows + most - 1) / most);
-  // row tiles of equal size, rounded up to what the kernel takes
-  pl.rows = mma ? static_cast<int>((rows + pl.nrt - 1) / pl.nrt + 15) / 16 * 16 : kGenRows;
+  pl.rows = mma ? static_cast<int>((rows + pl.nrt - 1) / pl.nrt) : kGenRows;  // row tiles of equal size
   pl.slot_rows = pl.rows;
   pl.nranges = std::max(1, (mma ? kMmaCtas : kGenCtas) / pl.nrt);
   // with one range nothing is shared, so no partial results
@@ -247,7 +246,8 @@ spec_status launch_mma(const KvArgs& args, const spec_kv_cache* c, const MapOrde
   maps.at_page = order.at_page;
   int smem = 0;
   const void* fn = specv_units::kv_mma(a.D, a.rows, &smem);
-  if (!fn || !allow_smem(fn, (a.D == 128 ? 4 : 0) + a.rows / 16, smem)) return SPEC_ERR_CUDA;
+  const int kind = a.rows <= 16 ? 0 : a.rows <= 32 ? 1 : a.rows <= 40 ? 2 : 3;
+  if (!fn || !allow_smem(fn, (a.D == 128 ? 4 : 0) + kind, smem)) return SPEC_ERR_CUDA;
   void* params[] = {&a, &maps};
   return launch(fn, grid, kMmaThreads, smem, st, params);
 }

@@ -49,7 +49,9 @@ namespace spec_kv_detail {
 constexpr int kMmaRows = 48;
 constexpr int kMmaThreads = 320;
 constexpr int kSoftThreads = 256;  // two groups of 128, a token a thread
+constexpr int kPieceRing = 8;       // pieces; at most two of a CTA's have no tiles
 constexpr int kScaleRing = 8;       // tiles of scales; a loader is never this far ahead of the softmax
+constexpr uint32_t kUnset = 0x80000000u;  // bits of -0: scores are taken as they are
 constexpr int kNear = 4;            // log2 of how far apart rows with one exponent may be
 constexpr int kSlack = 5;           // log2 of how far weights may pass the reference
 constexpr float kShift = 8 - kSlack;  // a raised reference is kShift below the largest score: weights stay within 2^8 < 448
@@ -77,20 +79,22 @@ template <int D, int NR>
 struct MmaSmall {
   using C = MmaCfg<D, NR>;
   uint64_t k_full[C::KS], k_empty[C::KS], v_full[C::VS], v_empty[C::VS];
-  uint64_t s_full[2], p_full[C::PB], pv_done[C::PB], q_full, drain;
-  alignas(16) float refs[NR];     // negated references of the rows
+  uint64_t s_full[2], p_full[C::PB], pv_done[C::PB], piece_full[kPieceRing], q_full, drain;
+  alignas(16) float refs[NR];     // negated references of the rows; kUnset: none yet
   alignas(16) float factor[NR];   // of the scores, where rows have exponents of their own
   uint32_t q_top, q_least;        // largest and least of the rows' largest magnitudes
   float4 scales[kScaleRing][kTile / 16];  // of a page: key scale; value scale's log2 and reciprocal
   int64_t out_at[NR];     // element of the output (of lse for `lse_at`) where a row begins
   int64_t lse_at[NR];
-  alignas(16) float fac[NR];
+  alignas(16) float fac[NR];      // by which a rescaling multiplies, and what it raises references by
+  alignas(16) float up[NR];
   alignas(16) float red[4][NR];
   int pos[NR];
   RangePlan plan;
   int scratch[kMmaThreads / 32];
   uint32_t tmem;
   int gave_up, last;
+  Piece pieces[kPieceRing];  // from the loader to the other roles; b < 0: no more
 };
 
 template <int D, int NR>
@@ -220,7 +224,37 @@ static __device__ __noinline__ RawChunk<__nv_bfloat16, 8> gather16(const __nv_bf
   return r;
 }
 
-template <int D, int NR>
+// A wait of the CTA ran out: the range's pieces from the `done`th on become NaN.
+static __device__ __noinline__ void abandon(const KvArgs& a, const RangePlan& plan, int range, int rt, int done,
+                                            int* last) {
+  const int tid = threadIdx.x;  // of the softmax warps
+  const float nan = __uint_as_float(0x7fc00000u);
+  if (tid == 0) report(a.status, SPEC_ERR_TIMEOUT);
+  Walk walk = walk_begin(plan, range, rt);
+  Piece p;
+  for (int i = 0; walk_next(a, walk, p); ++i) {
+    if (i < done) continue;
+    for (int r = tid >> 5; r < p.nrows; r += kSoftThreads / 32) {
+      const int gr = p.row0 + r, t = gr / a.G, hq = p.h * a.G + gr - t * a.G;
+      if (!p.whole()) {
+        if ((tid & 31) == 0) a.part_ml[static_cast<int64_t>(p.slot) * a.slot_rows + r] = make_float2(kNoRef, nan);
+        continue;
+      }
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + p.b * a.o_seq + t * a.o_tok + hq * a.o_head;
+      for (int d = tid & 31; d < a.D; d += 32) from_float(nan, o + d);
+      if (a.lse && (tid & 31) == 0) a.lse[(static_cast<int64_t>(p.b) * a.T + t) * a.Hq + hq] = nan;
+    }
+    if (a.join_here && !p.whole()) {
+      soft_sync();
+      if (tid == 0) *last = last_of_item(a, p, rt);
+      soft_sync();
+      if (*last) join_item<__nv_bfloat16>(a, p, rt, tid >> 5, kSoftThreads / 32);
+    }
+  }
+}
+
+// RU: rows that a softmax group keeps in registers, at most NR / 2
+template <int D, int NR, int RU>
 __global__ void __launch_bounds__(kMmaThreads, 2)
     spec_kv_attention_mma_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ MmaMaps maps) {
   using C = MmaCfg<D, NR>;
@@ -248,6 +282,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       bar_init(&sm.p_full[i], kSoftThreads / 32);
       bar_init(&sm.pv_done[i], 1);
     }
+    for (int i = 0; i < kPieceRing; ++i) bar_init(&sm.piece_full[i], 1);
     bar_init(&sm.q_full, 1);
     bar_init(&sm.drain, 1);
     sm.gave_up = 0;
@@ -268,9 +303,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   volatile int* const gave_up = &sm.gave_up;
 
   if (sm.plan.w0 < sm.plan.w1) {
-    Walk walk = walk_begin(sm.plan, range, rt);
-    Piece p;
-    int n = 0;  // tiles so far, over all pieces
+    int n = 0;       // tiles so far, over all pieces
+    int pieces = 0;  // pieces so far
 
     if (warp == 8) {
       // ---------------------------------------------------------------- loads
@@ -278,7 +312,16 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       const uint32_t page_bytes = static_cast<uint32_t>(D) << a.log_page;
       bool ok = true;
       int nk = -1;
-      while (ok && walk_next(a, walk, p)) {
+      Piece p;
+      Walk walk = walk_begin(sm.plan, range, rt);
+      while (ok) {
+        if (!walk_next(a, walk, p)) p.b = -1;
+        if (lane == 0) {
+          sm.pieces[pieces % kPieceRing] = p;
+          bar_arrive(&sm.piece_full[pieces % kPieceRing]);
+        }
+        ++pieces;
+        if (p.b < 0) break;
         const int end = p.L + p.n;
         const int first = p.tile0 * np, last = min(p.tile1 * np, (end + (1 << a.log_page) - 1) >> a.log_page);
         // 32 pages at a time, one a lane: numbers, then scales; the next 32 are under way
@@ -364,7 +407,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         constexpr uint32_t kDescS = instr_desc(128, NR, false, false);
         constexpr uint32_t kDescO = instr_desc(128, 2 * NR, true, true);
         bool ok = true;
-        int piece = 0;
+        int queries = 0;
         const auto scores = [&](int i) {
           const int st = i % C::KS;
           ok = ok && bar_wait(&sm.k_full[st], (i / C::KS) & 1, gave_up);
@@ -382,11 +425,16 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           mma_commit(&sm.s_full[i & 1]);
           bar_arrive(&sm.s_full[i & 1]);  // passes the loader's scales on, as a commit alone need not
         };
-        while (ok && walk_next(a, walk, p)) {
+        for (;; ++pieces) {
+          ok = ok && bar_wait(&sm.piece_full[pieces % kPieceRing], (pieces / kPieceRing) & 1, gave_up);
+          if (!ok) break;
+          const Piece& p = sm.pieces[pieces % kPieceRing];
+          if (p.b < 0) break;
           const int m = p.tile1 - p.tile0;
           if (m == 0) continue;
-          ok = bar_wait(&sm.q_full, piece & 1, gave_up);
-          ++piece;
+          ok = bar_wait(&sm.q_full, queries & 1, gave_up);
+          if (!ok) break;
+          ++queries;
           scores(n);
           if (m > 1) scores(n + 1);
           for (int i = 0; ok && i < m; ++i, ++n) {
@@ -419,20 +467,27 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;  // tensor memory lanes of this warp
       const uint32_t tO = tm + lanes + 2 * NR + r_base;                     // first pieces; the second NR further
       bool fail = false;
-      while (walk_next(a, walk, p)) {
-        const int m = p.tile1 - p.tile0;
-        // rows of the first group (the second has the rest), and of this one in fours
-        const int half = min(RT, (p.nrows + 7) / 8 * 4);
-        const int mine = group == 0 ? min(half, p.nrows) : p.nrows - half;
-        const int fours = max(0, (mine + 3) / 4 * 4);
+      for (;; ++pieces) {
+        // the piece stays in shared memory, out of the registers that the loop over the tiles needs
+        const Piece& p = sm.pieces[pieces % kPieceRing];
+        const auto half_of = [&]() { return min(RU, (p.nrows + 7) / 8 * 4); };  // rows of the first group
+        const auto rows_mine = [&]() { return group == 0 ? min(half_of(), p.nrows) : p.nrows - half_of(); };
         const auto row_of = [&](int col) {  // of a column: nrows and more for none
-          const int r = col < RT ? col : col - RT + half;
-          return col < RT ? (col < half ? r : p.nrows) : r;
+          const int half = half_of();
+          return col < RT ? (col < half ? col : p.nrows) : col - RT + half;
         };
+        if (!fail) fail = !bar_wait(&sm.piece_full[pieces % kPieceRing], (pieces / kPieceRing) & 1, gave_up);
+        if (tid == 0) {
+          sm.q_top = 0;
+          sm.q_least = 0x7f7fffffu;
+        }
+        fail = soft_any(fail);  // the piece before has been written out
+        if (fail || p.b < 0) break;
+        const int m = p.tile1 - p.tile0;
+        const int fours = max(0, (rows_mine() + 3) / 4 * 4);  // this group's rows, in fours
         float l[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) l[r] = 0.0f;
-        soft_sync();  // the piece before has been written out
         if (tid < NR) {
           const int r = row_of(tid);
           const bool row = r < p.nrows;
@@ -441,20 +496,15 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           sm.out_at[tid] = p.b * a.o_seq + t * a.o_tok + (p.h * a.G + g) * a.o_head;
           sm.lse_at[tid] = (static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g;
         }
-        if (tid == 0) {
-          sm.q_top = 0;
-          sm.q_least = 0x7f7fffffu;
-        }
         bool one_factor = true;
         float factor = 0.0f;
-        if (m > 0 && !fail) {
+        if (m > 0) {
           // queries: 16 channels a thread
           constexpr int kPer = D / 16;                 // threads a row
           constexpr int kStep = kSoftThreads / kPer;   // rows at a time
           constexpr int kTimes = (NR + kStep - 1) / kStep;
           RawChunk<__nv_bfloat16, 8> raw[kTimes];
           uint32_t tops[kTimes];  // bits of a row's largest magnitude (NaN above infinity)
-          soft_sync();            // q_top and q_least are set
 #pragma unroll
           for (int i = 0; i < kTimes; ++i) {
             const int col = i * kStep + tid / kPer, c = tid % kPer, r = row_of(col);
@@ -531,7 +581,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
               *reinterpret_cast<uint4*>(dst + C::kQBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
               if (c == 0) {
                 // a row that is not there has a reference no score passes
-                sm.refs[col] = row_of(col) >= p.nrows ? kNoRef : fin ? -kNoRef : __uint_as_float(0x7fc00000u);
+                sm.refs[col] = row_of(col) >= p.nrows ? kNoRef : __uint_as_float(fin ? kUnset : 0x7fc00000u);
                 sm.factor[col] = s;
               }
             }
@@ -540,23 +590,28 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           soft_sync();
           if (tid == 0) bar_arrive(&sm.q_full);
         }
-        const int end = p.L + p.n;
-        const int pos_lo = p.L + p.row0 / a.G, pos_hi = p.L + (p.row0 + p.nrows - 1) / a.G;
-        for (int t = p.tile0; t < p.tile1; ++t, ++n) {
+        const int tile0 = p.tile0, tile1 = p.tile1;
+        const int pos_hi = p.L + (p.row0 + p.nrows - 1) / a.G;
+        // tiles that some row sees only in part: from t_edge on, and up to t_win; and the tile from
+        // which on every row has seen a token
+        const int t_edge = (p.L + p.row0 / a.G + 1) / kTile;
+        const int t_win = a.window > 0 && pos_hi >= a.window ? (pos_hi - a.window) / kTile : -1;
+        const int t_unset = max(tile0, a.window > 0 ? (pos_hi + 1 - a.window) / kTile : 0);
+        for (int t = tile0; t < tile1; ++t, ++n) {
           const int j = t * kTile + token;
           // scores of this tile; they come with its scales, and with the end of the products two
           // tiles back (issued before them): with two buffers of weights this one's is free
           if (!fail) fail = !bar_wait(&sm.s_full[n & 1], (n >> 1) & 1, gave_up);
           tc_fence_after();
           float4 sc = sm.scales[n % kScaleRing][token >> a.log_page];
-          // tiles that some row sees only in part
-          const bool edge = t * kTile + kTile - 1 > pos_lo || (a.window > 0 && t * kTile <= pos_hi - a.window);
+          const bool edge = t >= t_edge || t <= t_win;
           bool poison = false;
           if (edge) {
             // no row may be touched by what it does not see: values that are not to be read are
             // zero, NaN codes and scales of a token that some rows see go to those rows' sums
-            const bool all_see = j <= pos_lo && (a.window <= 0 || j > pos_hi - a.window);
-            const bool gone = j >= end;
+            const int first = p.L + p.row0 / a.G, last = p.L + (p.row0 + p.nrows - 1) / a.G;
+            const bool all_see = j <= first && (a.window <= 0 || j > last - a.window);
+            const bool gone = j >= p.L + p.n;
             const bool bad_scale = !(sc.x == sc.x && sc.z == sc.z);
             uint8_t* row = sv + (n % C::VS) * C::kTileBytes + token * D;  // whole rows: the swizzle stays inside
             if (!fail) fail = !bar_wait(&sm.v_full[n % C::VS], (n / C::VS) & 1, gave_up);
@@ -581,77 +636,80 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             const int q = sm.pos[r_base + r];
             return j <= q && (a.window <= 0 || j > q - a.window);
           };
-          // scores of rows c.. in log2 units against their references
-          const auto against_refs = [&](int c, float* x) {
-            if (!one_factor) {
-              const float4 f = *reinterpret_cast<const float4*>(&sm.factor[r_base + c]);
-              x[0] *= f.x;
-              x[1] *= f.y;
-              x[2] *= f.z;
-              x[3] *= f.w;
-            }
-            const float4 ref = *reinterpret_cast<const float4*>(&sm.refs[r_base + c]);
-            unpack2(fma2(pack2(x[0], x[1]), ks2, add2(lv2, pack2(ref.x, ref.y))), x[0], x[1]);
-            unpack2(fma2(pack2(x[2], x[3]), ks2, add2(lv2, pack2(ref.z, ref.w))), x[2], x[3]);
-            if (edge) {
-#pragma unroll
-              for (int i = 0; i < CH; ++i) x[i] = sees(c + i) ? x[i] : -INFINITY;
-            }
-          };
           float x[RT];
-          while (true) {
-            float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < RT; c += 8) tmem_ld<8>(tS + c, &x[c]);
-            tmem_wait_ld();
+          for (int c = 0; c < RT; c += 8) tmem_ld<8>(tS + c, &x[c]);
+          tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < RT; c += 8) tmem_tie<8>(&x[c]);
+          for (int c = 0; c < RT; c += 8) tmem_tie<8>(&x[c]);
+          if (!one_factor) {
 #pragma unroll
-            for (int c = 0; c < RT; c += CH) {
+            for (int r = 0; r < RU; ++r) x[r] *= sm.factor[r_base + r];
+          }
+          // scores in log2 units against the rows' references
+#pragma unroll
+          for (int c = 0; c < RU; c += CH) {
+            if (c < fours) {
+              const float4 ref = *reinterpret_cast<const float4*>(&sm.refs[r_base + c]);
+              unpack2(fma2(pack2(x[c], x[c + 1]), ks2, add2(lv2, pack2(ref.x, ref.y))), x[c], x[c + 1]);
+              unpack2(fma2(pack2(x[c + 2], x[c + 3]), ks2, add2(lv2, pack2(ref.z, ref.w))), x[c + 2], x[c + 3]);
+            }
+          }
+          if (edge) {
+#pragma unroll
+            for (int r = 0; r < RU; ++r) x[r] = sees(r) ? x[r] : -INFINITY;
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < RU; c += CH)
+            if (c < fours) top = fmaxf(fmaxf(top, fmaxf(x[c], x[c + 1])), fmaxf(x[c + 2], x[c + 3]));
+          // would some weight leave the 8-bit range, or has some row no reference yet?
+          if (group_any(group, top > 8.0f || t <= t_unset)) {
+            float most = -INFINITY;  // of row `lane`, over the warp's tokens
+#pragma unroll
+            for (int c = 0; c < RU; c += CH) {
               if (c < fours) {
-                against_refs(c, &x[c]);
-                top = fmaxf(fmaxf(top, fmaxf(x[c], x[c + 1])), fmaxf(x[c + 2], x[c + 3]));
-              }
-            }
-            // would some weight leave the 8-bit range?
-            if (!group_any(group, top > 8.0f)) break;
-            // raise the references to the largest score so far
-#pragma unroll 1
-            for (int c = 0; c < fours; c += 8) {
-              float y[8];
-              tmem_ld<8>(tS + c, y);
-              tmem_wait_ld();
-              tmem_tie<8>(y);
-              float most = -INFINITY;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float u = fmaf(one_factor ? y[i] : y[i] * sm.factor[r_base + c + i], ks, sc.y);
-                if (edge && !sees(c + i)) u = -INFINITY;
-                u = u == u ? u : -INFINITY;
-                const float w = of_order(__reduce_max_sync(kFull, order_of(u)));
-                if (lane == i) most = w;
+                for (int i = 0; i < CH; ++i) {
+                  const float w = of_order(__reduce_max_sync(kFull, order_of(x[c + i])));
+                  if (lane == c + i) most = w;
+                }
               }
-              if (lane < 8) sm.red[warp & 3][r_base + c + lane] = most;
             }
+            if (lane < RT) sm.red[warp & 3][r_base + lane] = most;
             group_sync(group);
             if (token < fours) {
               const int r = r_base + token;
-              const float before = -sm.refs[r];
-              const float now =
-                  fmaxf(before, fmaxf(fmaxf(sm.red[0][r], sm.red[1][r]), fmaxf(sm.red[2][r], sm.red[3][r])) - kShift);
-              sm.fac[r] = now == before ? 1.0f : ex2(before - now);
-              if (before == before) sm.refs[r] = -now;  // (a NaN row stays one)
+              const float now = fmaxf(fmaxf(sm.red[0][r], sm.red[1][r]), fmaxf(sm.red[2][r], sm.red[3][r])) - kShift;
+              const float ref = sm.refs[r];
+              const bool unset = __float_as_uint(ref) == kUnset;
+              // raised by: nothing for a row that no token of this tile belongs to
+              const float up = unset ? (now == -INFINITY ? 0.0f : now) : fmaxf(now, 0.0f);
+              sm.up[r] = up;
+              sm.fac[r] = unset ? 1.0f : ex2(-up);
+              // 0 - x is never the mark of an unset reference
+              sm.refs[r] = unset && now == -INFINITY ? ref : (unset ? 0.0f : ref) - up;
             }
             group_sync(group);
-            if (t > p.tile0) {
 #pragma unroll
-              for (int r = 0; r < RT; r += 4) {
-                if (r < fours) {
-                  const float4 f = *reinterpret_cast<const float4*>(&sm.fac[r_base + r]);
-                  l[r] *= f.x;
-                  l[r + 1] *= f.y;
-                  l[r + 2] *= f.z;
-                  l[r + 3] *= f.w;
+            for (int c = 0; c < RU; c += CH) {
+              if (c < fours) {
+                const float4 u = *reinterpret_cast<const float4*>(&sm.up[r_base + c]);
+                x[c] -= u.x;
+                x[c + 1] -= u.y;
+                x[c + 2] -= u.z;
+                x[c + 3] -= u.w;
+              }
+            }
+            if (t > tile0) {
+#pragma unroll
+              for (int c = 0; c < RU; c += CH) {
+                if (c < fours) {
+                  const float4 f = *reinterpret_cast<const float4*>(&sm.fac[r_base + c]);
+                  l[c] *= f.x;
+                  l[c + 1] *= f.y;
+                  l[c + 2] *= f.z;
+                  l[c + 3] *= f.w;
                 }
               }
               if (!fail) fail = !bar_wait(&sm.pv_done[(n - 1) % C::PB], ((n - 1) / C::PB) & 1, gave_up);
@@ -684,7 +742,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < 16; i += CH) {
-              if (i < n16 && c + i < fours) {
+              if (i < n16 && c + i < RU && c + i < fours) {
                 uint32_t h[2], d[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -715,7 +773,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           }
           if (poison) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < RU; ++r)
               if (sees(r)) l[r] = __uint_as_float(0x7fc00000u);
           }
           fence_async();
@@ -736,7 +794,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         }
         soft_sync();
         if (tid < NR && row_of(tid) < p.nrows) {
-          const float ref = m > 0 ? -sm.refs[tid] : kNoRef;
+          const float ref = m > 0 && __float_as_uint(sm.refs[tid]) != kUnset ? -sm.refs[tid] : kNoRef;
           float s = sm.red[0][tid] + sm.red[1][tid] + sm.red[2][tid] + sm.red[3][tid];
           if (fail) s = __uint_as_float(0x7fc00000u);
           if (p.whole()) {
@@ -748,7 +806,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         }
         if (p.whole()) soft_sync();
         if (m > 0 && (warp & 3) * 32 < D) {
-          const int row0 = group == 0 ? 0 : half;
+          const int row0 = group == 0 ? 0 : half_of(), mine = rows_mine();
           float* part = a.part_o + (static_cast<int64_t>(p.slot) * a.slot_rows + row0) * D + token;
 #pragma unroll 1
           for (int c = 0; c < fours; c += 8) {
@@ -778,7 +836,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           if (sm.last) join_item<__nv_bfloat16>(a, p, rt, warp, kSoftThreads / 32);
         }
       }
-      if (fail && tid == 0) report(a.status, SPEC_ERR_TIMEOUT);
+      if (fail) abandon(a, sm.plan, range, rt, pieces, &sm.last);
     }
   }
   fill_empty<__nv_bfloat16>(a, tid, kMmaThreads);
