@@ -46,7 +46,7 @@ spec_status check_cache(const spec_kv_cache* c, const spec_kv_params* p) {
       c->token_stride % 16 || c->scale_page_stride < 0 || c->scale_head_stride < 0)
     return SPEC_ERR_INVALID_ARG;
   if (!p->page_table || !p->seq_lens || p->max_pages < 1 || p->table_stride < 0) return SPEC_ERR_INVALID_ARG;
-  const int64_t tiles = (static_cast<int64_t>(p->max_pages) * c->page_size + kTile - 1) / kTile;
+  const int64_t tiles = ((static_cast<int64_t>(p->max_pages) * c->page_size) >> kGenLogTile) + 1;
   // positions, and tiles of the whole call, are counted in 32 bits
   if (static_cast<int64_t>(p->max_pages) * c->page_size > INT_MAX - kTile) return SPEC_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(std::max(1, p->B)) * c->Hkv > (int64_t(1) << 30) / (tiles + kMmaOverhead)) return SPEC_ERR_UNSUPPORTED;
@@ -122,8 +122,8 @@ struct AttnPlan {
   size_t off_prefix = 0, off_ml = 0, off_o = 0, ws_bytes = 0;
 };
 
-// Parts of an item that one CTA joins, in bytes.
-constexpr int64_t kJoinBytes = 256 << 10;
+// Bytes of an item's parts that a warp of its last CTA joins, at most.
+constexpr int64_t kJoinBytes = 10 << 10;
 // Workspace bytes kept zero between calls: counters of the items' parts.
 constexpr size_t kPartCounters = 64 * 1024;
 
@@ -132,7 +132,9 @@ AttnPlan plan_attention(const spec_kv_cache* c, const spec_kv_params* p, bool mm
   const int64_t rows = static_cast<int64_t>(p->T) * (p->Hq / c->Hkv);
   const int most = mma ? kMmaRows : kGenRows;
   pl.nrt = static_cast<int>((rows + most - 1) / most);
-  pl.rows = mma ? static_cast<int>((rows + pl.nrt - 1) / pl.nrt) : kGenRows;  // row tiles of equal size
+  // row tiles of equal size; the general kernel's have 4 or 8 rows
+  pl.rows = static_cast<int>((rows + pl.nrt - 1) / pl.nrt);
+  if (!mma) pl.rows = pl.rows <= 4 ? 4 : kGenRows;
   pl.slot_rows = pl.rows;
   pl.nranges = std::max(1, (mma ? kMmaCtas : kGenCtas) / pl.nrt);
   // with one range nothing is shared, so no partial results
@@ -141,7 +143,7 @@ AttnPlan plan_attention(const spec_kv_cache* c, const spec_kv_params* p, bool mm
   // parts of one item, if all sequences are alike); else a kernel over all rows.
   const int64_t items = static_cast<int64_t>(std::max(1, p->B)) * c->Hkv;
   const int64_t parts = (pl.nranges + items - 1) / items;
-  pl.join_here = parts * pl.rows * c->D * 4 <= kJoinBytes;
+  pl.join_here = parts * pl.rows * c->D * 4 <= kJoinBytes * (mma ? kSoftThreads : kGenThreads) / 32;
   const size_t counters = round_up(static_cast<size_t>(p->B) * c->Hkv * pl.nrt * sizeof(int32_t), 256);
   pl.clear = pl.join_here && pl.nranges > 1 && counters > kPartCounters;
   pl.off_prefix = std::max(kPartCounters, counters);
@@ -226,13 +228,22 @@ bool allow_smem(const void* fn, int slot, int bytes) {
   return true;
 }
 
+template <typename E, int MAXD, int ROWS>
+const void* general_ptr() {
+  return reinterpret_cast<const void*>(&spec_kv_attention_kernel<E, MAXD, ROWS>);
+}
+template <typename E>
+const void* general_fn(int D, int rows) {
+  if (rows == 4) return D > 128 ? general_ptr<E, 256, 4>() : general_ptr<E, 128, 4>();
+  return D > 128 ? general_ptr<E, 256, 8>() : general_ptr<E, 128, 8>();
+}
+
 spec_status launch_general(const KvArgs& args, bool f32, int grid, cudaStream_t st) {
   KvArgs a = args;
   void* params[] = {&a};
-  const void* fn = f32 ? reinterpret_cast<const void*>(&spec_kv_attention_kernel<float>)
-                       : reinterpret_cast<const void*>(&spec_kv_attention_kernel<__nv_bfloat16>);
-  const int smem = gen_smem_bytes(a.D);
-  if (!allow_smem(fn, f32 ? 8 : 9, smem)) return SPEC_ERR_CUDA;
+  const void* fn = f32 ? general_fn<float>(a.D, a.rows) : general_fn<__nv_bfloat16>(a.D, a.rows);
+  const int smem = gen_smem_bytes(a.D, a.rows);
+  if (smem > 48 * 1024 && !allow_smem(fn, f32 ? 8 : 9, smem)) return SPEC_ERR_CUDA;
   return launch(fn, grid, kGenThreads, smem, st, params);
 }
 
@@ -362,6 +373,7 @@ spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const s
   a.scale2 = static_cast<float>(static_cast<double>(p->scale) * 1.4426950408889634);
   a.rows = pl.rows;
   a.nrt = pl.nrt;
+  a.log_tile = mma ? 7 : kGenLogTile;
   a.nranges = pl.nranges;
   a.overhead = mma ? kMmaOverhead : kGenOverhead;
   a.join_here = pl.join_here;

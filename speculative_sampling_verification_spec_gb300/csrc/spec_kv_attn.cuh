@@ -148,23 +148,28 @@ __device__ __forceinline__ void fill_empty(const KvArgs& a, int tid, int threads
 }
 
 constexpr int kGenThreads = 128;
-constexpr int kGenRows = 8;    // rows of a row tile
+constexpr int kGenRows = 8;    // rows of a row tile at most
+constexpr int kGenLogTile = 6; // tokens of a tile: short, for latency
 constexpr int kGenSub = 32;    // tokens staged at a time: a lane's token in the scores
 constexpr int kGenMaxD = 256;
-constexpr int gen_smem_bytes(int D) { return 4 * (kGenRows * D + kGenSub * (D + 4)) + kGenSub * D; }
+constexpr int gen_smem_bytes(int D, int rows) { return 4 * (rows * D + kGenSub * (D + 4)) + kGenSub * D; }
 
 // A CTA walks its pieces 32 tokens at a time.  The next 32 tokens' codes are in
 // registers (16-byte loads) while the present ones are worked on.  Scores: lane =
-// token, two rows a warp, so a row's maximum and sum stay in its warp.  Output:
-// thread = channel, eight rows in registers.
-template <typename E>
-__global__ void __launch_bounds__(kGenThreads) spec_kv_attention_kernel(const __grid_constant__ KvArgs a) {
-  constexpr int kVecs = 2 * kGenSub * (kGenMaxD / 16) / kGenThreads;  // 16-byte vectors a thread, keys and values
+// token, a row's maximum and sum stay in its warp.  Output: thread = channel, all
+// rows in registers.
+// MAXD: 128 or 256, the head sizes that the registers are laid out for; ROWS: rows
+// of a row tile, 4 or 8, a fourth of them a warp's.
+template <typename E, int MAXD, int ROWS>
+__global__ void __launch_bounds__(kGenThreads, MAXD == 128 ? 5 : 3)
+    spec_kv_attention_kernel(const __grid_constant__ KvArgs a) {
+  constexpr int kVecs = 2 * kGenSub * (MAXD / 16) / kGenThreads;  // 16-byte vectors a thread, keys and values
+  constexpr int kCh = MAXD / kGenThreads;                         // channels a thread
   __shared__ RangePlan plan;
   __shared__ int scratch[kGenThreads / 32];
-  extern __shared__ __align__(16) uint8_t dyn[];  // gen_smem_bytes(D)
-  __shared__ float sp[kGenRows][kGenSub];
-  __shared__ float sfac[kGenRows], sl[kGenRows], sm[kGenRows];
+  extern __shared__ __align__(16) uint8_t dyn[];  // gen_smem_bytes(D, ROWS)
+  __shared__ __align__(16) float sp[ROWS][kGenSub];
+  __shared__ float sfac[ROWS], sl[ROWS], sm[ROWS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int range = blockIdx.x / a.nrt, rt = blockIdx.x - range * a.nrt;
   start_dependents();
@@ -173,16 +178,16 @@ __global__ void __launch_bounds__(kGenThreads) spec_kv_attention_kernel(const __
   fill_empty<E>(a, tid, kGenThreads);
   if (plan.w0 >= plan.w1) return;
   const int D = a.D, kst = D + 4, dv = D / 16;
-  float* sq = reinterpret_cast<float*>(dyn);  // [kGenRows][D]
-  float* sk = sq + kGenRows * D;              // [kGenSub][kst]: four floats of padding keep the lanes' banks apart
+  float* sq = reinterpret_cast<float*>(dyn);  // [ROWS][D]
+  float* sk = sq + ROWS * D;              // [kGenSub][kst]: four floats of padding keep the lanes' banks apart
   uint8_t* sv = reinterpret_cast<uint8_t*>(sk + kGenSub * kst);  // [kGenSub][D]
   const int half_vecs = kGenSub * dv;  // vectors of the staged keys
   Walk walk = walk_begin(plan, range, rt);
   Piece p;
   while (walk_next(a, walk, p)) {
-    const int j0 = p.tile0 * kTile, j1 = min(p.tile1 * kTile, p.L + p.n);
+    const int j0 = p.tile0 << a.log_tile, j1 = min(p.tile1 << a.log_tile, p.L + p.n);
     // queries in log2 units, zero rows past the last
-    for (int i = tid; i < kGenRows * D; i += kGenThreads) {
+    for (int i = tid; i < ROWS * D; i += kGenThreads) {
       const int r = i / D, d = i - r * D;
       float x = 0.0f;
       if (r < p.nrows) {
@@ -191,19 +196,25 @@ __global__ void __launch_bounds__(kGenThreads) spec_kv_attention_kernel(const __
       }
       sq[i] = x;
     }
-    float m[2] = {kNoRef, kNoRef}, l[2] = {0.0f, 0.0f};
-    int pos[2], low[2];
+    constexpr int RW = ROWS / 4;  // rows of a warp
+    float m[RW], l[RW];
+    int pos[RW], low[RW];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = warp * 2 + i;
+    for (int i = 0; i < RW; ++i) {
+      const int r = warp * RW + i;
+      m[i] = kNoRef;
+      l[i] = 0.0f;
       pos[i] = r < p.nrows ? p.L + (p.row0 + r) / a.G : -1;
       low[i] = a.window > 0 ? pos[i] - a.window : -1;  // sees positions in (low, pos]
     }
-    float acc[2][kGenRows];
+    float acc[kCh][ROWS];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < kCh; ++i)
 #pragma unroll
-      for (int r = 0; r < kGenRows; ++r) acc[i][r] = 0.0f;
+      for (int r = 0; r < ROWS; ++r) acc[i][r] = 0.0f;
+    // positions that every row sees
+    const int all_from = a.window > 0 ? p.L + (p.row0 + p.nrows - 1) / a.G - a.window + 1 : 0;
+    const int all_to = p.L + p.row0 / a.G;
 
     uint4 reg[kVecs];
     auto fetch = [&](int base) {
@@ -264,25 +275,28 @@ __global__ void __launch_bounds__(kGenThreads) spec_kv_attention_kernel(const __
       }
       __syncthreads();
       if (base + kGenSub < j1) fetch(base + kGenSub);
-      // scores of two rows
-      float s0 = 0.0f, s1 = 0.0f;
+      // scores of the warp's rows
+      float sc[RW];
+#pragma unroll
+      for (int i = 0; i < RW; ++i) sc[i] = 0.0f;
       {
         const float4* kp = reinterpret_cast<const float4*>(&sk[lane * kst]);
-        const float4* qa = reinterpret_cast<const float4*>(&sq[(warp * 2) * D]);
-        const float4* qb = reinterpret_cast<const float4*>(&sq[(warp * 2 + 1) * D]);
+        const float4* qp = reinterpret_cast<const float4*>(&sq[warp * RW * D]);
 #pragma unroll 4
         for (int d = 0; d < D / 4; ++d) {
-          const float4 k4 = kp[d], a4 = qa[d], b4 = qb[d];
-          s0 = fmaf(k4.x, a4.x, fmaf(k4.y, a4.y, fmaf(k4.z, a4.z, fmaf(k4.w, a4.w, s0))));
-          s1 = fmaf(k4.x, b4.x, fmaf(k4.y, b4.y, fmaf(k4.z, b4.z, fmaf(k4.w, b4.w, s1))));
+          const float4 k4 = kp[d];
+#pragma unroll
+          for (int i = 0; i < RW; ++i) {
+            const float4 q4 = qp[i * (D / 4) + d];
+            sc[i] = fmaf(k4.x, q4.x, fmaf(k4.y, q4.y, fmaf(k4.z, q4.z, fmaf(k4.w, q4.w, sc[i]))));
+          }
         }
       }
-      const float sc[2] = {s0 * ks, s1 * ks};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = warp * 2 + i;
+      for (int i = 0; i < RW; ++i) {
+        const int r = warp * RW + i;
         const bool see = j < j1 && j <= pos[i] && j > low[i];
-        const float x = see ? sc[i] : -INFINITY;
+        const float x = see ? sc[i] * ks : -INFINITY;
         float top = x;
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
@@ -294,46 +308,56 @@ __global__ void __launch_bounds__(kGenThreads) spec_kv_attention_kernel(const __
         if (lane == 0) sfac[r] = f;
       }
       __syncthreads();
+      const bool all = base >= all_from && base + kGenSub - 1 <= all_to;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kCh; ++i) {
         const int d = tid + i * kGenThreads;
         if (d < D) {
-          float f[kGenRows];
 #pragma unroll
-          for (int r = 0; r < kGenRows; ++r) {
-            f[r] = sfac[r];
-            acc[i][r] *= f[r];
-          }
-          for (int t = 0; t < kGenSub; t += 2) {
-            const uint16_t c2 = static_cast<uint16_t>(sv[t * D + d] | (sv[(t + 1) * D + d] << 8));
-            const float2 v = codes2_to_float2(c2);
+          for (int r = 0; r < ROWS; ++r) acc[i][r] *= sfac[r];
+#pragma unroll 2
+          for (int t = 0; t < kGenSub; t += 4) {
+            const uint8_t* v0 = &sv[t * D + d];
+            const float2 va = codes2_to_float2(static_cast<uint16_t>(v0[0] | (v0[D] << 8)));
+            const float2 vb = codes2_to_float2(static_cast<uint16_t>(v0[2 * D] | (v0[3 * D] << 8)));
+            if (all) {
 #pragma unroll
-            for (int r = 0; r < kGenRows; ++r) {
-              const float2 w = *reinterpret_cast<const float2*>(&sp[r][t]);
+              for (int r = 0; r < ROWS; ++r) {
+                const float4 w = *reinterpret_cast<const float4*>(&sp[r][t]);
+                acc[i][r] = fmaf(w.w, vb.y, fmaf(w.z, vb.x, fmaf(w.y, va.y, fmaf(w.x, va.x, acc[i][r]))));
+              }
+            } else {
               // a token that the row does not see adds nothing, whatever its slot holds
-              if (__float_as_uint(w.x) != 0x80000000u) acc[i][r] = fmaf(w.x, v.x, acc[i][r]);
-              if (__float_as_uint(w.y) != 0x80000000u) acc[i][r] = fmaf(w.y, v.y, acc[i][r]);
+              const float v[4] = {va.x, va.y, vb.x, vb.y};
+#pragma unroll
+              for (int r = 0; r < ROWS; ++r) {
+                const float4 w4 = *reinterpret_cast<const float4*>(&sp[r][t]);
+                const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (__float_as_uint(w[e]) != 0x80000000u) acc[i][r] = fmaf(w[e], v[e], acc[i][r]);
+              }
             }
           }
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < RW; ++i) {
 #pragma unroll
       for (int d = 16; d; d >>= 1) l[i] += __shfl_xor_sync(kFull, l[i], d);
       if (lane == 0) {
-        sl[warp * 2 + i] = l[i];
-        sm[warp * 2 + i] = m[i];
+        sl[warp * RW + i] = l[i];
+        sm[warp * RW + i] = m[i];
       }
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kCh; ++i) {
       const int d = tid + i * kGenThreads;
       if (d < D) {
 #pragma unroll
-        for (int r = 0; r < kGenRows; ++r) {
+        for (int r = 0; r < ROWS; ++r) {
           if (r >= p.nrows) continue;
           if (p.whole()) {
             const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;

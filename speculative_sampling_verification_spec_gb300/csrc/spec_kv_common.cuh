@@ -2,7 +2,7 @@
 // spec_kv_common.cuh -- what the paged-cache kernels share: their arguments, how
 // the attention's work is cut into ranges of tiles, and small device helpers.
 //
-// The attention's work is a list of tiles of kTile tokens: sequence after
+// The attention's work is a list of tiles of 2^log_tile tokens: sequence after
 // sequence, within a sequence head after head, within a head in order of
 // position.  Before each head's tiles come `overhead` places without one, for what
 // it costs to take up a head.  The list is cut into `nranges` equal ranges (from
@@ -23,7 +23,7 @@
 
 namespace spec_kv_detail {
 
-constexpr int kTile = 128;          // tokens of a tile
+constexpr int kTile = 128;          // tokens of a tensor-core tile
 constexpr int kMinScaleExp = -100;  // scales are at least 2^kMinScaleExp
 constexpr float kNoRef = -1e30f;    // softmax reference before any token
 constexpr unsigned kFull = 0xffffffffu;
@@ -50,6 +50,7 @@ struct KvArgs {
   float scale2;       // scale * log2(e): scores are kept in log2 units
   int32_t rows;       // rows of a row tile (row = t * G + head in group)
   int32_t nrt;        // row tiles of a sequence
+  int32_t log_tile;   // log2 of a tile's tokens
   int32_t nranges;    // ranges of the tile list
   int32_t overhead;   // places of the list before a head's tiles
   int32_t join_here;  // the last CTA of an item joins it, else the join kernel
@@ -84,8 +85,8 @@ __device__ __forceinline__ float2 codes2_to_float2(uint16_t c) {
   return __half22float2(__half2(h));
 }
 
-// The tokens of sequence b and the tiles its rows read: positions [t0 * kTile,
-// L + n).  No tiles when it has no new token or its lengths are out of range.
+// The tokens of sequence b and the tiles its rows read: positions from tile
+// t0 to L + n.  No tiles when it has no new token or its lengths are out of range.
 struct SeqSpan {
   int L, n, t0, nt;
   int places;  // a head's in the list
@@ -102,8 +103,8 @@ __device__ __forceinline__ SeqSpan seq_span(const KvArgs& a, int b) {
   s.places = 0;
   if (!s.bad && s.n > 0) {
     const int first = (a.window > 0 && s.L + 1 > a.window) ? s.L + 1 - a.window : 0;
-    s.t0 = first / kTile;
-    s.nt = (s.L + s.n + kTile - 1) / kTile - s.t0;
+    s.t0 = first >> a.log_tile;
+    s.nt = ((s.L + s.n - 1) >> a.log_tile) + 1 - s.t0;
     s.places = s.nt + a.overhead;
   }
   return s;
@@ -232,9 +233,9 @@ __device__ __forceinline__ bool walk_next(const KvArgs& a, Walk& k, Piece& p) {
     if (p.nrows <= 0 || t1 <= 0) continue;
     // tiles that some row of this row tile sees
     const int t_first = p.row0 / a.G, t_last = (p.row0 + p.nrows - 1) / a.G;
-    const int hi = (s.L + t_last) / kTile + 1;
+    const int hi = ((s.L + t_last) >> a.log_tile) + 1;
     const int lo = (a.window > 0 && s.L + t_first + 1 > a.window) ? s.L + t_first + 1 - a.window : 0;
-    p.tile0 = max(s.t0 + t0, lo / kTile);
+    p.tile0 = max(s.t0 + t0, lo >> a.log_tile);
     p.tile1 = min(s.t0 + t1, hi);
     if (p.tile1 < p.tile0) p.tile1 = p.tile0;
     return true;
