@@ -40,43 +40,6 @@ __device__ __forceinline__ void store4(const KvArgs& a, E* o, float4 x) {
   from_float(x.w, o + 3);
 }
 
-// Adds up the parts c0 .. c1 of one row, in order, `step` apart from `from`: lane
-// by lane four channels (and four more from 128 on).  `top` is the largest
-// reference of all parts.
-__device__ __forceinline__ void add_parts(const KvArgs& a, int rt, int r, int c0, int c1, int from, int step, float top,
-                                          float4* acc, float& l) {
-  const int lane = threadIdx.x & 31;
-  const auto slot_row = [&](int c) { return static_cast<int64_t>(part_slot(a, c, c0, rt)) * a.slot_rows + r; };
-  for (int cb = from; cb <= c1; cb += 32 * step) {
-    // weights of up to 32 parts, one a lane; a part without tokens for this row left no output
-    float wl = 0.0f, ll = 0.0f;
-    if (cb + lane * step <= c1) {
-      const float2 ml = __ldcg(&a.part_ml[slot_row(cb + lane * step)]);
-      ll = ml.y;
-      wl = exp2f(ml.x - top);
-    }
-    const int m = min(32, (c1 - cb) / step + 1);
-#pragma unroll 8
-    for (int i = 0; i < m; ++i) {
-      const float w = __shfl_sync(kFull, wl, i), li = __shfl_sync(kFull, ll, i);
-      const bool none = li == 0.0f;
-      const float* po = a.part_o + slot_row(cb + i * step) * a.D;
-      l = none ? l : fmaf(w, li, l);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int d = lane * 4 + k * 128;
-        if (d < a.D) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(po + d));
-          acc[k].x = none ? acc[k].x : fmaf(w, x.x, acc[k].x);
-          acc[k].y = none ? acc[k].y : fmaf(w, x.y, acc[k].y);
-          acc[k].z = none ? acc[k].z : fmaf(w, x.z, acc[k].z);
-          acc[k].w = none ? acc[k].w : fmaf(w, x.w, acc[k].w);
-        }
-      }
-    }
-  }
-}
-
 // The largest reference of a row's parts, in every lane.
 __device__ __forceinline__ float top_of_parts(const KvArgs& a, int rt, int r, int c0, int c1) {
   float top = kNoRef;
@@ -85,6 +48,68 @@ __device__ __forceinline__ float top_of_parts(const KvArgs& a, int rt, int r, in
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
   return top;
+}
+
+// Adds up the parts of one row from `from` on, `step` apart, in order: lane by lane
+// four channels (and four more from 128 on).  `top` gets the largest reference of
+// all parts c0 .. c1.  The first outputs are asked for before the references are
+// there: a join is a few trips to the L2 cache, one after the other.
+__device__ __forceinline__ void add_parts(const KvArgs& a, int rt, int r, int c0, int c1, int from, int step, float& top,
+                                          float4* acc, float& l) {
+  constexpr int kAhead = 4;
+  const int lane = threadIdx.x & 31;
+  const auto slot_row = [&](int c) { return static_cast<int64_t>(part_slot(a, c, c0, rt)) * a.slot_rows + r; };
+  const auto part_ml = [&](int cb) {  // of up to 32 parts, one a lane
+    return cb + lane * step <= c1 ? __ldcg(&a.part_ml[slot_row(cb + lane * step)]) : make_float2(kNoRef, 0.0f);
+  };
+  float2 ml = part_ml(from);
+  bool have_top = false;
+  for (int cb = from; cb <= c1; cb += 32 * step) {
+    if (cb != from) ml = part_ml(cb);
+    float wl = 0.0f;
+    const int m = min(32, (c1 - cb) / step + 1);
+    for (int i0 = 0; i0 < m; i0 += kAhead) {
+      float4 x[kAhead][2];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int d = lane * 4 + k * 128;
+          x[i][k] = make_float4(0, 0, 0, 0);
+          if (i0 + i < m && d < a.D)
+            x[i][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot_row(cb + (i0 + i) * step) * a.D + d));
+        }
+      }
+      if (i0 == 0) {
+        if (!have_top) {
+          top = step == 1 && c1 - c0 < 32 ? ml.x : kNoRef;
+          if (step == 1 && c1 - c0 < 32) {
+#pragma unroll
+            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+          } else {
+            top = top_of_parts(a, rt, r, c0, c1);
+          }
+          have_top = true;
+        }
+        wl = exp2f(ml.x - top);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float w = __shfl_sync(kFull, wl, i0 + i), li = __shfl_sync(kFull, ml.y, i0 + i);
+        // a part without tokens for this row left no output
+        if (i0 + i >= m || li == 0.0f) continue;
+        l = fmaf(w, li, l);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          acc[k].x = fmaf(w, x[i][k].x, acc[k].x);
+          acc[k].y = fmaf(w, x[i][k].y, acc[k].y);
+          acc[k].z = fmaf(w, x[i][k].z, acc[k].z);
+          acc[k].w = fmaf(w, x[i][k].w, acc[k].w);
+        }
+      }
+    }
+  }
+  if (!have_top) top = top_of_parts(a, rt, r, c0, c1);
 }
 
 // A joined row's output and lse, by one warp.
@@ -119,7 +144,7 @@ template <typename E>
 __device__ __forceinline__ void join_item(const KvArgs& a, const Piece& p, int rt, int warp, int warps) {
   for (int r = warp; r < p.nrows; r += warps) {
     const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
-    const float top = top_of_parts(a, rt, r, p.c0, p.c1);
+    float top;
     float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
     float l = 0.0f;
     add_parts(a, rt, r, p.c0, p.c1, p.c0, 1, top, acc, l);
@@ -409,7 +434,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) spec_kv_join_kernel(const __g
   const int c0 = first / per, c1 = (first + s.nt - 1) / per;
   if (c0 == c1) return;
   const int gr = t * a.G + g, rt = gr / a.rows, r = gr - rt * a.rows;
-  const float top = top_of_parts(a, rt, r, c0, c1);
+  float top;
   float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
   float l = 0.0f;
   add_parts(a, rt, r, c0, c1, c0 + warp, kJoinWarps, top, acc, l);

@@ -212,15 +212,14 @@ __device__ __forceinline__ void two_pieces(float w0, float w1, uint32_t& hi, uin
   lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(d), __NV_SATFINITE, __NV_E4M3);
 }
 
-// 16 channels of a row that is not aligned, as if loaded 16 bytes at a time
-static __device__ __noinline__ RawChunk<__nv_bfloat16, 8> gather16(const __nv_bfloat16* src) {
-  RawChunk<__nv_bfloat16, 8> r;
+// 8 channels of a row that is not aligned, as if loaded 16 bytes at a time
+static __device__ __noinline__ Raw<__nv_bfloat16, 8> gather8(const __nv_bfloat16* src) {
+  Raw<__nv_bfloat16, 8> r;
   const unsigned short* s = reinterpret_cast<const unsigned short*>(src);
-  uint32_t u[8];
+  uint32_t u[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = s[2 * i] | (static_cast<uint32_t>(s[2 * i + 1]) << 16);
-  r.lo.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
-  r.hi.w[0] = make_uint4(u[4], u[5], u[6], u[7]);
+  for (int i = 0; i < 4; ++i) u[i] = s[2 * i] | (static_cast<uint32_t>(s[2 * i + 1]) << 16);
+  r.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
   return r;
 }
 
@@ -499,91 +498,80 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         bool one_factor = true;
         float factor = 0.0f;
         if (m > 0) {
-          // queries: 16 channels a thread
-          constexpr int kPer = D / 16;                 // threads a row
+          // queries: 8 channels a thread
+          constexpr int kPer = D / 8;                  // threads a row
           constexpr int kStep = kSoftThreads / kPer;   // rows at a time
           constexpr int kTimes = (NR + kStep - 1) / kStep;
-          RawChunk<__nv_bfloat16, 8> raw[kTimes];
+          Raw<__nv_bfloat16, 8> raw[kTimes];
           uint32_t tops[kTimes];  // bits of a row's largest magnitude (NaN above infinity)
 #pragma unroll
           for (int i = 0; i < kTimes; ++i) {
             const int col = i * kStep + tid / kPer, c = tid % kPer, r = row_of(col);
-            raw[i].lo.w[0] = raw[i].hi.w[0] = make_uint4(0, 0, 0, 0);
+            raw[i].w[0] = make_uint4(0, 0, 0, 0);
             if (col < NR && r < p.nrows) {
               const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
               const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + p.b * a.q_seq + t * a.q_tok +
-                                         (p.h * a.G + g) * a.q_head + c * 16;
-              if (a.q_vec) {
-                raw[i].lo.load(src);
-                raw[i].hi.load(src + 8);
-              } else {
-                raw[i] = gather16(src);
-              }
+                                         (p.h * a.G + g) * a.q_head + c * 8;
+              if (a.q_vec)
+                raw[i].load(src);
+              else
+                raw[i] = gather8(src);
             }
           }
+          uint32_t most = 0, least = 0x7f7fffffu;
 #pragma unroll
           for (int i = 0; i < kTimes; ++i) {
-            float x[16];
+            float x[8];
             raw[i].values(x);
             uint32_t top = 0;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+            for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
 #pragma unroll
             for (int d = kPer / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(kFull, top, d));
             tops[i] = top;
-            if (tid % kPer == 0 && top > 0 && top < 0x7f800000u) {
-              atomicMax(&sm.q_top, top);
-              atomicMin(&sm.q_least, top);
+            if (top > 0 && top < 0x7f800000u) {
+              most = max(most, top);
+              least = min(least, top);
             }
+          }
+          most = __reduce_max_sync(kFull, most);
+          least = __reduce_min_sync(kFull, least);
+          if (lane == 0) {
+            atomicMax(&sm.q_top, most);
+            atomicMin(&sm.q_least, least);
           }
           soft_sync();
           const uint32_t q_top = sm.q_top;
           const float common = scale_for(__uint_as_float(q_top));
           one_factor = q_top < sm.q_least + (static_cast<uint32_t>(kNear) << 23);
           factor = one_factor ? common * a.scale2 : a.scale2;
-#pragma unroll 1
+#pragma unroll
           for (int i = 0; i < kTimes; ++i) {
             const int col = i * kStep + tid / kPer, c = tid % kPer;
-            RawChunk<__nv_bfloat16, 8> now = raw[0];
-            uint32_t top = tops[0];
-#pragma unroll
-            for (int e = 1; e < kTimes; ++e) {
-              if (i == e) {
-                now = raw[e];
-                top = tops[e];
-              }
-            }
-            float x[16];
-            now.values(x);
-            const bool fin = top < 0x7f800000u;  // a row that is not is NaN by its reference
-            const float s = one_factor ? common : fin ? scale_for(__uint_as_float(top)) : 1.0f;
+            if (col >= NR) continue;
+            float x[8];
+            raw[i].values(x);
+            const bool fin = tops[i] < 0x7f800000u;  // a row that is not is NaN by its reference
+            const float s = one_factor ? common : fin ? scale_for(__uint_as_float(tops[i])) : 1.0f;
             const float inv = 1.0f / s;
-            uint32_t hi[4], lo[4];
+            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-              uint32_t h4 = 0, l4 = 0;
-#pragma unroll
-              for (int e = 0; e < 4; e += 2) {
-                const float2 y = make_float2(fin ? x[4 * e4 + e] * inv : 0.0f, fin ? x[4 * e4 + e + 1] * inv : 0.0f);
-                const uint16_t ch = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-                const float2 b = codes2_to_float2(ch);
-                const uint16_t cl =
-                    __nv_cvt_float2_to_fp8x2(make_float2(y.x - b.x, y.y - b.y), __NV_SATFINITE, __NV_E4M3);
-                h4 |= static_cast<uint32_t>(ch) << (8 * e);
-                l4 |= static_cast<uint32_t>(cl) << (8 * e);
-              }
-              hi[e4] = h4;
-              lo[e4] = l4;
+            for (int e = 0; e < 8; e += 2) {
+              const float2 y = make_float2(fin ? x[e] * inv : 0.0f, fin ? x[e + 1] * inv : 0.0f);
+              const uint16_t ch = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+              const float2 b = codes2_to_float2(ch);
+              const uint16_t cl =
+                  __nv_cvt_float2_to_fp8x2(make_float2(y.x - b.x, y.y - b.y), __NV_SATFINITE, __NV_E4M3);
+              hi[e / 4] |= static_cast<uint32_t>(ch) << (8 * (e & 2));
+              lo[e / 4] |= static_cast<uint32_t>(cl) << (8 * (e & 2));
             }
-            if (col < NR) {
-              uint8_t* dst = sq + c * (NR * 16) + col * 16;
-              *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(dst + C::kQBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              if (c == 0) {
-                // a row that is not there has a reference no score passes
-                sm.refs[col] = row_of(col) >= p.nrows ? kNoRef : __uint_as_float(fin ? kUnset : 0x7fc00000u);
-                sm.factor[col] = s;
-              }
+            uint8_t* dst = sq + (c >> 1) * (NR * 16) + col * 16 + (c & 1) * 8;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(dst + C::kQBytes) = make_uint2(lo[0], lo[1]);
+            if (c == 0) {
+              // a row that is not there has a reference no score passes
+              sm.refs[col] = row_of(col) >= p.nrows ? kNoRef : __uint_as_float(fin ? kUnset : 0x7fc00000u);
+              sm.factor[col] = s;
             }
           }
           fence_async();
