@@ -792,10 +792,12 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             a.part_ml[static_cast<int64_t>(p.slot) * a.slot_rows + row_of(tid)] = make_float2(ref, s);
           }
         }
-        if (p.whole()) soft_sync();
+        const bool whole = p.whole();
+        if (whole) soft_sync();
         if (m > 0 && (warp & 3) * 32 < D) {
           const int row0 = group == 0 ? 0 : half_of(), mine = rows_mine();
           float* part = a.part_o + (static_cast<int64_t>(p.slot) * a.slot_rows + row0) * D + token;
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + token;
 #pragma unroll 1
           for (int c = 0; c < fours; c += 8) {
             float o[16];  // both pieces of eight rows
@@ -804,15 +806,22 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             tmem_wait_ld();
             tmem_tie<16>(o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = r_base + c + i;
-              if (c + i < mine) {
-                const float y = fmaf(o[8 + i], 0.0625f, o[i]);
-                if (p.whole())
-                  from_float(y * sm.fac[r], static_cast<__nv_bfloat16*>(a.out) + sm.out_at[r] + token);
-                else
-                  part[(c + i) * D] = y;
+            for (int i = 0; i < 8; ++i) o[i] = fmaf(o[8 + i], 0.0625f, o[i]);
+            if (whole) {
+              int64_t at[8];  // (read before the stores, which for all the compiler knows write there)
+              float f[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                at[i] = sm.out_at[r_base + c + i];
+                f[i] = sm.fac[r_base + c + i];
               }
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (c + i < mine) from_float(o[i] * f[i], out + at[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (c + i < mine) part[(c + i) * D] = o[i];
             }
           }
         }
