@@ -57,12 +57,13 @@ def workload_desc(name, w):
 
 
 def kernel_source_sha():
-    """SHA-256 over the library's CUDA sources (csrc/, in name order)."""
+    """SHA-256 over the verification kernels' CUDA sources (csrc/ but for the paged
+    cache's files, in name order)."""
     import glob
     import hashlib
     h = hashlib.sha256()
     for p in sorted(glob.glob(os.path.join(ROOT, "speculative_sampling_verification_spec_gb300", "csrc", "*"))):
-        if p.endswith((".cu", ".cuh", ".h")):
+        if p.endswith((".cu", ".cuh", ".h")) and not os.path.basename(p).startswith("spec_kv"):
             with open(p, "rb") as f:
                 h.update(os.path.basename(p).encode() + b"\0" + f.read())
     return h.hexdigest()
