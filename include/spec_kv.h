@@ -45,7 +45,8 @@ typedef struct {
   uint8_t* v_codes;
   float* k_scale;            /* device, [num_pages, Hkv] by the strides below */
   float* v_scale;
-  /* strides in elements, the same for keys and values; positive multiples of 16 for the codes */
+  /* strides in elements, the same for keys and values; positive where there is more than one, and
+   * multiples of 16 for the codes */
   int64_t page_stride, head_stride, token_stride;
   int64_t scale_page_stride, scale_head_stride;
 } spec_kv_cache;
@@ -65,7 +66,8 @@ typedef struct {
   const int32_t* seq_lens;   /* device [B]: tokens stored before this round's new ones, >= 0 */
   const int32_t* new_lens;   /* device [B]: new tokens, 0 to T; NULL = T each */
   int64_t table_stride;
-  /* strides in elements of [B, T, heads, D] tensors, channels contiguous; >= 0 for inputs, > 0 for outputs */
+  /* strides in elements of [B, T, heads, D] tensors, channels contiguous; >= 0 for inputs (0 repeats),
+   * > 0 for outputs where there is more than one */
   int64_t q_seq_stride, q_tok_stride, q_head_stride;
   int64_t k_seq_stride, k_tok_stride, k_head_stride;   /* append */
   int64_t v_seq_stride, v_tok_stride, v_head_stride;   /* append */

@@ -45,6 +45,9 @@ spec_status check_cache(const spec_kv_cache* c, const spec_kv_params* p) {
   if (c->page_stride < 0 || c->head_stride < 0 || c->token_stride < 0 || c->page_stride % 16 || c->head_stride % 16 ||
       c->token_stride % 16 || c->scale_page_stride < 0 || c->scale_head_stride < 0)
     return SPEC_ERR_INVALID_ARG;
+  if (c->token_stride == 0 || (c->Hkv > 1 && (c->head_stride == 0 || c->scale_head_stride == 0)) ||
+      (c->num_pages > 1 && (c->page_stride == 0 || c->scale_page_stride == 0)))
+    return SPEC_ERR_INVALID_ARG;
   if (!p->page_table || !p->seq_lens || p->max_pages < 1 || p->table_stride < 0) return SPEC_ERR_INVALID_ARG;
   const int64_t tiles = ((static_cast<int64_t>(p->max_pages) * c->page_size) >> kGenLogTile) + 1;
   // positions, and tiles of the whole call, are counted in 32 bits
@@ -54,6 +57,11 @@ spec_status check_cache(const spec_kv_cache* c, const spec_kv_params* p) {
 }
 
 bool bad_strides(int64_t seq, int64_t tok, int64_t head) { return seq < 0 || tok < 0 || head < 0; }
+// what is written may not overlap itself
+bool bad_output(const spec_kv_params* p) {
+  return bad_strides(p->o_seq_stride, p->o_tok_stride, p->o_head_stride) || (p->B > 1 && p->o_seq_stride == 0) ||
+         (p->T > 1 && p->o_tok_stride == 0) || (p->Hq > 1 && p->o_head_stride == 0);
+}
 
 void fill_cache(const spec_kv_cache* c, const spec_kv_params* p, KvArgs& a) {
   a.k_codes = c->k_codes;
@@ -282,7 +290,7 @@ spec_status spec_kv_append(const void* q, const void* k, const void* v, const fl
       bad_strides(p->v_seq_stride, p->v_tok_stride, p->v_head_stride))
     return SPEC_ERR_INVALID_ARG;
   if (q && (bad_strides(p->q_seq_stride, p->q_tok_stride, p->q_head_stride) ||
-            bad_strides(p->o_seq_stride, p->o_tok_stride, p->o_head_stride)))
+            bad_output(p)))
     return SPEC_ERR_INVALID_ARG;
   AppendArgs g = {};
   KvArgs& a = g.a;
@@ -355,8 +363,7 @@ spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const s
   if (p->B == 0) return SPEC_OK;
   s = check_cache(cache, p);
   if (s != SPEC_OK) return s;
-  if (!q || !out || bad_strides(p->q_seq_stride, p->q_tok_stride, p->q_head_stride) ||
-      bad_strides(p->o_seq_stride, p->o_tok_stride, p->o_head_stride))
+  if (!q || !out || bad_strides(p->q_seq_stride, p->q_tok_stride, p->q_head_stride) || bad_output(p))
     return SPEC_ERR_INVALID_ARG;
   if (!p->workspace || !aligned(p->workspace, 256) ||
       p->workspace_bytes < spec_kv_attention_workspace_size(cache, params))

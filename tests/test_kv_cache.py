@@ -190,7 +190,9 @@ BAD_BOTH = [dict(num_pages=0), dict(page_size=0), dict(page_size=8), dict(page_s
             dict(Hkv=0), dict(D=0), dict(D=24), dict(D=272), dict(k_codes=0), dict(v_codes=0x2008), dict(k_scale=0),
             dict(v_scale=0), dict(page_stride=-16), dict(token_stride=72), dict(head_stride=1000),
             dict(scale_page_stride=-1), dict(B=-1), dict(T=0), dict(Hq=0), dict(Hq=3), dict(dtype=2), dict(max_pages=0),
-            dict(page_table=0), dict(seq_lens=0), dict(table_stride=-1), dict(q2=-1), dict(o3=-1)]
+            dict(page_table=0), dict(seq_lens=0), dict(table_stride=-1), dict(q2=-1), dict(o3=-1),
+            dict(token_stride=0), dict(head_stride=0), dict(page_stride=0), dict(scale_head_stride=0),
+            dict(scale_page_stride=0), dict(o1=0), dict(o2=0), dict(o3=0)]
 
 
 @pytest.mark.parametrize("over", BAD_BOTH + [dict(window=-1), dict(scale=math.inf), dict(scale=math.nan),
