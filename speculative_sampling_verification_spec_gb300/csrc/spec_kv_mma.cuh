@@ -29,12 +29,26 @@
 // exponent of 2, so that p is the weight of the 8-bit values).  The running
 // maximum of a row is over the threads; it is not needed exactly, only as a
 // reference that keeps p within the 8-bit range, so it is raised (and the
-// accumulators rescaled) only when a score passes it by more than 2^kSlack.
+// accumulators rescaled) only when a weight would pass 2^kSlack times the one at
+// which it was set: about one tile in fifteen, and the first of an item.
+//
+// The matrix unit adds to its float accumulators with truncation: about 2^-24 of
+// the sum for each 32 tokens, always downwards in magnitude.  At a million tokens
+// in one range that is 1e-3 of an output, of the order of its bfloat16 rounding.
 //
 // Roles: warps 0-3 and 4-7 softmax and epilogue, each four warps for half of the
 // rows; warp 8 loads; one thread of warp 9 issues the products.  Scores are
 // double-buffered, so the products of the next tile run under the softmax of this
 // one.  Two CTAs share an SM.
+//
+// What bounds it.  Long caches: memory while few rows read them (64 sequences of
+// up to 8192 tokens, 8 rows a key/value head: 653 MB in 114 us, 5.7 TB/s), the
+// softmax warps' instructions as rows grow (32 sequences of up to 32768 tokens, 36
+// rows: 1.24 GB in 232 us, 5.4 TB/s; a tile costs a softmax warp about 3000 cycles
+// beside three others on its scheduler, the tensor unit is busy a sixth of the
+// time).  Part of a prompt (512 queries on 8192 tokens): the same instructions,
+// 142 GFLOP in 295 us.  Short calls: the chain of dependent steps (lengths, page
+// numbers, keys, scores, weights, output, join: 1000 tokens take 10.5 us).
 #include <cuda_fp16.h>
 
 #include "spec_kv_attn.cuh"
@@ -44,21 +58,26 @@
 namespace spec_kv_detail {
 
 // Rows of a row tile at most.  More would share one reading of the cache between
-// more rows, but 64 do not fit the registers of the softmax threads (a tile of a
-// prompt part took 472 us in tiles of 64, 367 in tiles of 48, 414 in tiles of 32).
+// more rows, but 64 do not fit the registers of the softmax threads (512 queries on
+// 8192 tokens took 472 us in row tiles of 64, 367 in tiles of 48, 414 in tiles of 32).
 constexpr int kMmaRows = 48;
 constexpr int kMmaThreads = 320;
 constexpr int kSoftThreads = 256;  // two groups of 128, a token a thread
-constexpr int kPieceRing = 8;       // pieces; at most two of a CTA's have no tiles
-constexpr int kScaleRing = 8;       // tiles of scales; a loader is never this far ahead of the softmax
+// Rings without a way back, because the loader cannot go round them: it is at most
+// KS + 2 <= 5 tiles ahead of the softmax (stages of keys, and two buffers of scores),
+// so at most five pieces with tiles, one more announced, then an empty one and the end.
+constexpr int kPieceRing = 8;
+constexpr int kScaleRing = 8;
 constexpr uint32_t kUnset = 0x80000000u;  // bits of -0: scores are taken as they are
 constexpr int kNear = 4;            // log2 of how far apart rows with one exponent may be
-constexpr int kSlack = 5;           // log2 of how far weights may pass the reference
+constexpr int kSlack = 5;           // log2 of how far weights may pass the reference (3: 7 % slower at 36 rows)
 constexpr float kShift = 8 - kSlack;  // a raised reference is kShift below the largest score: weights stay within 2^8 < 448
 
 // Stages of keys and of values, buffers of weights: what two CTAs an SM leave room
 // for.  Keys are used up two tiles ahead of the weights (the scores are
-// double-buffered), so values get the larger share.
+// double-buffered), so values get the larger share (48 columns: 262 us with two and
+// three stages, 277 with three and two; with two and two and a second buffer of
+// weights 283).
 template <int D, int NR>
 struct MmaCfg {
   static constexpr int kTileBytes = kTile * D;
