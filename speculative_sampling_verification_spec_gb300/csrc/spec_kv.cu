@@ -18,7 +18,6 @@ using namespace spec_kv_detail;
 // CTAs the attention's tile list is cut for: the 152 SMs times the CTAs that stay
 // resident on one (constants, so that the workspace size needs no device).
 constexpr int kSMs = 152;
-constexpr int kGenCtas = kSMs * 4;
 constexpr int kMmaCtas = kSMs * 2;
 // What an item costs beside its tiles, in tiles.
 constexpr int kGenOverhead = 1;
@@ -138,13 +137,14 @@ constexpr size_t kPartCounters = 64 * 1024;
 AttnPlan plan_attention(const spec_kv_cache* c, const spec_kv_params* p, bool mma) {
   AttnPlan pl;
   const int64_t rows = static_cast<int64_t>(p->T) * (p->Hq / c->Hkv);
-  const int most = mma ? kMmaRows : kGenRows;
+  const int most = mma ? kMmaRows : c->D > 128 ? 4 : 8;
   pl.nrt = static_cast<int>((rows + most - 1) / most);
-  // row tiles of equal size; the general kernel's have 4 or 8 rows
+  // row tiles of equal size; the general kernel's have 4 or 8 rows (4 past 128 channels)
   pl.rows = static_cast<int>((rows + pl.nrt - 1) / pl.nrt);
-  if (!mma) pl.rows = pl.rows <= 4 ? 4 : kGenRows;
+  if (!mma) pl.rows = pl.rows <= 4 ? 4 : 8;
   pl.slot_rows = pl.rows;
-  pl.nranges = std::max(1, (mma ? kMmaCtas : kGenCtas) / pl.nrt);
+  const int ctas = mma ? kMmaCtas : kSMs * gen_ctas_an_sm(c->D > 128 ? 8 : 4, pl.rows);
+  pl.nranges = std::max(1, ctas / pl.nrt);
   // with one range nothing is shared, so no partial results
   const size_t slots = pl.nranges > 1 ? static_cast<size_t>(2) * pl.nranges * pl.nrt : 0;
   // The last CTA of an item adds up its parts where that is little to read (the
@@ -236,23 +236,21 @@ bool allow_smem(const void* fn, int slot, int bytes) {
   return true;
 }
 
-template <typename E, int MAXD, int ROWS>
+template <typename E, int CH, int ROWS>
 const void* general_ptr() {
-  return reinterpret_cast<const void*>(&spec_kv_attention_kernel<E, MAXD, ROWS>);
+  return reinterpret_cast<const void*>(&spec_kv_attention_kernel<E, CH, ROWS>);
 }
 template <typename E>
 const void* general_fn(int D, int rows) {
-  if (rows == 4) return D > 128 ? general_ptr<E, 256, 4>() : general_ptr<E, 128, 4>();
-  return D > 128 ? general_ptr<E, 256, 8>() : general_ptr<E, 128, 8>();
+  if (D > 128) return general_ptr<E, 8, 4>();
+  return rows == 4 ? general_ptr<E, 4, 4>() : general_ptr<E, 4, 8>();
 }
 
 spec_status launch_general(const KvArgs& args, bool f32, int grid, cudaStream_t st) {
   KvArgs a = args;
   void* params[] = {&a};
   const void* fn = f32 ? general_fn<float>(a.D, a.rows) : general_fn<__nv_bfloat16>(a.D, a.rows);
-  const int smem = gen_smem_bytes(a.D, a.rows);
-  if (smem > 48 * 1024 && !allow_smem(fn, f32 ? 8 : 9, smem)) return SPEC_ERR_CUDA;
-  return launch(fn, grid, kGenThreads, smem, st, params);
+  return launch(fn, grid, kGenThreads, 0, st, params);
 }
 
 spec_status launch_mma(const KvArgs& args, const spec_kv_cache* c, const MapOrder& order, int grid, cudaStream_t st) {

@@ -8,9 +8,7 @@
 // l likewise.  All of it is held in float.
 //
 // float32 queries come here because 8-bit pieces cannot reach their precision (and
-// the matrix unit's truncated sums would not keep it).  Bound by shared-memory
-// reads: 16 sequences of 8000 tokens, 32 float32 query heads on 8 key/value heads:
-// 263 MB in 299 us.
+// the matrix unit's truncated sums would not keep it).
 #include "spec_kv_common.cuh"
 
 namespace spec_kv_detail {
@@ -177,29 +175,52 @@ __device__ __forceinline__ void fill_empty(const KvArgs& a, int tid, int threads
   }
 }
 
-constexpr int kGenThreads = 128;
-constexpr int kGenRows = 8;    // rows of a row tile at most
-constexpr int kGenLogTile = 6; // tokens of a tile: short, for latency
-constexpr int kGenSub = 32;    // tokens staged at a time: a lane's token in the scores
-constexpr int kGenMaxD = 256;
-constexpr int gen_smem_bytes(int D, int rows) { return 4 * (rows * D + kGenSub * (D + 4)) + kGenSub * D; }
+// sums over the 32 lanes of N = 8, 16 or 32 values each; lane r (mod N) gets value r's
+template <int N>
+__device__ __forceinline__ float lane_sums(float* v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int w = 16; w >= N; w >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], w);
+#pragma unroll
+  for (int w = N / 2; w; w >>= 1) {
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const bool up = lane & w;
+      const float keep = up ? v[i + w] : v[i], send = up ? v[i] : v[i + w];
+      v[i] = keep + __shfl_xor_sync(kFull, send, w);
+    }
+  }
+  return v[0];
+}
 
-// A CTA walks its pieces 32 tokens at a time.  The next 32 tokens' codes are in
-// registers (16-byte loads) while the present ones are worked on.  Scores: lane =
-// token, a row's maximum and sum stay in its warp.  Output: thread = channel, all
-// rows in registers.
-// MAXD: 128 or 256, the head sizes that the registers are laid out for; ROWS: rows
-// of a row tile, 4 or 8, a fourth of them a warp's.
-template <typename E, int MAXD, int ROWS>
-__global__ void __launch_bounds__(kGenThreads, MAXD == 128 ? 5 : 3)
+constexpr int kGenThreads = 128, kGenWarps = kGenThreads / 32;
+constexpr int kGenLogTile = 6;  // tokens of a tile: short, for latency
+constexpr int kGenStep = 8;     // tokens of a warp's step; they share a page
+constexpr int kGenMaxD = 256;
+
+// Each warp walks the piece's tokens on its own, every fourth step of eight, with a
+// softmax of its own; the four are added up at the end of the piece.  A lane holds
+// CH consecutive channels of the queries, of the output, and of each token, whose
+// codes it loads straight from the cache (a token's head is one coalesced load).
+// Scores: a lane's share of four tokens times ROWS rows, summed over the lanes by
+// halving, which leaves lane (row, token) with its score; weights go back to all
+// lanes through shared memory.  The next step's codes are on their way meanwhile.
+//
+// CH: 4 or 8, for head sizes up to 128 or 256; ROWS: rows of a row tile, 4 or 8.
+constexpr int gen_ctas_an_sm(int ch, int rows) { return ch == 4 && rows == 4 ? 4 : 3; }
+
+template <typename E, int CH, int ROWS>
+__global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
     spec_kv_attention_kernel(const __grid_constant__ KvArgs a) {
-  constexpr int kVecs = 2 * kGenSub * (MAXD / 16) / kGenThreads;  // 16-byte vectors a thread, keys and values
-  constexpr int kCh = MAXD / kGenThreads;                         // channels a thread
+  constexpr int kWords = CH / 4;  // 32-bit words of codes a token and lane
   __shared__ RangePlan plan;
-  __shared__ int scratch[kGenThreads / 32];
-  extern __shared__ __align__(16) uint8_t dyn[];  // gen_smem_bytes(D, ROWS)
-  __shared__ __align__(16) float sp[ROWS][kGenSub];
-  __shared__ float sfac[ROWS], sl[ROWS], sm[ROWS];
+  __shared__ int scratch[kGenWarps];
+  __shared__ __align__(16) float sp[kGenWarps][ROWS][4];  // weights of four tokens
+  __shared__ __align__(16) float sf[kGenWarps][ROWS];     // what a step multiplies the sums by
+  __shared__ float sm[kGenWarps][ROWS], sl[kGenWarps][ROWS];
+  __shared__ __align__(16) float so[kGenWarps][ROWS][32 * CH];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int range = blockIdx.x / a.nrt, rt = blockIdx.x - range * a.nrt;
   start_dependents();
@@ -207,210 +228,192 @@ __global__ void __launch_bounds__(kGenThreads, MAXD == 128 ? 5 : 3)
   make_plan_range<kGenThreads>(a, range, &plan, scratch, blockIdx.x == 0 ? a.prefix : nullptr);
   fill_empty<E>(a, tid, kGenThreads);
   if (plan.w0 >= plan.w1) return;
-  const int D = a.D, kst = D + 4, dv = D / 16;
-  float* sq = reinterpret_cast<float*>(dyn);  // [ROWS][D]
-  float* sk = sq + ROWS * D;              // [kGenSub][kst]: four floats of padding keep the lanes' banks apart
-  uint8_t* sv = reinterpret_cast<uint8_t*>(sk + kGenSub * kst);  // [kGenSub][D]
-  const int half_vecs = kGenSub * dv;  // vectors of the staged keys
+  const int D = a.D, d0 = lane * CH;
+  const bool mine = d0 < D;  // the lane has channels
+  const int my_row = (lane >> 2) % ROWS, my_tok = lane & 3;
   Walk walk = walk_begin(plan, range, rt);
   Piece p;
   while (walk_next(a, walk, p)) {
     const int j0 = p.tile0 << a.log_tile, j1 = min(p.tile1 << a.log_tile, p.L + p.n);
-    // queries in log2 units, zero rows past the last
-    for (int i = tid; i < ROWS * D; i += kGenThreads) {
-      const int r = i / D, d = i - r * D;
-      float x = 0.0f;
-      if (r < p.nrows) {
-        const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
-        x = to_float(static_cast<const E*>(a.q)[p.b * a.q_seq + t * a.q_tok + (p.h * a.G + g) * a.q_head + d]) * a.scale2;
+    float q[ROWS][CH], acc[ROWS][CH];  // queries in log2 units; zero past the last row and channel
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
+      const E* src = static_cast<const E*>(a.q) + p.b * a.q_seq + t * a.q_tok + (p.h * a.G + g) * a.q_head + d0;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        q[r][c] = mine && r < p.nrows ? to_float(src[c]) * a.scale2 : 0.0f;
+        acc[r][c] = 0.0f;
       }
-      sq[i] = x;
     }
-    constexpr int RW = ROWS / 4;  // rows of a warp
-    float m[RW], l[RW];
-    int pos[RW], low[RW];
-#pragma unroll
-    for (int i = 0; i < RW; ++i) {
-      const int r = warp * RW + i;
-      m[i] = kNoRef;
-      l[i] = 0.0f;
-      pos[i] = r < p.nrows ? p.L + (p.row0 + r) / a.G : -1;
-      low[i] = a.window > 0 ? pos[i] - a.window : -1;  // sees positions in (low, pos]
-    }
-    float acc[kCh][ROWS];
-#pragma unroll
-    for (int i = 0; i < kCh; ++i)
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) acc[i][r] = 0.0f;
-    // positions that every row sees
+    // positions that every row sees, and the lane's row's
     const int all_from = a.window > 0 ? p.L + (p.row0 + p.nrows - 1) / a.G - a.window + 1 : 0;
     const int all_to = p.L + p.row0 / a.G;
+    const int pos = my_row < p.nrows ? p.L + (p.row0 + my_row) / a.G : -1;
+    const int low = a.window > 0 ? pos - a.window : -1;  // sees positions in (low, pos]
+    float m = kNoRef, l = 0.0f;
 
-    uint4 reg[kVecs];
-    auto fetch = [&](int base) {
+    uint32_t kc[kGenStep][kWords], vc[kGenStep][kWords];
+    float ks, vs;
+    const auto number = [&](int base) { return base < j1 ? page_of(a, p.b, base >> a.log_page) : 0; };
+    const auto fetch = [&](int base, int page) {
+      ks = vs = __uint_as_float(0x7fc00000u);  // a page that is not the pool's
+      const bool ok = base < j1 && page >= 0;
+      if (base < j1 && page < 0 && lane == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+      if (ok) {
+        const int64_t at = page * a.scale_page_stride + p.h * a.scale_head_stride;
+        ks = a.k_scale[at];
+        vs = a.v_scale[at];
+      }
+      const int64_t row = page * a.page_stride + p.h * a.head_stride +
+                          (base & ((1 << a.log_page) - 1)) * a.token_stride + d0;
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        int v = tid + i * kGenThreads;
-        const bool val = v >= half_vecs;
-        if (val) v -= half_vecs;
-        reg[i] = make_uint4(0, 0, 0, 0);
-        if (v < half_vecs) {
-          const int tok = v / dv, c = v - tok * dv, j = base + tok;
-          if (j < j1) {
-            const int page = page_of(a, p.b, j >> a.log_page);
-            if (page >= 0)
-              reg[i] = *reinterpret_cast<const uint4*>((val ? a.v_codes : a.k_codes) + page * a.page_stride +
-                                                       p.h * a.head_stride +
-                                                       (j & ((1 << a.log_page) - 1)) * a.token_stride + c * 16);
-          }
+      for (int t = 0; t < kGenStep; ++t) {
+        const bool get = ok && mine && base + t < j1;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          kc[t][w] = get ? *reinterpret_cast<const uint32_t*>(a.k_codes + row + t * a.token_stride + 4 * w) : 0u;
+          vc[t][w] = get ? *reinterpret_cast<const uint32_t*>(a.v_codes + row + t * a.token_stride + 4 * w) : 0u;
         }
       }
     };
-    if (j0 < j1) fetch(j0);
-    for (int base = j0; base < j1; base += kGenSub) {
-      // scales of the lane's token; a page that is not the pool's gives NaN
-      const int j = base + lane;
-      float ks = 0.0f, vs = 0.0f;
-      if (j < j1) {
-        const int page = page_of(a, p.b, j >> a.log_page);
-        if (page < 0) {
-          ks = vs = __uint_as_float(0x7fc00000u);
-          if (warp == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
-        } else {
-          const int64_t at = page * a.scale_page_stride + p.h * a.scale_head_stride;
-          ks = a.k_scale[at];
-          vs = a.v_scale[at];
+    constexpr int kStride = kGenStep * kGenWarps;
+    int base = j0 + warp * kGenStep;
+    int page = number(base), next_page = number(base + kStride);
+    if (base < j1) fetch(base, page);
+    for (; base < j1; base += kStride) {
+      float kf[kGenStep][CH];
+      uint32_t vnow[kGenStep][kWords];
+      const float ks_now = ks, vs_now = vs;
+#pragma unroll
+      for (int t = 0; t < kGenStep; ++t) {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          const float2 lo = codes2_to_float2(static_cast<uint16_t>(kc[t][w] & 0xffffu));
+          const float2 hi = codes2_to_float2(static_cast<uint16_t>(kc[t][w] >> 16));
+          kf[t][4 * w] = lo.x;
+          kf[t][4 * w + 1] = lo.y;
+          kf[t][4 * w + 2] = hi.x;
+          kf[t][4 * w + 3] = hi.y;
+          vnow[t][w] = vc[t][w];
         }
       }
-      __syncthreads();  // the staged tokens before have been read
+      page = next_page;
+      next_page = number(base + 2 * kStride);
+      if (base + kStride < j1) fetch(base + kStride, page);
+      const bool all = base >= all_from && base + kGenStep - 1 <= all_to;
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        int v = tid + i * kGenThreads;
-        const bool val = v >= half_vecs;
-        if (val) v -= half_vecs;
-        if (v < half_vecs) {
-          const int tok = v / dv, c = v - tok * dv;
-          if (val) {
-            *reinterpret_cast<uint4*>(&sv[tok * D + c * 16]) = reg[i];
-          } else {
-            const uint32_t w[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 lo = codes2_to_float2(static_cast<uint16_t>(w[e] & 0xffffu));
-              const float2 hi = codes2_to_float2(static_cast<uint16_t>(w[e] >> 16));
-              *reinterpret_cast<float4*>(&sk[tok * kst + c * 16 + e * 4]) = make_float4(lo.x, lo.y, hi.x, hi.y);
-            }
-          }
-        }
-      }
-      __syncthreads();
-      if (base + kGenSub < j1) fetch(base + kGenSub);
-      // scores of the warp's rows
-      float sc[RW];
-#pragma unroll
-      for (int i = 0; i < RW; ++i) sc[i] = 0.0f;
-      {
-        const float4* kp = reinterpret_cast<const float4*>(&sk[lane * kst]);
-        const float4* qp = reinterpret_cast<const float4*>(&sq[warp * RW * D]);
-#pragma unroll 4
-        for (int d = 0; d < D / 4; ++d) {
-          const float4 k4 = kp[d];
-#pragma unroll
-          for (int i = 0; i < RW; ++i) {
-            const float4 q4 = qp[i * (D / 4) + d];
-            sc[i] = fmaf(k4.x, q4.x, fmaf(k4.y, q4.y, fmaf(k4.z, q4.z, fmaf(k4.w, q4.w, sc[i]))));
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < RW; ++i) {
-        const int r = warp * RW + i;
-        const bool see = j < j1 && j <= pos[i] && j > low[i];
-        const float x = see ? sc[i] * ks : -INFINITY;
-        float top = x;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-        const float mn = fmaxf(m[i], top), f = ex2(m[i] - mn);
-        const float w = ex2(x - mn);
-        m[i] = mn;
-        l[i] = fmaf(l[i], f, w);  // a lane's share of the sum
-        sp[r][lane] = see ? w * vs : -0.0f;  // -0: not seen
-        if (lane == 0) sfac[r] = f;
-      }
-      __syncthreads();
-      const bool all = base >= all_from && base + kGenSub - 1 <= all_to;
-#pragma unroll
-      for (int i = 0; i < kCh; ++i) {
-        const int d = tid + i * kGenThreads;
-        if (d < D) {
-#pragma unroll
-          for (int r = 0; r < ROWS; ++r) acc[i][r] *= sfac[r];
-#pragma unroll 2
-          for (int t = 0; t < kGenSub; t += 4) {
-            const uint8_t* v0 = &sv[t * D + d];
-            const float2 va = codes2_to_float2(static_cast<uint16_t>(v0[0] | (v0[D] << 8)));
-            const float2 vb = codes2_to_float2(static_cast<uint16_t>(v0[2 * D] | (v0[3 * D] << 8)));
-            if (all) {
-#pragma unroll
-              for (int r = 0; r < ROWS; ++r) {
-                const float4 w = *reinterpret_cast<const float4*>(&sp[r][t]);
-                acc[i][r] = fmaf(w.w, vb.y, fmaf(w.z, vb.x, fmaf(w.y, va.y, fmaf(w.x, va.x, acc[i][r]))));
-              }
-            } else {
-              // a token that the row does not see adds nothing, whatever its slot holds
-              const float v[4] = {va.x, va.y, vb.x, vb.y};
-#pragma unroll
-              for (int r = 0; r < ROWS; ++r) {
-                const float4 w4 = *reinterpret_cast<const float4*>(&sp[r][t]);
-                const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (__float_as_uint(w[e]) != 0x80000000u) acc[i][r] = fmaf(w[e], v[e], acc[i][r]);
-              }
-            }
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < RW; ++i) {
-#pragma unroll
-      for (int d = 16; d; d >>= 1) l[i] += __shfl_xor_sync(kFull, l[i], d);
-      if (lane == 0) {
-        sl[warp * RW + i] = l[i];
-        sm[warp * RW + i] = m[i];
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kCh; ++i) {
-      const int d = tid + i * kGenThreads;
-      if (d < D) {
+      for (int t0 = 0; t0 < kGenStep; t0 += 4) {
+        float s[ROWS * 4];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-          if (r >= p.nrows) continue;
-          if (p.whole()) {
-            const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
-            from_float(acc[i][r] / sl[r], static_cast<E*>(a.out) + p.b * a.o_seq + t * a.o_tok + (p.h * a.G + g) * a.o_head + d);
-          } else {
-            a.part_o[(static_cast<int64_t>(p.slot) * a.slot_rows + r) * D + d] = acc[i][r];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            float x = q[r][0] * kf[t0 + t][0];
+#pragma unroll
+            for (int c = 1; c < CH; ++c) x = fmaf(q[r][c], kf[t0 + t][c], x);
+            s[r * 4 + t] = x;
+          }
+        }
+        const float score = lane_sums<ROWS * 4>(s) * ks_now;
+        const int j = base + t0 + my_tok;
+        const bool see = j <= pos && j > low;  // (positions from j1 on are past every row's own)
+        const float x = see ? score : -INFINITY;
+        float top = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+        const float mn = fmaxf(m, top), f = ex2(m - mn), w = ex2(x - mn);
+        m = mn;
+        l = fmaf(l, f, w);  // this lane's tokens' share of the sum
+        const bool raised = __any_sync(kFull, f != 1.0f);
+        __syncwarp();  // the weights before have been read
+        if (lane < ROWS * 4) {
+          sp[warp][my_row][my_tok] = see ? w * vs_now : -0.0f;  // -0: not seen
+          if (my_tok == 0) sf[warp][my_row] = f;
+        }
+        __syncwarp();
+        float v[4][CH];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+          for (int e = 0; e < kWords; ++e) {
+            const float2 lo = codes2_to_float2(static_cast<uint16_t>(vnow[t0 + t][e] & 0xffffu));
+            const float2 hi = codes2_to_float2(static_cast<uint16_t>(vnow[t0 + t][e] >> 16));
+            v[t][4 * e] = lo.x;
+            v[t][4 * e + 1] = lo.y;
+            v[t][4 * e + 2] = hi.x;
+            v[t][4 * e + 3] = hi.y;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          if (raised) {
+            const float fr = sf[warp][r];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) acc[r][c] *= fr;
+          }
+          const float4 w4 = *reinterpret_cast<const float4*>(sp[warp][r]);
+          const float wr[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            // a token that the row does not see adds nothing, whatever its slot holds
+            if (!all && __float_as_uint(wr[t]) == 0x80000000u) continue;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) acc[r][c] = fmaf(wr[t], v[t][c], acc[r][c]);
           }
         }
       }
     }
-    if (tid < p.nrows) {
-      const int gr = p.row0 + tid, t = gr / a.G, g = gr - t * a.G;
+    // the four warps' results: references and sums, then outputs
+    l += __shfl_xor_sync(kFull, l, 1);
+    l += __shfl_xor_sync(kFull, l, 2);
+    if (my_tok == 0 && lane < ROWS * 4) {
+      sm[warp][my_row] = m;
+      sl[warp][my_row] = l;
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int c = 0; c < CH; c += 4)
+        *reinterpret_cast<float4*>(&so[warp][r][d0 + c]) =
+            make_float4(acc[r][c], acc[r][c + 1], acc[r][c + 2], acc[r][c + 3]);
+    __syncthreads();
+    for (int r = warp; r < p.nrows; r += kGenWarps) {
+      float top = sm[0][r];
+#pragma unroll
+      for (int w = 1; w < kGenWarps; ++w) top = fmaxf(top, sm[w][r]);
+      float sum = 0.0f, o[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) o[c] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kGenWarps; ++w) {
+        const float f = ex2(sm[w][r] - top), lw = sl[w][r];
+        if (lw == 0.0f) continue;  // no tokens for this row
+        sum = fmaf(f, lw, sum);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) o[c] = fmaf(f, so[w][r][d0 + c], o[c]);
+      }
+      const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
       if (p.whole()) {
-        if (a.lse) a.lse[(static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g] = lse_of(sm[tid], sl[tid]);
+        const float inv = 1.0f / sum;
+        E* out = static_cast<E*>(a.out) + p.b * a.o_seq + t * a.o_tok + (p.h * a.G + g) * a.o_head + d0;
+#pragma unroll
+        for (int c = 0; c < CH; c += 4)
+          if (mine) store4(a, out + c, make_float4(o[c] * inv, o[c + 1] * inv, o[c + 2] * inv, o[c + 3] * inv));
+        if (lane == 0 && a.lse) a.lse[(static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g] = lse_of(top, sum);
       } else {
-        a.part_ml[static_cast<int64_t>(p.slot) * a.slot_rows + tid] = make_float2(sm[tid], sl[tid]);
+        const int64_t at = static_cast<int64_t>(p.slot) * a.slot_rows + r;
+#pragma unroll
+        for (int c = 0; c < CH; c += 4)
+          if (mine) *reinterpret_cast<float4*>(a.part_o + at * D + d0 + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+        if (lane == 0) a.part_ml[at] = make_float2(top, sum);
       }
     }
-    __syncthreads();  // queries and statistics are rewritten by the next piece
+    __syncthreads();  // the results' places are used again
     if (a.join_here && !p.whole()) {
       if (tid == 0) scratch[0] = last_of_item(a, p, rt);
       __syncthreads();
-      if (scratch[0]) join_item<E>(a, p, rt, warp, kGenThreads / 32);
+      if (scratch[0]) join_item<E>(a, p, rt, warp, kGenWarps);
+      __syncthreads();
     }
   }
 }

@@ -202,26 +202,6 @@ __device__ __forceinline__ int order_of(float x) {
 }
 __device__ __forceinline__ float of_order(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
-// sums over the 32 lanes of N = 8, 16 or 32 values each; lane r (mod N) gets value r's
-template <int N>
-__device__ __forceinline__ float lane_sums(float* v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int w = 16; w >= N; w >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], w);
-#pragma unroll
-  for (int w = N / 2; w; w >>= 1) {
-#pragma unroll
-    for (int i = 0; i < w; ++i) {
-      const bool up = lane & w;
-      const float keep = up ? v[i + w] : v[i], send = up ? v[i] : v[i + w];
-      v[i] = keep + __shfl_xor_sync(kFull, send, w);
-    }
-  }
-  return v[0];
-}
-
 // the e4m3 codes of two floats' nearest halves, and of 16 times what they leave over
 __device__ __forceinline__ void two_pieces(float w0, float w1, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(w0, w1);
