@@ -209,7 +209,7 @@ constexpr int kGenMaxD = 256;
 // lanes through shared memory.  The next step's codes are on their way meanwhile.
 //
 // CH: 4 or 8, for head sizes up to 128 or 256; ROWS: rows of a row tile, 4 or 8.
-constexpr int gen_ctas_an_sm(int ch, int rows) { return ch == 4 && rows == 4 ? 4 : 3; }
+constexpr int gen_ctas_an_sm(int ch, int rows) { return ch == 8 ? 2 : rows == 4 ? 4 : 3; }
 
 template <typename E, int CH, int ROWS>
 __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
