@@ -704,6 +704,74 @@ def test_rounds_with_rejected_tokens(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pad", [0, 16, 64])
+def test_padded_pools(D, pad):
+    """Token slots `pad` bytes apart beyond their channels: strides that a tensor map holds and strides that it does
+    not (another kernel then) give the definition's results; so does a pool of one page and one head."""
+    import speculative_sampling_verification_spec_gb300 as sv
+    for B, Hkv, seq, new in ((2, 2, [37, 300], [3, 2]), (1, 1, [5], [3])):
+        s = Setup(40, B, 3, 4, Hkv, D, 16, seq, new, "bf16", rot=D)
+        if B == 1:      # one page
+            keep = int(s.table[0, 0])
+            s.kc, s.vc, s.ks, s.vs = (x[keep:keep + 1].copy() for x in (s.kc, s.vc, s.ks, s.vs))
+            s.table, s.cs, s.N = np.zeros((1, 1), np.int32), s.cs[:16], 1
+        codes = []
+        for x in (s.kc, s.vc):
+            wide = torch.full((s.N, Hkv, 16, D + pad), 0x7F, dtype=torch.uint8, device="cuda")
+            wide[..., :D] = torch.from_numpy(x).cuda()
+            codes.append(wide[..., :D])
+        cache = sv.PagedKVCache(*codes, torch.from_numpy(s.ks).cuda(), torch.from_numpy(s.vs).cuda())
+        q = s.append(cache)
+        raw = s.q
+        s.q = s.ref_append()
+        assert np.array_equal(q.float().cpu().numpy(), s.q)
+        assert_cache(cache, s)
+        if pad:
+            assert all((c._base if c._base is not None else c)[..., D:].eq(0x7F).all() for c in codes)
+        out, lse = sv.spec_kv_attention(q, cache, *s.idx(), return_lse=True)
+        assert_attention(out, lse, s.ref_attention())
+        s.q = raw
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_calls_replay_from_a_graph(dtype):
+    """Append and attention captured once and replayed with other lengths, queries and tokens in the same tensors give
+    what direct calls give: lengths and page numbers are read on the device."""
+    import speculative_sampling_verification_spec_gb300 as sv
+    s = Setup(41, 3, 4, 8, 2, 64, 16, [20, 400, 0], [4, 2, 3], dtype, rot=64)
+    a, b = s.cache(), s.cache()
+    table, seq, new = s.idx()
+    cs = torch.from_numpy(s.cs).cuda()
+    q, k, v = s.dev(s.q), s.dev(s.k), s.dev(s.v)
+
+    def step(cache):
+        r = sv.spec_kv_append(q, k, v, cache, table, seq, new, cos_sin=cs)
+        return sv.spec_kv_attention(r, cache, table, seq, new, return_lse=True)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(a)             # makes the stream's workspace
+        a = s.cache()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = step(a)
+    torch.cuda.current_stream().wait_stream(side)
+    for seqs, news in (([20, 400, 0], [4, 2, 3]), ([22, 402, 3], [4, 4, 0]), ([24, 250, 3], [1, 4, 4])):
+        seq.copy_(torch.tensor(seqs, dtype=torch.int32))
+        new.copy_(torch.tensor(news, dtype=torch.int32))
+        q.copy_(s.dev(s.values(3, 4, 8, 64)))
+        k.copy_(s.dev(s.values(3, 4, 2, 64)))
+        graph.replay()
+        want = step(b)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(a.k_codes.view(torch.uint8), b.k_codes.view(torch.uint8))
+        assert torch.equal(a.k_scale, b.k_scale) and torch.equal(a.v_scale, b.v_scale)
+
+
+@gpu
 def test_python_checks():
     import speculative_sampling_verification_spec_gb300 as sv
     s = Setup(39, 2, 3, 4, 2, 64, 16, [5, 6], [3, 3], "bf16", 64)
