@@ -20,7 +20,7 @@ EXPORTED = ("spec_kv_append", "spec_kv_attention", "spec_kv_attention_workspace_
 # spec_kv_cache and spec_kv_params of include/spec_kv.h, in native layout
 _CACHE = struct.Struct("@4i4P5q")
 _PARAMS = struct.Struct("@6if3i3P13q3PN")
-_F32, _BF16 = torch.float32, torch.bfloat16
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 _DTYPES = {_F32: binding.SPEC_F32, _BF16: binding.SPEC_BF16}
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _WS_LEAST = 1 << 20     # bytes of a stream's first workspace: most shapes' later calls need no other
@@ -67,6 +67,7 @@ class PagedKVCache:
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k_codes.shape
         self.device = k_codes.device
+        self._index = k_codes.get_device()
         st = k_codes.stride()
         self._packed = _CACHE.pack(self.num_pages, self.page_size, self.kv_heads, self.head_dim, k_codes.data_ptr(),
                                    v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), st[0], st[1], st[2],
@@ -120,24 +121,31 @@ def _workspace(key, nbytes, device, stream):
 
 
 def _check_table(cache, B, page_table, seq_lens, new_lens, status):
-    dev = cache.device
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
-            page_table.shape[1] < 1 or page_table.stride(1) != 1:
-        raise ValueError("page_table must be int32 [B, max_pages], contiguous along the pages")
-    if seq_lens.dtype != torch.int32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
-        raise ValueError("seq_lens must be contiguous int32 [B]")
-    if new_lens is not None and (new_lens.dtype != torch.int32 or new_lens.shape != (B,) or
-                                 not new_lens.is_contiguous() or new_lens.device != dev):
+    """The columns and row stride of the page table, after checking it and the lengths."""
+    dev = cache._index
+    shape = page_table.shape
+    if page_table.dtype is not _I32 or len(shape) != 2 or shape[0] != B or shape[1] < 1 or \
+            page_table.get_device() != dev:
+        raise ValueError("page_table must be int32 [B, max_pages] on the cache's device")
+    row, col = page_table.stride()
+    if col != 1:
+        raise ValueError("page_table must be contiguous along the pages")
+    if seq_lens.dtype is not _I32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous() or \
+            seq_lens.get_device() != dev:
+        raise ValueError("seq_lens must be contiguous int32 [B] on the cache's device")
+    if new_lens is not None and (new_lens.dtype is not _I32 or new_lens.shape != (B,) or
+                                 not new_lens.is_contiguous() or new_lens.get_device() != dev):
         raise ValueError("new_lens must be contiguous int32 [B] on the cache's device")
-    if page_table.device != dev or seq_lens.device != dev or (status is not None and status.device != dev):
-        raise ValueError("page_table, lengths and status must be on the cache's device")
+    if status is not None and (status.dtype is not _I32 or status.get_device() != dev or status.numel() < 1):
+        raise ValueError("status must be int32 [1] on the cache's device")
+    return shape[1], row
 
 
 def _strides(name, t, shape, dtype, device):
     """The strides of a [B, T, heads, head_dim] tensor, after checking it."""
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError("%s must be %s %s on %s, got %s %s on %s" % (name, dtype, tuple(shape), device, t.dtype,
-                                                                     tuple(t.shape), t.device))
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError("%s must be %s %s on device %d, got %s %s on %s" % (name, dtype, tuple(shape), device, t.dtype,
+                                                                            tuple(t.shape), t.device))
     st = t.stride()
     if st[3] != 1:
         raise ValueError("%s must be contiguous along the channels" % name)
@@ -167,16 +175,16 @@ def spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens=None, *, cos_s
     Returns the rotated queries (q_out, or a new contiguous tensor; zero in slots past new_lens); q_out may be q.
     The cache is written in place."""
     dtype = _first_check("k", k, "kv_heads")
-    shape, dt, dev = k.shape, k.dtype, cache.device
+    shape, dt, dev, index = k.shape, k.dtype, cache.device, cache._index
     B, T, hq, D = shape
     if hq != cache.kv_heads or D != cache.head_dim:
         raise ValueError("k must be [B, T, %d, %d], got %s" % (cache.kv_heads, cache.head_dim, tuple(shape)))
-    ks = _strides("k", k, shape, dt, dev)
-    vs = _strides("v", v, shape, dt, dev)
-    _check_table(cache, B, page_table, seq_lens, new_lens, status)
+    ks = _strides("k", k, shape, dt, index)
+    vs = _strides("v", v, shape, dt, index)
+    columns, row = _check_table(cache, B, page_table, seq_lens, new_lens, status)
     rot = rot_len = cs = 0
     if cos_sin is not None:
-        if cos_sin.dtype != _F32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.device != dev:
+        if cos_sin.dtype is not _F32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.get_device() != index:
             raise ValueError("cos_sin must be contiguous float32 [positions, rot_dim] on the cache's device")
         rot_len, rot = cos_sin.shape
         cs = cos_sin.data_ptr()
@@ -186,18 +194,18 @@ def spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens=None, *, cos_s
             raise ValueError("q must be [B, T, Hq, head_dim]")
         hq = q.shape[2]
         shape = (B, T, hq, D)
-        qs = _strides("q", q, shape, dt, dev)
+        qs = _strides("q", q, shape, dt, index)
         if q_out is None:
             q_out = _new(shape, dt, dev, stream)
             os = q_out.stride()
         else:
-            os = _strides("q_out", q_out, shape, dt, dev)
+            os = _strides("q_out", q_out, shape, dt, index)
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    prm = _PARAMS.pack(B, T, hq, dtype, page_table.shape[1], 0, 0.0, rot, rot_len, 1 if interleaved else 0,
+    prm = _PARAMS.pack(B, T, hq, dtype, columns, 0, 0.0, rot, rot_len, 1 if interleaved else 0,
                        page_table.data_ptr(), seq_lens.data_ptr(), 0 if new_lens is None else new_lens.data_ptr(),
-                       page_table.stride(0), qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], os[0],
+                       row, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], os[0],
                        os[1], os[2], _stream_of(stream, dev), 0 if status is None else status.data_ptr(), 0, 0)
     code = _lib().spec_kv_append(qp, k.data_ptr(), v.data_ptr(), cs, cache._packed, prm, op)
     if code != binding.SPEC_OK:
@@ -215,29 +223,29 @@ def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=No
     natural logarithm of the sum of the weights, when return_lse or lse is given.  ws: a workspace of
     spec_kv_attention_workspace_size bytes (uint8, CUDA, zeroed once); by default one is kept for each stream."""
     dtype = _first_check("q", q, "Hq")
-    shape, dt, dev = q.shape, q.dtype, cache.device
+    shape, dt, dev, index = q.shape, q.dtype, cache.device, cache._index
     B, T, hq, D = shape
     if D != cache.head_dim:
         raise ValueError("q must be [B, T, Hq, %d], got %s" % (cache.head_dim, tuple(shape)))
-    qs = _strides("q", q, shape, dt, dev)
-    _check_table(cache, B, page_table, seq_lens, new_lens, status)
+    qs = _strides("q", q, shape, dt, index)
+    columns, row = _check_table(cache, B, page_table, seq_lens, new_lens, status)
     if out is None:
         out = _new(shape, dt, dev, stream)
         os = out.stride()
     else:
-        os = _strides("out", out, shape, dt, dev)
+        os = _strides("out", out, shape, dt, index)
     if lse is not None:
-        if lse.dtype != _F32 or lse.shape != shape[:3] or not lse.is_contiguous() or lse.device != dev:
+        if lse.dtype is not _F32 or lse.shape != shape[:3] or not lse.is_contiguous() or lse.get_device() != index:
             raise ValueError("lse must be contiguous float32 [B, T, Hq] on the cache's device")
     elif return_lse:
         lse = _new(shape[:3], _F32, dev, stream)
     handle = _stream_of(stream, dev)
-    key = (dev.index, handle)
+    key = (index, handle)
     if ws is None:
         ws = _ws_cache.get(key)
-    fixed = (B, T, hq, dtype, page_table.shape[1], window, 1.0 / math.sqrt(D) if scale is None else scale, 0, 0, 0,
+    fixed = (B, T, hq, dtype, columns, window, 1.0 / math.sqrt(D) if scale is None else scale, 0, 0, 0,
              page_table.data_ptr(), seq_lens.data_ptr(), 0 if new_lens is None else new_lens.data_ptr(),
-             page_table.stride(0), qs[0], qs[1], qs[2], 0, 0, 0, 0, 0, 0, os[0], os[1], os[2], handle,
+             row, qs[0], qs[1], qs[2], 0, 0, 0, 0, 0, 0, os[0], os[1], os[2], handle,
              0 if status is None else status.data_ptr())
     args = (q.data_ptr(), cache._packed, out.data_ptr(), 0 if lse is None else lse.data_ptr())
     L = _lib()

@@ -107,7 +107,8 @@ def attention(q, kc, vc, ks, vs, table, seq, new, page_size, scale, window=0, dt
           |out - exact| <= 2 (e + n u) sum_j w_j |v_j| / sum_j w_j.
       bfloat16 queries: the weights reach the products in two 8-bit pieces of 4 significant bits each, a relative 2^-8
       of a weight, or 2^-17 of the largest weight where a piece is subnormal; the queries in two pieces as well, exact
-      but for 2^-17 of the row's largest; and the output is rounded to 8 bits, 2^-8 |out| at most.
+      but for 2^-17 of the row's largest (of rows that share an exponent, the largest's, 2^4 times more at most: far
+      inside the 2^-8 of the weights); and the output is rounded to 8 bits, 2^-8 |out| at most.
       lse: off by e + n u, and u |lse| a few times over."""
     B, T, Hq, D = q.shape
     Hkv, S = kc.shape[1], page_size
