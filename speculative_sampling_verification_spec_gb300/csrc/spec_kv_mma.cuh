@@ -605,17 +605,22 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             const bool bad_scale = !(sc.x == sc.x && sc.z == sc.z);
             uint8_t* row = sv + (n % C::VS) * C::kTileBytes + token * D;  // whole rows: the swizzle stays inside
             if (!fail) fail = !bar_wait(&sm.v_full[n % C::VS], (n / C::VS) & 1, gave_up);
+            // (lanes begin at different places of their rows, which all start at one bank)
             if (!all_see && !gone) {
               uint32_t nan = 0;
-#pragma unroll 4
-              for (int i = 0; i < D / 4; ++i)
-                nan |= __vcmpeq4(reinterpret_cast<const uint32_t*>(row)[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint4 u = reinterpret_cast<const uint4*>(row)[(i + lane) % (D / 16)];
+                nan |= __vcmpeq4(u.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(u.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                       __vcmpeq4(u.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(u.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              }
               poison = nan != 0 || bad_scale;
             }
             soft_sync();  // both groups have looked
             if (gone || poison) {
 #pragma unroll 4
-              for (int i = 0; i < D / 16; ++i) reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < D / 16; ++i)
+                reinterpret_cast<uint4*>(row)[(i + lane) % (D / 16)] = make_uint4(0, 0, 0, 0);
               if (gone || bad_scale) sc = make_float4(0.0f, 0.0f, 1.0f, 0.0f);
             }
           }
