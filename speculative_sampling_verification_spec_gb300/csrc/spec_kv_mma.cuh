@@ -44,10 +44,10 @@
 // What bounds it.  Long caches: memory while few rows read them (64 sequences of
 // up to 8192 tokens, 8 rows a key/value head: 653 MB in 106 us, 6.2 TB/s), the
 // softmax warps' instructions beside it as rows grow (32 sequences of up to 32768
-// tokens, 36 rows: 1.24 GB in 216 us, 5.8 TB/s; a tile costs a softmax warp about
+// tokens, 36 rows: 1.24 GB in 211 us, 5.9 TB/s; a tile costs a softmax warp about
 // 3000 cycles beside three others on its scheduler, the tensor unit is busy a sixth
 // of the time).  Part of a prompt (512 queries on 8192 tokens): the same instructions,
-// 142 GFLOP in 295 us.  Short calls: the chain of dependent steps (lengths, page
+// 142 GFLOP in 291 us.  Short calls: the chain of dependent steps (lengths, page
 // numbers, keys, scores, weights, output, join: 1000 tokens take 10.5 us).
 #include <cuda_fp16.h>
 
