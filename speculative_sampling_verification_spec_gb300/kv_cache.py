@@ -110,13 +110,23 @@ def _new(shape, dtype, device, stream):
 
 
 _ws_cache = {}
+_ws_outgrown = []      # kept: a captured graph may hold their addresses
 
 
 def _workspace(key, nbytes, device, stream):
-    """The workspace of (device, stream): calls on different streams may overlap, so each stream has its own."""
+    """The workspace of (device, stream): calls on different streams may overlap, so each stream has its own.  One that
+    is made while the stream is captured belongs to the graph, which clears it at every replay, and is not kept; a call
+    before the capture spares the graph that."""
+    old = _ws_cache.get(key)
     with torch.cuda.stream(stream):
+        capturing = torch.cuda.is_current_stream_capturing()
+        if old is not None and not capturing:
+            nbytes = max(nbytes, 2 * old.numel())
         ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)  # counters that calls leave at zero
-    _ws_cache[key] = ws
+    if not capturing:
+        if old is not None:
+            _ws_outgrown.append(old)
+        _ws_cache[key] = ws
     return ws
 
 

@@ -772,6 +772,34 @@ def test_calls_replay_from_a_graph(dtype):
 
 
 @gpu
+def test_capture_on_a_fresh_stream():
+    """A call captured on a stream that has no workspace yet: the graph's is its own, so a direct call on that stream,
+    before and after a replay, finds cleared counters."""
+    import speculative_sampling_verification_spec_gb300 as sv
+    s = Setup(42, 1, 1, 4, 1, 64, 16, [3000], [1], "bf16")
+    cache = s.cache()
+    s.append(cache)
+    s.ref_append()
+    want = s.ref_attention()
+    q, idx = s.dev(s.q), s.idx()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    key = (torch.cuda.current_device(), side.cuda_stream)
+    sv.kv_cache._ws_cache.pop(key, None)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = sv.spec_kv_attention(q, cache, *idx, return_lse=True)
+    assert key not in sv.kv_cache._ws_cache
+    for _ in range(2):
+        with torch.cuda.stream(side):
+            direct = sv.spec_kv_attention(q, cache, *idx, return_lse=True)
+            graph.replay()
+        side.synchronize()
+        assert_attention(*direct, want)
+        assert_attention(*got, want)
+
+
+@gpu
 def test_python_checks():
     import speculative_sampling_verification_spec_gb300 as sv
     s = Setup(39, 2, 3, 4, 2, 64, 16, [5, 6], [3, 3], "bf16", 64)
