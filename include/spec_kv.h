@@ -120,7 +120,14 @@ size_t spec_kv_attention_workspace_size(const spec_kv_cache* cache, const spec_k
  *        t >= new_lens[b]
  *   lse  device float [B, T, Hq], contiguous, or NULL: log sum_j w_j (natural
  *        logarithm), -inf for slots t >= new_lens[b]
- * Sums and softmax statistics are float.  Tokens a query does not see have no
+ * Sums and softmax statistics are float.  float32 calls, and bfloat16 ones whose
+ * head size is not 64 or 128 or whose pool is laid out as no tensor map can be, hold
+ * queries and weights in float too.  The other bfloat16 calls run on 8-bit matrix
+ * products and hold them in 8-bit pieces: a query channel to 2^-17 of the largest of
+ * its row (2^-13, where rows of one sequence and head are within 16 times of each
+ * other); a weight to 2^-9 of itself, or to 2^-33 of the largest weight of its row
+ * where that is more.  Their running sums lose up to 2^-24 of themselves for each 32
+ * tokens.  Tokens a query does not see have no
  * influence on its output, whatever their slots hold; a NaN key or value that it
  * sees makes its output NaN (a value: in the affected channels at least).
  * Device errors: a sequence whose lengths are out of range gets NaN, and so does

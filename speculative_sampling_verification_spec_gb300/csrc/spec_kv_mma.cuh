@@ -15,20 +15,24 @@
 // take half of the rows each, four at a time, the first half in columns 0.. and
 // the second in columns NR / 2...
 //
-// What is not 8 bits is carried in two 8-bit pieces of 4 significant bits each:
-//   q / 2^e = hi + lo, two products into one accumulator (a bfloat16 has 8
+// What is not 8 bits is carried in 8-bit pieces:
+//   q / 2^e = hi + lo in e4m3, two products into one accumulator (a bfloat16 has 8
 //     significant bits: exact but for 2^-17 of the row's largest channel; rows
 //     within 2^kNear of each other share one e, for 2^-17 of the largest's, and
 //     one factor of the scores with it);
-//   p = hi + lo / 16, the pieces side by side as columns of one product and added
-//     at the end (a relative 2^-8 at most, 2^-10.6 on average; sums are of the
-//     float p).
+//   p = p0 + p1 / 8 + p2 / 64 in e5m2, the pieces side by side as columns of one
+//     product and added at the end (sums are of the float p).
+// Long contexts are full of small weights that only count together, so each weight
+// keeps its own precision: an error of 2^-9 of it at most down to 2^-24 of the
+// largest weight of its row in the range, and of 2^-33 of the largest below.  (Two
+// e4m3 pieces lost what lay under 2^-17 of it: 40 % of the output where a quarter of
+// the weight is spread evenly over 32768 tokens.)
 //
 // A thread of the softmax warps holds one token: the token's two scales are
 // scalars of the thread, applied to the scores in float (the value scale as
 // exponent of 2, so that p is the weight of the 8-bit values).  The running
 // maximum of a row is over the threads; it is not needed exactly, only as a
-// reference that keeps p within the 8-bit range, so it is raised (and the
+// reference that keeps p within the pieces' range, so it is raised (and the
 // accumulators rescaled) only when a weight would pass 2^kSlack times the one at
 // which it was set: about one tile in fifteen, and the first of an item.
 //
@@ -67,31 +71,34 @@ constexpr int kSoftThreads = 256;  // two groups of 128, a token a thread
 // KS + 2 <= 5 tiles ahead of the softmax (stages of keys, and two buffers of scores),
 // so at most five pieces with tiles, one more announced, then an empty one and the end.
 constexpr int kPieceRing = 8;
-constexpr int kScaleRing = 8;
 constexpr uint32_t kUnset = 0x80000000u;  // bits of -0: scores are taken as they are
 constexpr int kNear = 4;            // log2 of how far apart rows with one exponent may be
+constexpr int kTop = 15;            // log2 of the largest weight (e5m2 and half hold more than 2^15)
 constexpr int kSlack = 5;           // log2 of how far weights may pass the reference (3: 7 % slower at 36 rows)
-constexpr float kShift = 8 - kSlack;  // a raised reference is kShift below the largest score: weights stay within 2^8 < 448
+constexpr float kShift = kTop - kSlack;  // a raised reference is kShift below the largest score
+// The sums are of weights times this: with value scales down to 2^-100 those of 2^24 tokens stay finite.
+constexpr int kSumExp = 12;
+constexpr float kSumUnit = 1.0f / (1 << kSumExp);
+constexpr int kPieces = 3;          // of a weight
 
 // Stages of keys and of values, buffers of weights: what two CTAs an SM leave room
 // for.  Keys are used up two tiles ahead of the weights (the scores are
-// double-buffered), so values get the larger share (48 columns: 262 us with two and
-// three stages, 277 with three and two; with two and two and a second buffer of
-// weights 283).
+// double-buffered), so values get the larger share.
 template <int D, int NR>
 struct MmaCfg {
   static constexpr int kTileBytes = kTile * D;
   static constexpr int KS = D == 64 ? 3 : 2;
-  static constexpr int VS = D == 64 ? 5 : NR == 16 ? 4 : 3;
-  static constexpr int PB = (D == 64 || NR <= 32) ? 2 : 1;
-  static constexpr int kQBytes = NR * D;             // one piece
-  static constexpr int kPBytes = kTile * 2 * NR;     // both pieces
+  static constexpr int VS = D == 64 ? 5 : 3;
+  static constexpr int kScaleRing = KS == 2 ? 4 : 8;    // at least KS + 2: see kPieceRing
+  static constexpr int PB = D == 64 || NR == 16 ? 2 : 1;
+  static constexpr int kQBytes = NR * D;                // one piece
+  static constexpr int kPBytes = kTile * kPieces * NR;  // all pieces
   static constexpr int kOffV = 0;                    // values first: a 64-channel operand reads on into what follows
   static constexpr int kOffK = kOffV + VS * kTileBytes;
   static constexpr int kOffQ = kOffK + KS * kTileBytes;
   static constexpr int kOffP = kOffQ + 2 * kQBytes;
   static constexpr int kOffSmall = kOffP + PB * kPBytes;
-  static constexpr uint32_t kCols = NR == 16 ? 64 : NR == 32 ? 128 : 256;  // 2 x scores, 2 pieces of output
+  static constexpr uint32_t kCols = NR == 16 ? 128 : 256;  // 2 x scores, 3 pieces of output
 };
 
 template <int D, int NR>
@@ -102,12 +109,11 @@ struct MmaSmall {
   alignas(16) float refs[NR];     // negated references of the rows; kUnset: none yet
   alignas(16) float factor[NR];   // of the scores, where rows have exponents of their own
   uint32_t q_top, q_least;        // largest and least of the rows' largest magnitudes
-  float4 scales[kScaleRing][kTile / 16];  // of a page: key scale; value scale's log2 and reciprocal
-  int64_t out_at[NR];     // element of the output (of lse for `lse_at`) where a row begins
-  int64_t lse_at[NR];
-  alignas(16) float fac[NR];      // by which a rescaling multiplies, and what it raises references by
-  alignas(16) float up[NR];
-  alignas(16) float red[4][NR];
+  float4 scales[C::kScaleRing][kTile / 16];  // of a page: key scale; value scale's log2, and kSumUnit over it
+  int64_t out_at[NR];             // element of the output where a row begins
+  alignas(16) float red[4][NR];   // a row's maxima or sums by warp; then, by the thread that has read them,
+  __device__ float* up() { return red[0]; }   // what a rescaling raises the reference by,
+  __device__ float* fac() { return red[1]; }  // and what it multiplies by
   int pos[NR];
   RangePlan plan;
   int scratch[kMmaThreads / 32];
@@ -116,9 +122,13 @@ struct MmaSmall {
   Piece pieces[kPieceRing];  // from the loader to the other roles; b < 0: no more
 };
 
+// two CTAs share an SM's 228 KB, of which each takes 1 KB beside its own
+constexpr int kMostSmem = (228 / 2 - 1) * 1024;
 template <int D, int NR>
 constexpr int mma_smem_bytes() {
-  return MmaCfg<D, NR>::kOffSmall + static_cast<int>(sizeof(MmaSmall<D, NR>)) + 1024;
+  constexpr int bytes = MmaCfg<D, NR>::kOffSmall + static_cast<int>(sizeof(MmaSmall<D, NR>));
+  static_assert(bytes <= kMostSmem, "two CTAs an SM");
+  return bytes;
 }
 
 // tensor maps of the pool: the channel, then token, head and page in the order of
@@ -202,14 +212,24 @@ __device__ __forceinline__ int order_of(float x) {
 }
 __device__ __forceinline__ float of_order(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
-// the e4m3 codes of two floats' nearest halves, and of 16 times what they leave over
-__device__ __forceinline__ void two_pieces(float w0, float w1, uint32_t& hi, uint32_t& lo) {
+// Two weights as halves, in three pieces whose bytes are those of e5m2: a half's upper byte is an e5m2 (of the half
+// rounded towards zero, 3 significant bits), so the first piece is the half without its lower byte; the second is that of
+// eight times what it leaves, exactly; the third the nearest to eight times what that leaves.  a and b get the first two
+// pieces in their upper bytes, c the third in two bytes.
+__device__ __forceinline__ void three_pieces(float w0, float w1, uint32_t& a, uint32_t& b, uint32_t& c) {
+  const auto bits = [](__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); };
+  const auto upper = [&](__half2 x, uint32_t& u) {
+    u = bits(x) & 0xff00ff00u;
+    return *reinterpret_cast<const __half2*>(&u);
+  };
+  const __half2 eight = __half2half2(__ushort_as_half(0x4800));
   const __half2 h = __floats2half2_rn(w0, w1);
-  hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
-  const __half2 b(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3));
-  const __half2 d = __hmul2(__hsub2(h, b), __half2half2(__ushort_as_half(0x4c00)));  // x 16
-  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(d), __NV_SATFINITE, __NV_E4M3);
+  const __half2 d = __hmul2(__hsub2(h, upper(h, a)), eight);
+  const __half2 e = __hmul2(__hsub2(d, upper(d, b)), eight);
+  c = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(e), __NV_SATFINITE, __NV_E5M2);
 }
+// the upper bytes of the halves of x and y, in order
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t x, uint32_t y) { return __byte_perm(x, y, 0x7531); }
 
 // 8 channels of a row that is not aligned, as if loaded 16 bytes at a time
 static __device__ __noinline__ Raw<__nv_bfloat16, 8> gather8(const __nv_bfloat16* src) {
@@ -256,8 +276,7 @@ template <int D, int NR, int RU>
 __global__ void __launch_bounds__(kMmaThreads, 2)
     spec_kv_attention_mma_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ MmaMaps maps) {
   using C = MmaCfg<D, NR>;
-  extern __shared__ uint8_t dyn_raw[];
-  uint8_t* dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t dyn[];  // the swizzles repeat every 1024 bytes
   MmaSmall<D, NR>& sm = *reinterpret_cast<MmaSmall<D, NR>*>(dyn + C::kOffSmall);
   uint8_t* const sv = dyn + C::kOffV;
   uint8_t* const sk = dyn + C::kOffK;
@@ -375,7 +394,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           // the tile's scales come with its keys: the arrival that the copies' bytes wait for is after them
           if (mine >= 0 && mine < np) {
             const float v = sc.y < 7.8886090522101181e-31f ? 7.8886090522101181e-31f : sc.y;  // 2^-100
-            sm.scales[n % kScaleRing][mine] = make_float4(sc.x, log2f(v), 1.0f / v, 0.0f);
+            sm.scales[n % C::kScaleRing][mine] = make_float4(sc.x, log2f(v), kSumUnit / v, 0.0f);
           }
           __syncwarp();
           if (lane == 0) bar_arrive_expect(&sm.k_full[ks], cnt * page_bytes);
@@ -405,8 +424,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       // ------------------------------------------------------------- products
       if (lane == 0) {
         const uint32_t q0 = smem_u32(sq), k0 = smem_u32(sk), v0 = smem_u32(sv), p0 = smem_u32(sp);
-        constexpr uint32_t kDescS = instr_desc(128, NR, false, false);
-        constexpr uint32_t kDescO = instr_desc(128, 2 * NR, true, true);
+        constexpr uint32_t kDescS = instr_desc(128, NR, false, false, kE4m3);
+        constexpr uint32_t kDescO = instr_desc(128, kPieces * NR, true, true, kE5m2);
         bool ok = true;
         int queries = 0;
         const auto scores = [&](int i) {
@@ -466,7 +485,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       constexpr int CH = 4;              // rows at a time
       const int group = warp >> 2, token = tid & 127, r_base = group * RT;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;  // tensor memory lanes of this warp
-      const uint32_t tO = tm + lanes + 2 * NR + r_base;                     // first pieces; the second NR further
+      const uint32_t tO = tm + lanes + 2 * NR + r_base;                     // first pieces; the others NR and 2 NR further
       bool fail = false;
       for (;; ++pieces) {
         // the piece stays in shared memory, out of the registers that the loop over the tiles needs
@@ -495,7 +514,6 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           const int gr = p.row0 + r, t = gr / a.G, g = gr - t * a.G;
           sm.pos[tid] = row ? p.L + t : -1;
           sm.out_at[tid] = p.b * a.o_seq + t * a.o_tok + (p.h * a.G + g) * a.o_head;
-          sm.lse_at[tid] = (static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g;
         }
         bool one_factor = true;
         float factor = 0.0f;
@@ -593,7 +611,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           // tiles back (issued before them): with two buffers of weights this one's is free
           if (!fail) fail = !bar_wait(&sm.s_full[n & 1], (n >> 1) & 1, gave_up);
           tc_fence_after();
-          float4 sc = sm.scales[n % kScaleRing][token >> a.log_page];
+          float4 sc = sm.scales[n % C::kScaleRing][token >> a.log_page];
           const bool edge = t >= t_edge || t <= t_win;
           bool poison = false;
           if (edge) {
@@ -658,8 +676,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
 #pragma unroll
           for (int c = 0; c < RU; c += CH)
             if (c < fours) top = fmaxf(fmaxf(top, fmaxf(x[c], x[c + 1])), fmaxf(x[c + 2], x[c + 3]));
-          // would some weight leave the 8-bit range, or has some row no reference yet?
-          if (group_any(group, top > 8.0f || t <= t_unset)) {
+          // would some weight leave the pieces' range, or has some row no reference yet?
+          if (group_any(group, top > static_cast<float>(kTop) || t <= t_unset)) {
             float most = -INFINITY;  // of row `lane`, over the warp's tokens
 #pragma unroll
             for (int c = 0; c < RU; c += CH) {
@@ -680,8 +698,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
               const bool unset = __float_as_uint(ref) == kUnset;
               // raised by: nothing for a row that no token of this tile belongs to
               const float up = unset ? (now == -INFINITY ? 0.0f : now) : fmaxf(now, 0.0f);
-              sm.up[r] = up;
-              sm.fac[r] = unset ? 1.0f : ex2(-up);
+              sm.up()[r] = up;
+              sm.fac()[r] = unset ? 1.0f : ex2(-up);
               // 0 - x is never the mark of an unset reference
               sm.refs[r] = unset && now == -INFINITY ? ref : (unset ? 0.0f : ref) - up;
             }
@@ -689,7 +707,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
 #pragma unroll
             for (int c = 0; c < RU; c += CH) {
               if (c < fours) {
-                const float4 u = *reinterpret_cast<const float4*>(&sm.up[r_base + c]);
+                const float4 u = *reinterpret_cast<const float4*>(&sm.up()[r_base + c]);
                 x[c] -= u.x;
                 x[c + 1] -= u.y;
                 x[c + 2] -= u.z;
@@ -700,7 +718,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
 #pragma unroll
               for (int c = 0; c < RU; c += CH) {
                 if (c < fours) {
-                  const float4 f = *reinterpret_cast<const float4*>(&sm.fac[r_base + c]);
+                  const float4 f = *reinterpret_cast<const float4*>(&sm.fac()[r_base + c]);
                   l[c] *= f.x;
                   l[c + 1] *= f.y;
                   l[c + 2] *= f.z;
@@ -711,58 +729,57 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
               tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < fours; c += 8) {  // (past the last row, what is there is not used)
-                float o[16];
-                tmem_ld<8>(tO + c, o);
-                tmem_ld<8>(tO + NR + c, o + 8);
-                tmem_wait_ld();
-                tmem_tie<16>(o);
+#pragma unroll 1
+                for (uint32_t at = tO + c; at < tO + c + kPieces * NR; at += NR) {
+                  float o[8];
+                  tmem_ld<8>(at, o);
+                  tmem_wait_ld();
+                  tmem_tie<8>(o);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  o[i] *= sm.fac[r_base + c + i];
-                  o[8 + i] *= sm.fac[r_base + c + i];
+                  for (int i = 0; i < 8; ++i) o[i] *= sm.fac()[r_base + c + i];
+                  tmem_st<8>(at, o);
                 }
-                tmem_st<8>(tO + c, o);
-                tmem_st<8>(tO + NR + c, o + 8);
               }
               tmem_wait_st();
             }
           }
-          // weights: two 8-bit pieces each, 16 rows of a token side by side
+          // weights: three 8-bit pieces each, 16 rows of a token side by side
           if (C::PB == 1 && n > 0 && !fail) fail = !bar_wait(&sm.pv_done[0], (n - 1) & 1, gave_up);
           uint8_t* dst = sp + (n % C::PB) * C::kPBytes + token * 16;
+          constexpr int kNext = (NR / 16) * (kTile * 16);  // from a piece to the next
 #pragma unroll
           for (int c = 0; c < RT; c += 16) {
             constexpr int kLast = RT % 16 ? 8 : 16;
             const int n16 = c + 16 <= RT ? 16 : kLast;
-            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+            uint32_t w[kPieces][4] = {};
 #pragma unroll
             for (int i = 0; i < 16; i += CH) {
               if (i < n16 && c + i < RU && c + i < fours) {
-                uint32_t h[2], d[2];
+                uint32_t u[kPieces][2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const int r = c + i + 2 * e;
                   const float w0 = ex2(x[r]), w1 = ex2(x[r + 1]);
                   unpack2(fma2(pack2(w0, w1), ivs2, pack2(l[r], l[r + 1])), l[r], l[r + 1]);
-                  two_pieces(w0, w1, h[e], d[e]);
+                  three_pieces(w0, w1, u[0][e], u[1][e], u[2][e]);
                 }
-                hi[i / 4] = h[0] | (h[1] << 16);
-                lo[i / 4] = d[0] | (d[1] << 16);
+                w[0][i / 4] = upper_bytes(u[0][0], u[0][1]);
+                w[1][i / 4] = upper_bytes(u[1][0], u[1][1]);
+                w[2][i / 4] = u[2][0] | (u[2][1] << 16);
               }
             }
             const int col = r_base + c;
             uint8_t* at = dst + (col / 16) * (kTile * 16) + (col % 16);
-            constexpr int kLoAt = (NR / 16) * (kTile * 16);
-            if (RT % 16 == 0) {
-              *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(at + kLoAt) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            } else {  // eight columns at a time: a block of 16 may be shared with the other group
-              *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(at + kLoAt) = make_uint2(lo[0], lo[1]);
-              if (n16 == 16) {
-                uint8_t* next = dst + ((col + 8) / 16) * (kTile * 16) + ((col + 8) % 16);
-                *reinterpret_cast<uint2*>(next) = make_uint2(hi[2], hi[3]);
-                *reinterpret_cast<uint2*>(next + kLoAt) = make_uint2(lo[2], lo[3]);
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+              if (RT % 16 == 0) {
+                *reinterpret_cast<uint4*>(at + k * kNext) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+              } else {  // eight columns at a time: a block of 16 may be shared with the other group
+                *reinterpret_cast<uint2*>(at + k * kNext) = make_uint2(w[k][0], w[k][1]);
+                if (n16 == 16) {
+                  uint8_t* next = dst + ((col + 8) / 16) * (kTile * 16) + ((col + 8) % 16);
+                  *reinterpret_cast<uint2*>(next + k * kNext) = make_uint2(w[k][2], w[k][3]);
+                }
               }
             }
           }
@@ -789,12 +806,13 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         }
         soft_sync();
         if (tid < NR && row_of(tid) < p.nrows) {
-          const float ref = m > 0 && __float_as_uint(sm.refs[tid]) != kUnset ? -sm.refs[tid] : kNoRef;
+          const float ref = (m > 0 && __float_as_uint(sm.refs[tid]) != kUnset ? -sm.refs[tid] : kNoRef) + kSumExp;
           float s = sm.red[0][tid] + sm.red[1][tid] + sm.red[2][tid] + sm.red[3][tid];
           if (fail) s = __uint_as_float(0x7fc00000u);
           if (p.whole()) {
-            if (a.lse) a.lse[sm.lse_at[tid]] = lse_of(ref, s);
-            sm.fac[tid] = 1.0f / s;
+            const int gr = p.row0 + row_of(tid), t = gr / a.G, g = gr - t * a.G;
+            if (a.lse) a.lse[(static_cast<int64_t>(p.b) * a.T + t) * a.Hq + p.h * a.G + g] = lse_of(ref, s);
+            sm.fac()[tid] = kSumUnit / s;
           } else {
             a.part_ml[static_cast<int64_t>(p.slot) * a.slot_rows + row_of(tid)] = make_float2(ref, s);
           }
@@ -807,20 +825,23 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + token;
 #pragma unroll 1
           for (int c = 0; c < fours; c += 8) {
-            float o[16];  // both pieces of eight rows
+            float o[8], o1[8], o2[8];  // the pieces of eight rows
             tmem_ld<8>(tO + c, o);
-            tmem_ld<8>(tO + NR + c, o + 8);
+            tmem_ld<8>(tO + NR + c, o1);
+            tmem_ld<8>(tO + 2 * NR + c, o2);
             tmem_wait_ld();
-            tmem_tie<16>(o);
+            tmem_tie<8>(o);
+            tmem_tie<8>(o1);
+            tmem_tie<8>(o2);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = fmaf(o[8 + i], 0.0625f, o[i]);
+            for (int i = 0; i < 8; ++i) o[i] = fmaf(fmaf(o2[i], 0.125f, o1[i]), 0.125f, o[i]);
             if (whole) {
               int64_t at[8];  // (read before the stores, which for all the compiler knows write there)
               float f[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 at[i] = sm.out_at[r_base + c + i];
-                f[i] = sm.fac[r_base + c + i];
+                f[i] = sm.fac()[r_base + c + i];
               }
 #pragma unroll
               for (int i = 0; i < 8; ++i)
@@ -828,7 +849,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if (c + i < mine) part[(c + i) * D] = o[i];
+                if (c + i < mine) part[(c + i) * D] = o[i] * kSumUnit;
             }
           }
         }

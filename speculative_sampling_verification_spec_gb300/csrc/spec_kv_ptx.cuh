@@ -111,22 +111,6 @@ template <>
 __device__ __forceinline__ void tmem_tie<8>(float* x) {
   asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]));
 }
-template <>
-__device__ __forceinline__ void tmem_ld<16>(uint32_t addr, float* x) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
-               : "r"(addr));
-}
-template <>
-__device__ __forceinline__ void tmem_st<16>(uint32_t addr, const float* x) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(x[8]), "f"(x[9]), "f"(x[10]), "f"(x[11]), "f"(x[12]), "f"(x[13]), "f"(x[14]), "f"(x[15])
-               : "memory");
-}
-// nothing that uses these values moves ahead of the wait before it
-template <>
-__device__ __forceinline__ void tmem_tie<16>(float* x) {
-  asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]), "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]));
-}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -141,11 +125,12 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead_by
          (static_cast<uint64_t>((stride_bytes >> 4) & 0x3fffu) << 32) | (uint64_t(1) << 46) |
          (static_cast<uint64_t>(swizzle) << 61);
 }
-// Instruction descriptor: e4m3 operands, float accumulators, M x N; an operand is
-// K-major (its K runs along the contiguous bytes) or else transposed.
-__host__ __device__ constexpr uint32_t instr_desc(int M, int N, bool a_transposed, bool b_transposed) {
-  return (1u << 4) | ((a_transposed ? 1u : 0u) << 15) | ((b_transposed ? 1u : 0u) << 16) |
-         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// Instruction descriptor: e4m3 times e4m3 or e5m2, float accumulators, M x N; an
+// operand is K-major (its K runs along the contiguous bytes) or else transposed.
+enum { kE4m3 = 0, kE5m2 = 1 };
+__host__ __device__ constexpr uint32_t instr_desc(int M, int N, bool a_transposed, bool b_transposed, int b_type) {
+  return (1u << 4) | (static_cast<uint32_t>(b_type) << 10) | ((a_transposed ? 1u : 0u) << 15) |
+         ((b_transposed ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 // D (+)= A B, 32 of K at a time; one thread issues it
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
