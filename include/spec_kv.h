@@ -131,8 +131,9 @@ size_t spec_kv_attention_workspace_size(const spec_kv_cache* cache, const spec_k
  * influence on its output, whatever their slots hold; a NaN key or value that it
  * sees makes its output NaN (a value: in the affected channels at least).
  * Device errors: a sequence whose lengths are out of range gets NaN, and so does
- * a row that reads a page outside [0, num_pages); both store
- * SPEC_ERR_CACHE_RANGE in *status.  A bounded wait that runs out (about two
+ * a row that sees a token of a page outside [0, num_pages); both store
+ * SPEC_ERR_CACHE_RANGE in *status.  Entries of the table for pages that lie wholly
+ * before what any query of the sequence sees through its window may hold anything.  A bounded wait that runs out (about two
  * seconds) gives NaN and SPEC_ERR_TIMEOUT. */
 spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const spec_kv_params* params, void* out,
                               float* lse);

@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
     const auto fetch = [&](int base, int page) {
       ks = vs = __uint_as_float(0x7fc00000u);  // a page that is not the pool's
       const bool ok = base < j1 && page >= 0;
-      if (base < j1 && page < 0 && lane == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+      if (base < j1 && page < 0 && lane == 0 && (((base >> a.log_page) + 1) << a.log_page) > p.first)
+        report(a.status, SPEC_ERR_CACHE_RANGE);
       if (ok) {
         const int64_t at = page * a.scale_page_stride + p.h * a.scale_head_stride;
         ks = a.k_scale[at];

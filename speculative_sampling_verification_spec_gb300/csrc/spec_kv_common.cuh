@@ -178,6 +178,7 @@ struct Piece {
   int L, n;          // tokens before the new ones; new tokens
   int row0, nrows;   // rows of this row tile
   int tile0, tile1;  // absolute tiles [tile0, tile1); may be empty
+  int first;         // first position that a row sees
   int c0, c1;        // first and last range that hold tiles of the item
   int slot;          // where a partial result goes, when these differ
   __device__ bool whole() const { return c0 == c1; }
@@ -235,6 +236,7 @@ __device__ __forceinline__ bool walk_next(const KvArgs& a, Walk& k, Piece& p) {
     const int t_first = p.row0 / a.G, t_last = (p.row0 + p.nrows - 1) / a.G;
     const int hi = ((s.L + t_last) >> a.log_tile) + 1;
     const int lo = (a.window > 0 && s.L + t_first + 1 > a.window) ? s.L + t_first + 1 - a.window : 0;
+    p.first = lo;
     p.tile0 = max(s.t0 + t0, lo >> a.log_tile);
     p.tile1 = min(s.t0 + t1, hi);
     if (p.tile1 < p.tile0) p.tile1 = p.tile0;
@@ -243,7 +245,8 @@ __device__ __forceinline__ bool walk_next(const KvArgs& a, Walk& k, Piece& p) {
   return false;
 }
 
-// page number of a token's page, -1 where it is not one of the pool's
+// page number of a token's page, -1 where it is not one of the pool's (an error
+// only if some row sees a token of it: a tile may begin before the window)
 __device__ __forceinline__ int page_of(const KvArgs& a, int b, int page_index) {
   const int pid = a.table[b * a.table_stride + page_index];
   return (pid >= 0 && pid < a.num_pages) ? pid : -1;

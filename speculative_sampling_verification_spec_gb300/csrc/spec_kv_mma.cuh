@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           int pid = 0;
           if (base + lane < last) {
             pid = page_of(a, p.b, base + lane);
-            if (pid < 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+            if (pid < 0 && ((base + lane + 1) << a.log_page) > p.first) report(a.status, SPEC_ERR_CACHE_RANGE);
           }
           return pid;
         };
