@@ -24,8 +24,9 @@
  * page_table[b * table_stride + p / page_size], slot p % page_size.  Keys and
  * values are e4m3 codes; the value a code stands for is code * scale, with one
  * float scale for each (page, key/value head), for keys and values apart.
- * Appending chooses powers of two for the scales; attention takes any positive
- * finite ones (values below 2^-100 count as 2^-100).
+ * Appending chooses powers of two for the scales; attention takes any from 2^-100
+ * to 2^100.  Smaller ones may count as 2^-100, and a value scale as 2^-80 times the
+ * largest one of the sequence and head where it is below that.
  */
 #ifndef SPEC_KV_H
 #define SPEC_KV_H

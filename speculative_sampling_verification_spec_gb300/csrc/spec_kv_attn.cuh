@@ -94,20 +94,22 @@ __device__ __forceinline__ void add_parts(const KvArgs& a, int rt, int r, int c0
           }
           have_top = true;
         }
-        wl = exp2f(ml.x - top);
+        wl = exp2f(0.5f * (ml.x - top));
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const float w = __shfl_sync(kFull, wl, i0 + i), li = __shfl_sync(kFull, ml.y, i0 + i);
         // a part without tokens for this row left no output
         if (i0 + i >= m || li == 0.0f) continue;
-        l = fmaf(w, li, l);
+        // (references take in the values' scales, so a part far below the top may still have a large sum)
+        l = fmaf(w, w * li, l);
+        const float ww = w * w;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          acc[k].x = fmaf(w, x[i][k].x, acc[k].x);
-          acc[k].y = fmaf(w, x[i][k].y, acc[k].y);
-          acc[k].z = fmaf(w, x[i][k].z, acc[k].z);
-          acc[k].w = fmaf(w, x[i][k].w, acc[k].w);
+          acc[k].x = fmaf(ww, x[i][k].x, acc[k].x);
+          acc[k].y = fmaf(ww, x[i][k].y, acc[k].y);
+          acc[k].z = fmaf(ww, x[i][k].z, acc[k].z);
+          acc[k].w = fmaf(ww, x[i][k].w, acc[k].w);
         }
       }
     }

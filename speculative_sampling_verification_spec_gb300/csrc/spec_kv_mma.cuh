@@ -80,6 +80,9 @@ constexpr float kShift = kTop - kSlack;  // a raised reference is kShift below t
 constexpr int kSumExp = 12;
 constexpr float kSumUnit = 1.0f / (1 << kSumExp);
 constexpr int kPieces = 3;          // of a weight
+// Value scales count as this times the largest that came before them in the piece, at least:
+// below, a token's weight would leave the float range on its way to the sum.
+constexpr float kLeastOfTop = 1.0f / (1ull << 40) / (1ull << 40);
 
 // Stages of keys and of values, buffers of weights: what two CTAs an SM leave room
 // for.  Keys are used up two tiles ahead of the weights (the scores are
@@ -113,7 +116,8 @@ struct MmaSmall {
   int64_t out_at[NR];             // element of the output where a row begins
   alignas(16) float red[4][NR];   // a row's maxima or sums by warp; then, by the thread that has read them,
   __device__ float* up() { return red[0]; }   // what a rescaling raises the reference by,
-  __device__ float* fac() { return red[1]; }  // and what it multiplies by
+  __device__ float* fac() { return red[1]; }  // what it multiplies by,
+  __device__ float* root() { return red[2]; }  // and the root of that
   int pos[NR];
   RangePlan plan;
   int scratch[kMmaThreads / 32];
@@ -366,6 +370,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           }
           return s;
         };
+        uint32_t v_top = 0;  // bits of the largest value scale so far
         int base = first;
         int pid = number(base), pid_next = 0;
         float2 sc = scales(base, pid), sc_next = make_float2(0.0f, 0.0f);
@@ -392,8 +397,13 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           if (has)
             tma_load_4d(sk + ks * C::kTileBytes + mine * page_bytes, &maps.k, 0, y, z, w, &sm.k_full[ks], policy);
           // the tile's scales come with its keys: the arrival that the copies' bytes wait for is after them
+          if (in == 0) {
+            const bool counts = base + lane < last && sc.y > 0.0f && is_finite(sc.y);
+            v_top = max(v_top, __reduce_max_sync(kFull, counts ? __float_as_uint(sc.y) : 0u));
+          }
           if (mine >= 0 && mine < np) {
-            const float v = sc.y < 7.8886090522101181e-31f ? 7.8886090522101181e-31f : sc.y;  // 2^-100
+            const float least = fmaxf(7.8886090522101181e-31f, __uint_as_float(v_top) * kLeastOfTop);  // 2^-100
+            const float v = sc.y < least ? least : sc.y;
             sm.scales[n % C::kScaleRing][mine] = make_float4(sc.x, log2f(v), kSumUnit / v, 0.0f);
           }
           __syncwarp();
@@ -700,6 +710,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
               const float up = unset ? (now == -INFINITY ? 0.0f : now) : fmaxf(now, 0.0f);
               sm.up()[r] = up;
               sm.fac()[r] = unset ? 1.0f : ex2(-up);
+              sm.root()[r] = unset ? 1.0f : ex2(-0.5f * up);
               // 0 - x is never the mark of an unset reference
               sm.refs[r] = unset && now == -INFINITY ? ref : (unset ? 0.0f : ref) - up;
             }
@@ -718,11 +729,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
 #pragma unroll
               for (int c = 0; c < RU; c += CH) {
                 if (c < fours) {
-                  const float4 f = *reinterpret_cast<const float4*>(&sm.fac()[r_base + c]);
-                  l[c] *= f.x;
-                  l[c + 1] *= f.y;
-                  l[c + 2] *= f.z;
-                  l[c + 3] *= f.w;
+                  const float4 f = *reinterpret_cast<const float4*>(&sm.root()[r_base + c]);
+                  l[c] = l[c] * f.x * f.x;  // (a large value scale may raise a reference beyond the float range)
+                  l[c + 1] = l[c + 1] * f.y * f.y;
+                  l[c + 2] = l[c + 2] * f.z * f.z;
+                  l[c + 3] = l[c + 3] * f.w * f.w;
                 }
               }
               if (!fail) fail = !bar_wait(&sm.pv_done[(n - 1) % C::PB], ((n - 1) / C::PB) & 1, gave_up);

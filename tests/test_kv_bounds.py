@@ -37,3 +37,32 @@ def test_pages_before_the_window_may_be_gone(T, Hq, Hkv, D, S, seq, window, dtyp
     out, lse = sv.spec_kv_attention(q, cache, table, lens, new, window=window, return_lse=True, status=status)
     assert status.item() == 8
     assert torch.isnan(out[0, 0]).all() and torch.isnan(lse[0, 0]).all() and torch.isfinite(out[1]).all()
+
+
+@gpu
+@pytest.mark.parametrize("order", ["small first", "large first", "alternating"])
+@pytest.mark.parametrize("large,small", [(60, -100), (20, -100), (120, -100), (120, 10)])
+@pytest.mark.parametrize("B", [1, 304])         # one sequence cut into many ranges, or one range for each
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+def test_value_scales_far_apart(order, large, small, B, dtype, D):
+    """Half of the pages have value scales of 2^large, half of 2^small (what an append of zeros leaves): the tokens of
+    both count in the sum of the weights."""
+    import speculative_sampling_verification_spec_gb300 as sv
+    g = torch.Generator(device="cuda").manual_seed(5)
+    S, n = 16, 1024
+    pages = n // S
+    i = torch.arange(pages, device="cuda")
+    big = {"small first": i >= pages // 2, "large first": i < pages // 2, "alternating": i % 2 == 0}[order]
+    kc, vc = (torch.randn(pages, 1, S, D, generator=g, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    vs = torch.where(big, 2.0 ** large, 2.0 ** small).double().float()[:, None].contiguous()
+    q = torch.randn(1, 1, 4, D, generator=g, device="cuda").expand(B, 1, 4, D).to(DT[dtype])
+    table = i.to(torch.int32).expand(B, pages).contiguous()
+    seq = torch.full((B,), n - 1, dtype=torch.int32, device="cuda")
+    cache = sv.PagedKVCache(kc, vc, torch.ones_like(vs), vs)
+    out, lse = sv.spec_kv_attention(q, cache, table, seq, scale=0.1, return_lse=True)
+    k, v = kc.double().reshape(n, D), (vc.double() * vs.double()[:, :, None, None]).reshape(n, D)
+    s = q[0, 0].double() @ k.T * 0.1
+    w = torch.softmax(s, 1)
+    tol = (2.0 ** -8 if dtype == "bf16" else 2.0 ** -15) * (w @ v.abs()) + 2.0 ** -9 * (w @ v).abs()
+    assert ((out[:, 0].double() - w @ v).abs() <= tol).all()
+    assert ((lse[:, 0].double() - torch.logsumexp(s, 1)).abs() <= 2.0 ** -11).all()
