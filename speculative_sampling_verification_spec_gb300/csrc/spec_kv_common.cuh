@@ -25,7 +25,7 @@ namespace spec_kv_detail {
 
 constexpr int kTile = 128;          // tokens of a tensor-core tile
 constexpr int kMinScaleExp = -100;  // scales are at least 2^kMinScaleExp
-constexpr float kNoRef = -1e30f;    // softmax reference before any token
+constexpr float kNoRef = -3.4028234663852886e38f;  // softmax reference before any token: the lowest float
 constexpr unsigned kFull = 0xffffffffu;
 
 struct KvArgs {

@@ -66,3 +66,50 @@ def test_value_scales_far_apart(order, large, small, B, dtype, D):
     tol = (2.0 ** -8 if dtype == "bf16" else 2.0 ** -15) * (w @ v.abs()) + 2.0 ** -9 * (w @ v).abs()
     assert ((out[:, 0].double() - w @ v).abs() <= tol).all()
     assert ((lse[:, 0].double() - torch.logsumexp(s, 1)).abs() <= 2.0 ** -11).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 80), ("f32", 64), ("f32", 256)])
+@pytest.mark.parametrize("n", [3, 100, 9000])
+@pytest.mark.parametrize("size", [1e20, 1e32])
+def test_scores_far_below_zero(dtype, D, n, size):
+    """Scores of -2 * size for one token and -4 * size and less for the others: all of the weight is the one's."""
+    import speculative_sampling_verification_spec_gb300 as sv
+    g = torch.Generator(device="cuda").manual_seed(6)
+    S, pages = 16, -(-n // 16)
+    k = torch.randint(4, 9, (pages, 1, S, D), generator=g, device="cuda").float()
+    at = n // 3
+    k[at // S, 0, at % S] = 2
+    v = torch.randn(pages, 1, S, D, generator=g, device="cuda").to(torch.float8_e4m3fn)
+    one = torch.ones(pages, 1, device="cuda")
+    cache = sv.PagedKVCache(k.to(torch.float8_e4m3fn), v, one, one.clone())
+    q = torch.zeros(1, 1, 2, D, device="cuda")
+    q[..., 0] = -size
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    seq = torch.full((1,), n - 1, dtype=torch.int32, device="cuda")
+    q = q.to(DT[dtype])
+    out, lse = sv.spec_kv_attention(q, cache, table, seq, scale=1.0, return_lse=True)
+    assert torch.equal(out[0, 0].float(), v[at // S, 0, at % S].float().expand(2, D))
+    want = 2 * q[0, 0, 0, 0].double().item()
+    assert (lse.double() / want - 1).abs().max().item() < 1e-6
+
+
+@gpu
+def test_far_joined_parts():
+    """Parts whose largest scores are far apart: the lower ones add nothing, whatever their size."""
+    import speculative_sampling_verification_spec_gb300 as sv
+    n, S, D = 4096, 16, 64
+    for dtype in ("bf16", "f32"):
+        k = torch.zeros(n // S, 1, S, D, device="cuda")
+        k.view(n, D)[:, 0] = torch.where(torch.arange(n, device="cuda") < n // 2, 448.0, -448.0)
+        v = torch.ones(n // S, 1, S, D, device="cuda")
+        v.view(n, D)[n // 2:] = 2.0
+        one = torch.ones(n // S, 1, device="cuda")
+        cache = sv.PagedKVCache(k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn), one, one.clone())
+        table = torch.arange(n // S, dtype=torch.int32, device="cuda")[None]
+        seq = torch.full((1,), n - 1, dtype=torch.int32, device="cuda")
+        for sign, want in ((1.0, 1.0), (-1.0, 2.0)):
+            q = torch.zeros(1, 1, 2, D, device="cuda")
+            q[..., 0] = sign * 2.0 ** 100
+            out = sv.spec_kv_attention(q.to(DT[dtype]), cache, table, seq, scale=1.0)
+            assert (out.float() == want).all()
