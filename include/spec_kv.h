@@ -15,8 +15,8 @@
  * Dropping rejected tokens is a smaller length at the next call: the next
  * append writes over them.
  *
- * Conventions: those of spec_verify.h.  The caller owns every buffer, calls are
- * asynchronous on params->stream, host-side argument errors are returned before
+ * Conventions: those of spec_verify.h.  The caller owns every buffer, which is on
+ * the current device like the stream; calls are asynchronous on params->stream, host-side argument errors are returned before
  * anything is launched, and device-side errors never trap (see each entry).
  *
  * The cache.  A pool of pages of page_size token slots each, shared by all

@@ -88,6 +88,12 @@ class PagedKVCache:
 
 # the current stream's handle without building a Stream object, where torch offers it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _check_stream(stream, device):
+    if stream is not None and stream.device != device:
+        raise ValueError("stream is on %s, the cache on %s" % (stream.device, device))
 
 
 def _stream_of(stream, device):
@@ -183,7 +189,12 @@ def spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens=None, *, cos_s
     tokens, at most T (None: T each).  cos_sin float32 [positions, rot_dim]: cosines of a position's angles, then their
     sines (None: no rotation); interleaved: pairs are neighbouring channels, else channels i and i + rot_dim / 2.
     Returns the rotated queries (q_out, or a new contiguous tensor; zero in slots past new_lens); q_out may be q.
-    The cache is written in place."""
+    The cache is written in place.  The call runs on the cache's device, whichever is current."""
+    if _current_device() != cache._index:
+        with torch.cuda.device(cache._index):
+            return spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens, cos_sin=cos_sin,
+                                  interleaved=interleaved, q_out=q_out, status=status, stream=stream)
+    _check_stream(stream, cache.device)
     dtype = _first_check("k", k, "kv_heads")
     shape, dt, dev, index = k.shape, k.dtype, cache.device, cache._index
     B, T, hq, D = shape
@@ -231,7 +242,13 @@ def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=No
     new tokens.  scale: factor of the scores (1 / sqrt(D)); window > 0: a query sees that many tokens, its own
     included.  Returns out [B, T, Hq, D] (zero in slots past new_lens), or (out, lse) with lse [B, T, Hq] float32, the
     natural logarithm of the sum of the weights, when return_lse or lse is given.  ws: a workspace of
-    spec_kv_attention_workspace_size bytes (uint8, CUDA, zeroed once); by default one is kept for each stream."""
+    spec_kv_attention_workspace_size bytes (uint8, CUDA, zeroed once); by default one is kept for each stream.  The
+    call runs on the cache's device, whichever is current."""
+    if _current_device() != cache._index:
+        with torch.cuda.device(cache._index):
+            return spec_kv_attention(q, cache, page_table, seq_lens, new_lens, scale=scale, window=window, out=out,
+                                     lse=lse, return_lse=return_lse, status=status, ws=ws, stream=stream)
+    _check_stream(stream, cache.device)
     dtype = _first_check("q", q, "Hq")
     shape, dt, dev, index = q.shape, q.dtype, cache.device, cache._index
     B, T, hq, D = shape

@@ -113,3 +113,63 @@ def test_far_joined_parts():
             q[..., 0] = sign * 2.0 ** 100
             out = sv.spec_kv_attention(q.to(DT[dtype]), cache, table, seq, scale=1.0)
             assert (out.float() == want).all()
+
+
+class _OtherDevice:
+    """Stands in for torch's notion of the current device: `index` until torch.cuda.device is entered."""
+
+    def __init__(self, monkeypatch, kv_cache, index):
+        self.now, self.entered = index, []
+        monkeypatch.setattr(kv_cache, "_current_device", lambda: self.now)
+        outer = self
+
+        class Device:
+            def __init__(self, i):
+                self.i = i
+
+            def __enter__(self):
+                outer.entered.append(self.i)
+                self.before, outer.now = outer.now, self.i
+
+            def __exit__(self, *exc):
+                outer.now = self.before
+
+        monkeypatch.setattr(torch.cuda, "device", Device)
+
+
+@gpu
+def test_calls_run_on_the_caches_device(monkeypatch):
+    """With another device current, a call makes the cache's current for its time (a launch goes to the current device,
+    whatever the tensors' is); with the cache's current it leaves things as they are."""
+    import speculative_sampling_verification_spec_gb300 as sv
+    s = Setup(310, 2, 3, 4, 2, 64, 16, [5, 100], [3, 2], "bf16")
+    a, b = s.cache(), s.cache()
+    idx, q, k, v = s.idx(), s.dev(s.q), s.dev(s.k), s.dev(s.v)
+    sv.spec_kv_append(q, k, v, a, *idx)
+    want = sv.spec_kv_attention(q, a, *idx, return_lse=True)
+    here = a.device.index
+    other = _OtherDevice(monkeypatch, sv.kv_cache, here + 1)
+    sv.spec_kv_append(q, k, v, b, *idx)
+    assert other.entered == [here] and other.now == here + 1
+    got = sv.spec_kv_attention(q, b, *idx, return_lse=True)
+    assert other.entered == [here, here] and other.now == here + 1
+    assert torch.equal(a.k_codes.view(torch.uint8), b.k_codes.view(torch.uint8))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    other.now = here
+    sv.spec_kv_attention(q, b, *idx)
+    assert len(other.entered) == 2
+
+
+@gpu
+def test_streams_of_other_devices_are_refused():
+    import speculative_sampling_verification_spec_gb300 as sv
+    s = Setup(311, 1, 1, 2, 2, 64, 16, [5], [1], "bf16")
+    cache, idx, q, k = s.cache(), s.idx(), s.dev(s.q), s.dev(s.k)
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", cache.device.index + 1), 0
+
+    with pytest.raises(ValueError):
+        sv.spec_kv_append(q, k, k, cache, *idx, stream=Stream())
+    with pytest.raises(ValueError):
+        sv.spec_kv_attention(q, cache, *idx, stream=Stream())
