@@ -16,8 +16,9 @@
  * append writes over them.
  *
  * Conventions: those of spec_verify.h.  The caller owns every buffer, which is on
- * the current device like the stream; calls are asynchronous on params->stream, host-side argument errors are returned before
- * anything is launched, and device-side errors never trap (see each entry).
+ * the current device like the stream; calls are asynchronous on params->stream,
+ * host-side argument errors are returned before anything is launched, and
+ * device-side errors never trap (see each entry).
  *
  * The cache.  A pool of pages of page_size token slots each, shared by all
  * sequences.  Token position p of sequence b lies in page

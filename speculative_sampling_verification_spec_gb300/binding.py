@@ -121,10 +121,18 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _check_cuda(*ts):
+    """CUDA tensors of the current device, which is where kernels are launched."""
     for t in ts:
-        if t is not None and not t.is_cuda:
+        if t is None:
+            continue
+        if not t.is_cuda:
             raise ValueError("spec_* calls take CUDA tensors (copy host data to the GPU first)")
+        if t.get_device() != _current_device():
+            raise ValueError("a tensor is on cuda:%d, the current device is cuda:%d" % (t.get_device(), _current_device()))
 
 
 _ws_cache = {}
