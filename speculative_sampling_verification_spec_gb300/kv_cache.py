@@ -270,6 +270,8 @@ def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=No
     key = (index, handle)
     if ws is None:
         ws = _ws_cache.get(key)
+    elif ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous uint8 on the cache's device")
     fixed = (B, T, hq, dtype, columns, window, 1.0 / math.sqrt(D) if scale is None else scale, 0, 0, 0,
              page_table.data_ptr(), seq_lens.data_ptr(), 0 if new_lens is None else new_lens.data_ptr(),
              row, qs[0], qs[1], qs[2], 0, 0, 0, 0, 0, 0, os[0], os[1], os[2], handle,

@@ -173,3 +173,17 @@ def test_streams_of_other_devices_are_refused():
         sv.spec_kv_append(q, k, k, cache, *idx, stream=Stream())
     with pytest.raises(ValueError):
         sv.spec_kv_attention(q, cache, *idx, stream=Stream())
+
+
+@gpu
+def test_workspaces_are_checked():
+    """A workspace on the host, of another type or with gaps is refused before its address is used."""
+    import speculative_sampling_verification_spec_gb300 as sv
+    s = Setup(312, 1, 1, 2, 2, 64, 16, [5], [1], "bf16")
+    cache, idx, q = s.cache(), s.idx(), s.dev(s.q)
+    n = sv.spec_kv_attention_workspace_size(cache, 1, 1, 2)
+    good = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    for ws in (good.cpu(), torch.zeros(n, device="cuda"), torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            sv.spec_kv_attention(q, cache, *idx, ws=ws)
+    sv.spec_kv_attention(q, cache, *idx, ws=good)
