@@ -112,6 +112,11 @@ spec_status spec_kv_append(const void* q, const void* k, const void* v, const fl
  * share one must not overlap in time on the GPU. */
 size_t spec_kv_attention_workspace_size(const spec_kv_cache* cache, const spec_kv_params* params);
 
+/* The capture (the graph being recorded) that calls on the stream go to; 0: none,
+ * they run.  For callers that keep workspaces: a graph may be replayed on any
+ * stream, so it needs one of its own, cleared in the graph. */
+uint64_t spec_kv_capture_id(void* stream);
+
 /* Attention of the new tokens' queries over the cache.  The new tokens' keys and
  * values are in the cache already (spec_kv_append), and lengths and page table
  * are the same as for that call.

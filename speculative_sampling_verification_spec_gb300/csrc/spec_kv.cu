@@ -352,6 +352,16 @@ size_t spec_kv_attention_workspace_size(const spec_kv_cache* cache, const spec_k
   return mma_shape(cache, params) ? std::max(general, plan_attention(cache, params, true).ws_bytes) : general;
 }
 
+uint64_t spec_kv_capture_id(void* stream) {
+  cudaStreamCaptureStatus state = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &state, &id) != cudaSuccess) {
+    cudaGetLastError();  // (the default stream, beside a capture: calls on it are not part of one)
+    return 0;
+  }
+  return state == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const spec_kv_params* params, void* out,
                               float* lse) {
   spec_status s = check_shapes(cache, params);

@@ -15,7 +15,7 @@ import torch
 
 from . import binding
 
-EXPORTED = ("spec_kv_append", "spec_kv_attention", "spec_kv_attention_workspace_size")
+EXPORTED = ("spec_kv_append", "spec_kv_attention", "spec_kv_attention_workspace_size", "spec_kv_capture_id")
 
 # spec_kv_cache and spec_kv_params of include/spec_kv.h, in native layout
 _CACHE = struct.Struct("@4i4P5q")
@@ -40,6 +40,8 @@ def _lib():
         L.spec_kv_attention.restype = ctypes.c_int
         L.spec_kv_append.argtypes = [P] * 7
         L.spec_kv_append.restype = ctypes.c_int
+        L.spec_kv_capture_id.argtypes = [P]
+        L.spec_kv_capture_id.restype = ctypes.c_uint64
         _loaded = L
     return _loaded
 
@@ -115,23 +117,27 @@ def _new(shape, dtype, device, stream):
     return t
 
 
-_ws_cache = {}
-_ws_outgrown = []      # kept: a captured graph may hold their addresses
+_ws_cache = {}     # (device, stream) -> workspace
+_ws_graphs = {}    # (device, stream) -> (capture, workspace) of the newest capture
+_COUNTERS = 1 << 16     # leading bytes that have to be zero before the first use; calls leave them at zero
 
 
-def _workspace(key, nbytes, device, stream):
-    """The workspace of (device, stream): calls on different streams may overlap, so each stream has its own.  One that
-    is made while the stream is captured belongs to the graph, which clears it at every replay, and is not kept; a call
-    before the capture spares the graph that."""
-    old = _ws_cache.get(key)
+def _workspace(key, nbytes, device, stream, capture):
+    """A workspace of at least nbytes for the calls of one (device, stream): calls on different streams may overlap, so
+    each stream has its own.  So has each capture, because graphs are replayed on any stream and may overlap what runs on
+    the one they were captured on: the calls of a capture share one from the graph's memory, cleared at every replay."""
+    if capture:
+        newest = _ws_graphs.get(key)
+        if newest is not None and newest[0] == capture and newest[1].numel() >= nbytes:
+            return newest[1]
+    elif key in _ws_cache:
+        nbytes = max(nbytes, 2 * _ws_cache[key].numel())
     with torch.cuda.stream(stream):
-        capturing = torch.cuda.is_current_stream_capturing()
-        if old is not None and not capturing:
-            nbytes = max(nbytes, 2 * old.numel())
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)  # counters that calls leave at zero
-    if not capturing:
-        if old is not None:
-            _ws_outgrown.append(old)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws[:_COUNTERS].zero_()
+    if capture:
+        _ws_graphs[key] = (capture, ws)
+    else:
         _ws_cache[key] = ws
     return ws
 
@@ -242,8 +248,8 @@ def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=No
     new tokens.  scale: factor of the scores (1 / sqrt(D)); window > 0: a query sees that many tokens, its own
     included.  Returns out [B, T, Hq, D] (zero in slots past new_lens), or (out, lse) with lse [B, T, Hq] float32, the
     natural logarithm of the sum of the weights, when return_lse or lse is given.  ws: a workspace of
-    spec_kv_attention_workspace_size bytes (uint8, CUDA, zeroed once); by default one is kept for each stream.  The
-    call runs on the cache's device, whichever is current."""
+    spec_kv_attention_workspace_size bytes (uint8, CUDA, zeroed once); by default one is kept for each stream
+    and one for each graph that is captured.  The call runs on the cache's device, whichever is current."""
     if _current_device() != cache._index:
         with torch.cuda.device(cache._index):
             return spec_kv_attention(q, cache, page_table, seq_lens, new_lens, scale=scale, window=window, out=out,
@@ -268,8 +274,15 @@ def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=No
         lse = _new(shape[:3], _F32, dev, stream)
     handle = _stream_of(stream, dev)
     key = (index, handle)
+    L = _lib()
+    capture = own = 0
     if ws is None:
-        ws = _ws_cache.get(key)
+        own = 1
+        # (asked of torch where it is about the current stream, which is cheaper)
+        if stream is not None or torch.cuda.is_current_stream_capturing():
+            capture = L.spec_kv_capture_id(handle)
+        if not capture:
+            ws = _ws_cache.get(key)
     elif ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
         raise ValueError("ws must be contiguous uint8 on the cache's device")
     fixed = (B, T, hq, dtype, columns, window, 1.0 / math.sqrt(D) if scale is None else scale, 0, 0, 0,
@@ -277,16 +290,15 @@ def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=No
              row, qs[0], qs[1], qs[2], 0, 0, 0, 0, 0, 0, os[0], os[1], os[2], handle,
              0 if status is None else status.data_ptr())
     args = (q.data_ptr(), cache._packed, out.data_ptr(), 0 if lse is None else lse.data_ptr())
-    L = _lib()
     if ws is None:
         nbytes = L.spec_kv_attention_workspace_size(cache._packed, _PARAMS.pack(*fixed, 0, 0))
-        ws = _workspace(key, max(nbytes, _WS_LEAST), dev, stream)
+        ws = _workspace(key, max(nbytes, _WS_LEAST), dev, stream, capture)
     code = L.spec_kv_attention(args[0], args[1], _PARAMS.pack(*fixed, ws.data_ptr(), ws.numel()), args[2], args[3])
-    if code == binding.SPEC_ERR_INVALID_ARG and ws is _ws_cache.get(key):
+    if code == binding.SPEC_ERR_INVALID_ARG and own and not capture:
         # the stream's workspace may be too small for this shape: a larger one is made, once
         nbytes = L.spec_kv_attention_workspace_size(cache._packed, _PARAMS.pack(*fixed, 0, 0))
         if nbytes > ws.numel():
-            ws = _workspace(key, nbytes, dev, stream)
+            ws = _workspace(key, nbytes, dev, stream, capture)
             code = L.spec_kv_attention(args[0], args[1], _PARAMS.pack(*fixed, ws.data_ptr(), ws.numel()), args[2],
                                        args[3])
     if code != binding.SPEC_OK:

@@ -187,3 +187,85 @@ def test_workspaces_are_checked():
         with pytest.raises(ValueError):
             sv.spec_kv_attention(q, cache, *idx, ws=ws)
     sv.spec_kv_attention(q, cache, *idx, ws=good)
+
+
+def _long_call(seed, n=3000, B=1):
+    import speculative_sampling_verification_spec_gb300 as sv
+    s = Setup(seed, B, 1, 4, 1, 64, 16, [n] * B, [1] * B, "bf16")
+    cache = s.cache()
+    s.append(cache)
+    s.ref_append()
+    q, idx = s.dev(s.q), s.idx()
+    return (lambda **kw: sv.spec_kv_attention(q, cache, *idx, return_lse=True, **kw)), s.ref_attention()
+
+
+@gpu
+def test_a_graph_has_a_workspace_of_its_own():
+    """Whatever happens to the workspace that direct calls on the capturing stream use, before the capture too, is not
+    the graph's concern: it may be replayed beside them."""
+    import speculative_sampling_verification_spec_gb300 as sv
+    call, want = _long_call(313, B=8)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    key = (torch.cuda.current_device(), side.cuda_stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        assert_attention(*call(), want)
+        with torch.cuda.graph(graph, stream=side):
+            got = call()
+        direct = sv.kv_cache._ws_cache[key]
+        direct[:1 << 16] = 0x3F         # counters that no call leaves
+        graph.replay()
+        side.synchronize()
+        assert_attention(*got, want)
+        direct[:1 << 16] = 0
+        assert_attention(*call(), want)
+    side.synchronize()
+
+
+@gpu
+def test_overlapping_replays():
+    """Two graphs of one stream, each of several calls of different sizes, replayed side by side on other streams with
+    direct calls beside them."""
+    import speculative_sampling_verification_spec_gb300 as sv
+    calls = [_long_call(320 + i, n, B) for i, (n, B) in enumerate([(3000, 8), (9000, 1), (2000, 5), (500, 20)])]
+    torch.cuda.synchronize()
+    side, streams = torch.cuda.Stream(), [torch.cuda.Stream() for _ in range(2)]
+    graphs, results = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            results.append([call() for call, _ in calls])
+        graphs.append(g)
+    key = (torch.cuda.current_device(), side.cuda_stream)
+    assert key not in sv.kv_cache._ws_cache
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                for _ in range(3):
+                    g.replay()
+        with torch.cuda.stream(side):
+            direct = [call() for call, _ in calls]
+        torch.cuda.synchronize()
+        for res in results + [direct]:
+            for r, (_, want) in zip(res, calls):
+                assert_attention(*r, want)
+
+
+@gpu
+def test_capture_ids():
+    import speculative_sampling_verification_spec_gb300 as sv
+    L = sv.kv_cache._lib()
+    side = torch.cuda.Stream()
+    x = torch.zeros(4, device="cuda")
+    ids = []
+    assert L.spec_kv_capture_id(side.cuda_stream) == 0
+    torch.cuda.synchronize()
+    for _ in range(2):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+            x.add_(1)
+            ids.append(L.spec_kv_capture_id(side.cuda_stream))
+    assert ids[0] and ids[1] and ids[0] != ids[1]
+    assert L.spec_kv_capture_id(side.cuda_stream) == 0
+    torch.cuda.synchronize()
