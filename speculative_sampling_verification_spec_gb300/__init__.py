@@ -12,7 +12,7 @@ from .binding import (  # noqa: F401
     spec_verify_workspace_size, spec_verify_noalloc, spec_verify_ragged, workspace,
 )
 from .kv_cache import (  # noqa: F401
-    PagedKVCache, spec_kv_append, spec_kv_attention, spec_kv_attention_workspace_size,
+    PagedKVCache, spec_kv_append, spec_kv_attention, spec_kv_attention_workspace_size, spec_kv_reset_workspaces,
 )
 from . import decode  # noqa: F401
 from ._build import build  # noqa: F401

@@ -142,6 +142,14 @@ def _workspace(key, nbytes, device, stream, capture):
     return ws
 
 
+def spec_kv_reset_workspaces():
+    """Forget the workspaces that spec_kv_attention keeps for its callers, so that the next calls start from cleared
+    ones: to be called after a SPEC_ERR_TIMEOUT in a status word, which leaves the counters of the call's workspace
+    undefined.  (A captured graph clears its own at every replay; a caller's ws is the caller's to clear.)"""
+    _ws_cache.clear()
+    _ws_graphs.clear()
+
+
 def _check_table(cache, B, page_table, seq_lens, new_lens, status):
     """The columns and row stride of the page table, after checking it and the lengths."""
     dev = cache._index

@@ -269,3 +269,17 @@ def test_capture_ids():
     assert ids[0] and ids[1] and ids[0] != ids[1]
     assert L.spec_kv_capture_id(side.cuda_stream) == 0
     torch.cuda.synchronize()
+
+
+@gpu
+def test_workspaces_after_a_timeout():
+    """A call that gave up leaves counters behind; with the kept workspaces forgotten, calls are as on a fresh stream.
+    (The counters are put there by the test: no wait runs out.)"""
+    import speculative_sampling_verification_spec_gb300 as sv
+    call, want = _long_call(314, B=8)
+    assert_attention(*call(), want)
+    key = (torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream)
+    sv.kv_cache._ws_cache[key][:1 << 16] = 0x3F
+    sv.spec_kv_reset_workspaces()
+    for _ in range(2):
+        assert_attention(*call(), want)
