@@ -67,9 +67,9 @@ typedef enum {
   SPEC_ERR_CUDA = 2,         /* host: a CUDA runtime call failed (launch, attribute) */
   SPEC_ERR_NONFINITE = 3,    /* device: NaN or +inf logit, or no finite logit, in a row read */
   SPEC_ERR_TOKEN_RANGE = 4,  /* device: a draft token outside [0, V) */
-  SPEC_ERR_TIMEOUT = 5,      /* device: a bounded wait ran out in spec_kv_attention (spec_kv.h); never
-                                reported by verification, where a bulk copy that misses its wait is
-                                replaced by plain loads */
+  SPEC_ERR_TIMEOUT = 5,      /* device: a bounded wait ran out.  In verification a bulk copy missed it and its
+                                rows were read by plain loads (the results stand); in spec_kv_attention the
+                                affected rows are NaN (spec_kv.h) */
   SPEC_ERR_UNSUPPORTED = 6,  /* host: more shared memory than the device offers, or more than
                                 2^31 - 1 row segments in one call */
   SPEC_ERR_SCRATCH_LIMIT = 7, /* host: spec_verify_noalloc asked for more than its fixed scratch */
