@@ -23,8 +23,8 @@
 //   p = p0 + p1 / 8 + p2 / 64 in e5m2, the pieces side by side as columns of one
 //     product and added at the end (sums are of the float p).
 // Long contexts are full of small weights that only count together, so each weight
-// keeps its own precision: an error of 2^-9 of it at most down to 2^-24 of the
-// largest weight of its row in the range, and of 2^-33 of the largest below.  (Two
+// keeps its own precision: an error of 2^-9 of it at most down to 2^-23 of the
+// largest weight of its row in the range, and of 2^-32 of the largest below.  (Two
 // e4m3 pieces lost what lay under 2^-17 of it: 40 % of the output where a quarter of
 // the weight is spread evenly over 32768 tokens.)
 //
@@ -74,7 +74,10 @@ constexpr int kPieceRing = 8;
 constexpr uint32_t kUnset = 0x80000000u;  // bits of -0: scores are taken as they are
 constexpr int kNear = 4;            // log2 of how far apart rows with one exponent may be
 constexpr int kTop = 15;            // log2 of the largest weight (e5m2 and half hold more than 2^15)
-constexpr int kSlack = 5;           // log2 of how far weights may pass the reference (3: 7 % slower at 36 rows)
+// log2 of how far weights may pass the reference: a bit more costs the smallest weights one, a bit less makes
+// references move more often (36 rows on 32768 tokens 236 us with 3, 222 with 5, 219 with 6, 219 with 7; 512 queries
+// on 8192 351, 308, 299, 293)
+constexpr int kSlack = 6;
 constexpr float kShift = kTop - kSlack;  // a raised reference is kShift below the largest score
 // The sums are of weights times this: with value scales down to 2^-100 those of 2^24 tokens stay finite.
 constexpr int kSumExp = 12;
@@ -739,16 +742,20 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
               if (!fail) fail = !bar_wait(&sm.pv_done[(n - 1) % C::PB], ((n - 1) / C::PB) & 1, gave_up);
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < fours; c += 8) {  // (past the last row, what is there is not used)
-#pragma unroll 1
-                for (uint32_t at = tO + c; at < tO + c + kPieces * NR; at += NR) {
-                  float o[8];
-                  tmem_ld<8>(at, o);
-                  tmem_wait_ld();
-                  tmem_tie<8>(o);
+              for (int c = 0; c < fours; c += 4) {
+                float o[kPieces][4];
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) o[i] *= sm.fac()[r_base + c + i];
-                  tmem_st<8>(at, o);
+                for (int k = 0; k < kPieces; ++k) tmem_ld<4>(tO + c + k * NR, o[k]);
+                tmem_wait_ld();
+                const float4 f = *reinterpret_cast<const float4*>(&sm.fac()[r_base + c]);
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k) {
+                  tmem_tie<4>(o[k]);
+                  o[k][0] *= f.x;
+                  o[k][1] *= f.y;
+                  o[k][2] *= f.z;
+                  o[k][3] *= f.w;
+                  tmem_st<4>(tO + c + k * NR, o[k]);
                 }
               }
               tmem_wait_st();

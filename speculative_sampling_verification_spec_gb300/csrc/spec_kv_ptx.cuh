@@ -106,6 +106,21 @@ __device__ __forceinline__ void tmem_st<8>(uint32_t addr, const float* x) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
                : "memory");
 }
+template <>
+__device__ __forceinline__ void tmem_ld<4>(uint32_t addr, float* x) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+               : "r"(addr));
+}
+template <>
+__device__ __forceinline__ void tmem_st<4>(uint32_t addr, const float* x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3])
+               : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_tie<4>(float* x) {
+  asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]));
+}
 // nothing that uses these values moves ahead of the wait before it
 template <>
 __device__ __forceinline__ void tmem_tie<8>(float* x) {
