@@ -132,16 +132,17 @@ uint64_t spec_kv_capture_id(void* stream);
  * queries and weights in float too.  The other bfloat16 calls run on 8-bit matrix
  * products and hold them in 8-bit pieces: a query channel to 2^-17 of the largest of
  * its row (2^-13, where rows of one sequence and head are within 16 times of each
- * other); a weight (times its page's value scale) to 2^-9 of itself, or to
- * 2^-32 of the largest of its row where that is more.  Their running sums lose up to 2^-24 of themselves for each 32
- * tokens.  Tokens a query does not see have no
- * influence on its output, whatever their slots hold; a NaN key or value that it
- * sees makes its output NaN (a value: in the affected channels at least).
- * Device errors: a sequence whose lengths are out of range gets NaN, and so does
- * a row that sees a token of a page outside [0, num_pages); both store
+ * other); a weight (times its page's value scale) to 2^-9 of itself, or to 2^-32 of
+ * the largest of its row where that is more.  Their running sums lose up to 2^-24 of
+ * themselves for each 32 tokens.
+ * Tokens a query does not see have no influence on its output, whatever their slots
+ * hold; a NaN key or value that it sees makes its output NaN (a value: in the
+ * affected channels at least).
+ * Device errors: a sequence whose lengths are out of range gets NaN, and so does a
+ * row that sees a token of a page outside [0, num_pages); both store
  * SPEC_ERR_CACHE_RANGE in *status.  Entries of the table for pages that lie wholly
- * before what any query of the sequence sees through its window may hold anything.  A bounded wait that runs out (about two
- * seconds) gives NaN and SPEC_ERR_TIMEOUT. */
+ * before what any query of the sequence sees through its window may hold anything.
+ * A bounded wait that runs out (about two seconds) gives NaN and SPEC_ERR_TIMEOUT. */
 spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const spec_kv_params* params, void* out,
                               float* lse);
 

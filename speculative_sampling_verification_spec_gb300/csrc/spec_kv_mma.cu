@@ -10,7 +10,7 @@ const void* entry(int* smem_bytes) {
   return reinterpret_cast<const void*>(&spec_kv_detail::spec_kv_attention_mma_kernel<D, NR, RU>);
 }
 // 33 to 40 rows have a kernel of their own: 20 rows of each half fit the registers
-// where 24 do not quite (36 rows of 32768 tokens: 243 us against 256)
+// where 24 do not quite (36 rows of 32768 tokens: 223 us against 228)
 template <int D>
 const void* of_rows(int rows, int* smem_bytes) {
   if (rows <= 16) return entry<D, 16, 8>(smem_bytes);

@@ -25,7 +25,7 @@
 // Long contexts are full of small weights that only count together, so each weight
 // keeps its own precision: an error of 2^-9 of it at most down to 2^-23 of the
 // largest weight of its row in the range, and of 2^-32 of the largest below.  (Two
-// e4m3 pieces lost what lay under 2^-17 of it: 40 % of the output where a quarter of
+// e4m3 pieces lost what lay under 2^-17 of it: 58 % of the output where a quarter of
 // the weight is spread evenly over 32768 tokens.)
 //
 // A thread of the softmax warps holds one token: the token's two scales are
@@ -34,7 +34,7 @@
 // maximum of a row is over the threads; it is not needed exactly, only as a
 // reference that keeps p within the pieces' range, so it is raised (and the
 // accumulators rescaled) only when a weight would pass 2^kSlack times the one at
-// which it was set: about one tile in fifteen, and the first of an item.
+// which it was set, and in the first tile of an item.
 //
 // The matrix unit adds to its float accumulators with truncation: about 2^-24 of
 // the sum for each 32 tokens, always downwards in magnitude.  At a million tokens
@@ -48,10 +48,10 @@
 // What bounds it.  Long caches: memory while few rows read them (64 sequences of
 // up to 8192 tokens, 8 rows a key/value head: 653 MB in 106 us, 6.2 TB/s), the
 // softmax warps' instructions beside it as rows grow (32 sequences of up to 32768
-// tokens, 36 rows: 1.24 GB in 211 us, 5.9 TB/s; a tile costs a softmax warp about
-// 3000 cycles beside three others on its scheduler, the tensor unit is busy a sixth
+// tokens, 36 rows: 1.24 GB in 219 us, 5.7 TB/s; a tile costs a softmax warp about
+// 3000 cycles beside three others on its scheduler, the tensor unit is busy a fifth
 // of the time).  Part of a prompt (512 queries on 8192 tokens): the same instructions,
-// 142 GFLOP in 291 us.  Short calls: the chain of dependent steps (lengths, page
+// 142 GFLOP in 299 us.  Short calls: the chain of dependent steps (lengths, page
 // numbers, keys, scores, weights, output, join: 1000 tokens take 10.5 us).
 #include <cuda_fp16.h>
 
@@ -62,8 +62,9 @@
 namespace spec_kv_detail {
 
 // Rows of a row tile at most.  More would share one reading of the cache between
-// more rows, but 64 do not fit the registers of the softmax threads (512 queries on
-// 8192 tokens took 472 us in row tiles of 64, 367 in tiles of 48, 414 in tiles of 32).
+// more rows, but 64 do not fit the registers of the softmax threads (with two-piece
+// weights, 512 queries on 8192 tokens took 472 us in row tiles of 64, 367 in tiles of
+// 48, 414 in tiles of 32).
 constexpr int kMmaRows = 48;
 constexpr int kMmaThreads = 320;
 constexpr int kSoftThreads = 256;  // two groups of 128, a token a thread
@@ -89,7 +90,9 @@ constexpr float kLeastOfTop = 1.0f / (1ull << 40) / (1ull << 40);
 
 // Stages of keys and of values, buffers of weights: what two CTAs an SM leave room
 // for.  Keys are used up two tiles ahead of the weights (the scores are
-// double-buffered), so values get the larger share.
+// double-buffered), so values get the larger share (36 rows on 32768 tokens: 223 us,
+// 236 with two stages of values; 20 rows on 131072: 52.8 us, 54.7 with a second buffer
+// of weights in place of the third stage).
 template <int D, int NR>
 struct MmaCfg {
   static constexpr int kTileBytes = kTile * D;
