@@ -10,7 +10,8 @@
  *   spec_kv_append     rotates the new tokens' queries and keys by position and
  *                      stores their keys and values in the sequences' pages;
  *   spec_kv_attention  attends from the new tokens' queries to every token
- *                      stored for their sequence up to their own position.
+ *                      stored for their sequence up to their own position;
+ *   spec_kv_attention_sinks  to the last ones and the first ones of them.
  *
  * Dropping rejected tokens is a smaller length at the next call: the next
  * append writes over them.
@@ -145,6 +146,15 @@ uint64_t spec_kv_capture_id(void* stream);
  * A bounded wait that runs out (about two seconds) gives NaN and SPEC_ERR_TIMEOUT. */
 spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const spec_kv_params* params, void* out,
                               float* lse);
+
+/* The same with first tokens that stay visible: beside its window, a query sees the
+ * positions j < sinks (those up to its own).  sinks >= 0; without a window (0) every
+ * position is seen anyway.  A token of both counts once.  Entries of the table for pages
+ * that lie wholly behind the sinks and before what any query of the sequence sees through
+ * its window may hold anything.  Everything else, the workspace's size among it, is as for
+ * spec_kv_attention, which is this with no sinks. */
+spec_status spec_kv_attention_sinks(const void* q, const spec_kv_cache* cache, const spec_kv_params* params,
+                                    int32_t sinks, void* out, float* lse);
 
 #ifdef __cplusplus
 }

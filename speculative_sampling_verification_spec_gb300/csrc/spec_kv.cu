@@ -262,9 +262,9 @@ spec_status launch_mma(const KvArgs& args, const spec_kv_cache* c, const MapOrde
   maps.at_head = order.at_head;
   maps.at_page = order.at_page;
   int smem = 0;
-  const void* fn = specv_units::kv_mma(a.D, a.rows, &smem);
+  const void* fn = specv_units::kv_mma(a.D, a.rows, a.sinks > 0, &smem);
   const int kind = a.rows <= 16 ? 0 : a.rows <= 32 ? 1 : a.rows <= 40 ? 2 : 3;
-  if (!fn || !allow_smem(fn, (a.D == 128 ? 4 : 0) + kind, smem)) return SPEC_ERR_CUDA;
+  if (!fn || !allow_smem(fn, (a.sinks > 0 ? 8 : 0) + (a.D == 128 ? 4 : 0) + kind, smem)) return SPEC_ERR_CUDA;
   void* params[] = {&a, &maps};
   return launch(fn, grid, kMmaThreads, smem, st, params);
 }
@@ -364,10 +364,15 @@ uint64_t spec_kv_capture_id(void* stream) {
 
 spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const spec_kv_params* params, void* out,
                               float* lse) {
+  return spec_kv_attention_sinks(q, cache, params, 0, out, lse);
+}
+
+spec_status spec_kv_attention_sinks(const void* q, const spec_kv_cache* cache, const spec_kv_params* params,
+                                    int32_t sinks, void* out, float* lse) {
   spec_status s = check_shapes(cache, params);
   if (s != SPEC_OK) return s;
   const spec_kv_params* p = params;
-  if (p->window < 0 || !std::isfinite(p->scale)) return SPEC_ERR_INVALID_ARG;
+  if (p->window < 0 || sinks < 0 || !std::isfinite(p->scale)) return SPEC_ERR_INVALID_ARG;
   if (p->B == 0) return SPEC_OK;
   s = check_cache(cache, p);
   if (s != SPEC_OK) return s;
@@ -385,6 +390,7 @@ spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const s
   a.out = out;
   a.lse = lse;
   a.window = p->window;
+  a.sinks = p->window > 0 ? sinks : 0;
   a.scale2 = static_cast<float>(static_cast<double>(p->scale) * 1.4426950408889634);
   a.rows = pl.rows;
   a.nrt = pl.nrt;

@@ -242,7 +242,10 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
   Walk walk = walk_begin(plan, range, rt);
   Piece p;
   while (walk_next(a, walk, p)) {
-    const int j0 = p.tile0 << a.log_tile, j1 = min(p.tile1 << a.log_tile, p.L + p.n);
+    // the piece's tokens are counted from 0, without what is left out; position_of: where they are
+    const int j0 = p.tile0 << a.log_tile, near = p.near << a.log_tile, skip = p.skip << a.log_tile;
+    const int count = min(p.tile1 << a.log_tile, p.L + p.n) - j0 - skip;
+    const auto position_of = [&](int i) { return j0 + i + (i >= near ? skip : 0); };
     float q[ROWS][CH], acc[ROWS][CH];  // queries in log2 units; zero past the last row and channel
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
@@ -263,12 +266,13 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
 
     uint32_t kc[kGenStep][kWords], vc[kGenStep][kWords];
     float ks, vs;
-    const auto number = [&](int base) { return base < j1 ? page_of(a, p.b, base >> a.log_page) : 0; };
-    const auto fetch = [&](int base, int page) {
-      ks = vs = __uint_as_float(0x7fc00000u);  // a page that is not the pool's
-      const bool ok = base < j1 && page >= 0;
-      if (base < j1 && page < 0 && lane == 0 && (((base >> a.log_page) + 1) << a.log_page) > p.first)
-        report(a.status, SPEC_ERR_CACHE_RANGE);
+    const auto number = [&](int i) { return i < count ? page_of(a, p.b, position_of(i) >> a.log_page) : 0; };
+    const auto fetch = [&](int i, int page) {
+      ks = vs = __uint_as_float(0x7fc00000u);  // a page that is not the pool's, or tokens that no row sees
+      const int base = position_of(i);
+      const bool sees = i < count && piece_sees(a, p, base, base + kGenStep);
+      const bool ok = sees && page >= 0;
+      if (sees && page < 0 && lane == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
       if (ok) {
         const int64_t at = page * a.scale_page_stride + p.h * a.scale_head_stride;
         ks = a.k_scale[at];
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
                           (base & ((1 << a.log_page) - 1)) * a.token_stride + d0;
 #pragma unroll
       for (int t = 0; t < kGenStep; ++t) {
-        const bool get = ok && mine && base + t < j1;
+        const bool get = ok && mine && i + t < count;
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
           kc[t][w] = get ? *reinterpret_cast<const uint32_t*>(a.k_codes + row + t * a.token_stride + 4 * w) : 0u;
@@ -287,10 +291,11 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
       }
     };
     constexpr int kStride = kGenStep * kGenWarps;
-    int base = j0 + warp * kGenStep;
-    int page = number(base), next_page = number(base + kStride);
-    if (base < j1) fetch(base, page);
-    for (; base < j1; base += kStride) {
+    int i = warp * kGenStep;
+    int page = number(i), next_page = number(i + kStride);
+    if (i < count) fetch(i, page);
+    for (; i < count; i += kStride) {
+      const int base = position_of(i);
       float kf[kGenStep][CH];
       uint32_t vnow[kGenStep][kWords];
       const float ks_now = ks, vs_now = vs;
@@ -308,9 +313,9 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
         }
       }
       page = next_page;
-      next_page = number(base + 2 * kStride);
-      if (base + kStride < j1) fetch(base + kStride, page);
-      const bool all = base >= all_from && base + kGenStep - 1 <= all_to;
+      next_page = number(i + 2 * kStride);
+      if (i + kStride < count) fetch(i + kStride, page);
+      const bool all = (base >= all_from || base + kGenStep <= a.sinks) && base + kGenStep - 1 <= all_to;
 #pragma unroll
       for (int t0 = 0; t0 < kGenStep; t0 += 4) {
         float s[ROWS * 4];
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
         }
         const float score = lane_sums<ROWS * 4>(s) * ks_now;
         const int j = base + t0 + my_tok;
-        const bool see = j <= pos && j > low;  // (positions from j1 on are past every row's own)
+        const bool see = j <= pos && (j > low || j < a.sinks);  // (positions past the last are past every row's own)
         const float x = see ? score : -INFINITY;
         float top = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));

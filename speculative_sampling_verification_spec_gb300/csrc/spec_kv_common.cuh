@@ -4,7 +4,9 @@
 //
 // The attention's work is a list of tiles of 2^log_tile tokens: sequence after
 // sequence, within a sequence head after head, within a head in order of
-// position.  Before each head's tiles come `overhead` places without one, for what
+// position: from the first tile that the window reaches, or from 0; where first
+// tokens stay visible beside a window, their tiles come first and the tiles between
+// are left out.  Before each head's tiles come `overhead` places without one, for what
 // it costs to take up a head.  The list is cut into `nranges` equal ranges (from
 // the lengths on the device, so a batch of unequal sequences is spread evenly and
 // no length crosses to the host); a range is walked by one CTA for one row tile.
@@ -42,6 +44,7 @@ struct KvArgs {
   int32_t* status;
   int32_t B, T, Hq, Hkv, G, D;
   int32_t log_page, num_pages, max_pages, window;
+  int32_t sinks;      // first tokens that every row sees beside its window (0 without a window)
   // attention
   const void* q;
   void* out;
@@ -85,10 +88,14 @@ __device__ __forceinline__ float2 codes2_to_float2(uint16_t c) {
   return __half22float2(__half2(h));
 }
 
-// The tokens of sequence b and the tiles its rows read: positions from tile
-// t0 to L + n.  No tiles when it has no new token or its lengths are out of range.
+// tiles that hold the sinks
+__device__ __forceinline__ int sink_tiles(const KvArgs& a) { return a.sinks > 0 ? ((a.sinks - 1) >> a.log_tile) + 1 : 0; }
+
+// The tokens of sequence b and the tiles its rows read: the first ns (before t0), and
+// from tile t0 to position L + n.  No tiles when it has no new token or its lengths are
+// out of range.
 struct SeqSpan {
-  int L, n, t0, nt;
+  int L, n, t0, ns, nt;
   int places;  // a head's in the list
   bool bad;
 };
@@ -99,12 +106,14 @@ __device__ __forceinline__ SeqSpan seq_span(const KvArgs& a, int b) {
   const int64_t cap = static_cast<int64_t>(a.max_pages) << a.log_page;
   s.bad = s.L < 0 || s.n < 0 || s.n > a.T || static_cast<int64_t>(s.L) + s.n > cap;
   s.t0 = 0;
+  s.ns = 0;
   s.nt = 0;
   s.places = 0;
   if (!s.bad && s.n > 0) {
     const int first = (a.window > 0 && s.L + 1 > a.window) ? s.L + 1 - a.window : 0;
     s.t0 = first >> a.log_tile;
-    s.nt = ((s.L + s.n - 1) >> a.log_tile) + 1 - s.t0;
+    s.ns = min(s.t0, sink_tiles(a));
+    s.nt = s.ns + ((s.L + s.n - 1) >> a.log_tile) + 1 - s.t0;
     s.places = s.nt + a.overhead;
   }
   return s;
@@ -178,7 +187,8 @@ struct Piece {
   int L, n;          // tokens before the new ones; new tokens
   int row0, nrows;   // rows of this row tile
   int tile0, tile1;  // absolute tiles [tile0, tile1); may be empty
-  int first;         // first position that a row sees
+  int near, skip;    // the `skip` tiles from tile0 + near on are left out (0: none)
+  int first;         // first position that a row sees through its window
   int c0, c1;        // first and last range that hold tiles of the item
   int slot;          // where a partial result goes, when these differ
   __device__ bool whole() const { return c0 == c1; }
@@ -237,12 +247,25 @@ __device__ __forceinline__ bool walk_next(const KvArgs& a, Walk& k, Piece& p) {
     const int hi = ((s.L + t_last) >> a.log_tile) + 1;
     const int lo = (a.window > 0 && s.L + t_first + 1 > a.window) ? s.L + t_first + 1 - a.window : 0;
     p.first = lo;
-    p.tile0 = max(s.t0 + t0, lo >> a.log_tile);
-    p.tile1 = min(s.t0 + t1, hi);
-    if (p.tile1 < p.tile0) p.tile1 = p.tile0;
+    // Of the tiles of sinks, those in the piece (they may go on past t0, where nothing is left out
+    // and places are tiles); of the others, those in it from tile `far` on, where this row tile's
+    // window begins.
+    const int st = sink_tiles(a), near0 = min(t0, st), near1 = max(near0, min(min(t1, st), hi));
+    const int far = max(max(s.t0 + max(t0 - s.ns, 0), lo >> a.log_tile), st);
+    const int more = max(min(s.t0 + t1 - s.ns, hi) - far, 0);
+    p.near = near1 - near0;
+    p.tile0 = p.near > 0 ? near0 : far;
+    p.tile1 = more > 0 ? far + more : p.tile0 + p.near;
+    p.skip = p.near > 0 && more > 0 ? far - near1 : 0;
     return true;
   }
   return false;
+}
+
+// Whether some row of the piece sees a token of [from, to) (which begins at or before
+// the last position that a row sees).
+__device__ __forceinline__ bool piece_sees(const KvArgs& a, const Piece& p, int from, int to) {
+  return to > p.first || from < a.sinks;
 }
 
 // page number of a token's page, -1 where it is not one of the pool's (an error

@@ -282,7 +282,9 @@ static __device__ __noinline__ void abandon(const KvArgs& a, const RangePlan& pl
 }
 
 // RU: rows that a softmax group keeps in registers, at most NR / 2
-template <int D, int NR, int RU>
+// SINKS: first tokens may be seen beside the window (a few instructions a tile, which cost the calls without
+// them 3 to 5 % where rows are many: 36 rows on 32768 tokens 219 -> 226 us, 512 queries on 8192 297 -> 314)
+template <int D, int NR, int RU, bool SINKS>
 __global__ void __launch_bounds__(kMmaThreads, 2)
     spec_kv_attention_mma_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ MmaMaps maps) {
   using C = MmaCfg<D, NR>;
@@ -352,14 +354,22 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         }
         ++pieces;
         if (p.b < 0) break;
-        const int end = p.L + p.n;
-        const int first = p.tile0 * np, last = min(p.tile1 * np, (end + (1 << a.log_page) - 1) >> a.log_page);
+        // The pages of the piece, without what is left out: page i is page i + skip of the sequence from
+        // `near` on.  One that no row sees (beside a tile's sinks, before the window) or that is not the
+        // pool's has NaN scales and is not fetched: its tokens are treated by these, whatever shared
+        // memory holds.
+        const int near = (p.tile0 + p.near) * np, skip = SINKS ? p.skip * np : 0;
+        const int first = p.tile0 * np;
+        const int last = min(p.tile1 * np, (p.L + p.n + (1 << a.log_page) - 1) >> a.log_page) - skip;
         // 32 pages at a time, one a lane: numbers, then scales; the next 32 are under way
         const auto number = [&](int base) {
-          int pid = 0;
+          int pid = -1;
           if (base + lane < last) {
-            pid = page_of(a, p.b, base + lane);
-            if (pid < 0 && ((base + lane + 1) << a.log_page) > p.first) report(a.status, SPEC_ERR_CACHE_RANGE);
+            const int at = base + lane + (SINKS && base + lane >= near ? skip : 0);
+            if (piece_sees(a, p, at << a.log_page, (at + 1) << a.log_page)) {
+              pid = page_of(a, p.b, at);
+              if (pid < 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+            }
           }
           return pid;
         };
@@ -380,7 +390,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         int base = first;
         int pid = number(base), pid_next = 0;
         float2 sc = scales(base, pid), sc_next = make_float2(0.0f, 0.0f);
-        for (int t = p.tile0; t < p.tile1; ++t, ++n) {
+        for (int t = p.tile0; t < p.tile1 - (SINKS ? p.skip : 0); ++t, ++n) {
           int in = t * np - base;  // the tile's first page among the 32
           if (in == 32) {
             base += 32;
@@ -389,13 +399,12 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             sc = sc_next;
           }
           const int mine = lane - in;  // this lane's page of the tile
-          const bool has = mine >= 0 && mine < np && base + lane < last;
-          const int cnt = min(np, last - (base + in));
+          const bool has = mine >= 0 && mine < np && pid >= 0;
+          const int cnt = __popc(__ballot_sync(kFull, has));
           // coordinates after the channel: token 0, the head and the page, in the maps' order
-          const int page = max(pid, 0);
-          const int y = maps.at_head == 0 ? p.h : maps.at_page == 0 ? page : 0;
-          const int z = maps.at_head == 1 ? p.h : maps.at_page == 1 ? page : 0;
-          const int w = maps.at_head == 2 ? p.h : maps.at_page == 2 ? page : 0;
+          const int y = maps.at_head == 0 ? p.h : maps.at_page == 0 ? pid : 0;
+          const int z = maps.at_head == 1 ? p.h : maps.at_page == 1 ? pid : 0;
+          const int w = maps.at_head == 2 ? p.h : maps.at_page == 2 ? pid : 0;
           const int ks = n % C::KS, vs = n % C::VS;
           if (n >= C::KS) ok = bar_wait(&sm.k_empty[ks], (n / C::KS - 1) & 1, gave_up);
           ok = __all_sync(kFull, ok);
@@ -466,7 +475,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           if (!ok) break;
           const Piece& p = sm.pieces[pieces % kPieceRing];
           if (p.b < 0) break;
-          const int m = p.tile1 - p.tile0;
+          const int m = p.tile1 - p.tile0 - (SINKS ? p.skip : 0);
           if (m == 0) continue;
           ok = bar_wait(&sm.q_full, queries & 1, gave_up);
           if (!ok) break;
@@ -519,7 +528,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         }
         fail = soft_any(fail);  // the piece before has been written out
         if (fail || p.b < 0) break;
-        const int m = p.tile1 - p.tile0;
+        const int m = p.tile1 - p.tile0 - (SINKS ? p.skip : 0);
         const int fours = max(0, (rows_mine() + 3) / 4 * 4);  // this group's rows, in fours
         float l[RT];
 #pragma unroll
@@ -615,26 +624,36 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           if (tid == 0) bar_arrive(&sm.q_full);
         }
         const int tile0 = p.tile0, tile1 = p.tile1;
+        const int t_near = SINKS && p.skip > 0 ? tile0 + p.near : -1;  // the first of the tiles that are left out
+        const int sinks = SINKS ? a.sinks : 0;
         const int pos_hi = p.L + (p.row0 + p.nrows - 1) / a.G;
-        // tiles that some row sees only in part: from t_edge on, and up to t_win; and the tile from
-        // which on every row has seen a token
+        // tiles that some row sees only in part: from t_edge on, and up to t_win but for those of sinks
+        // alone; and the tile up to which a row may not have seen a token (a row that sees nothing of
+        // a first tile with sinks sees nothing of the piece)
         const int t_edge = (p.L + p.row0 / a.G + 1) / kTile;
         const int t_win = a.window > 0 && pos_hi >= a.window ? (pos_hi - a.window) / kTile : -1;
-        const int t_unset = max(tile0, a.window > 0 ? (pos_hi + 1 - a.window) / kTile : 0);
+        const int t_unset = max(tile0, a.window > 0 && (!SINKS || tile0 * kTile >= sinks) ? (pos_hi + 1 - a.window) / kTile : 0);
         for (int t = tile0; t < tile1; ++t, ++n) {
+          if (SINKS && t == t_near) t += p.skip;
           const int j = t * kTile + token;
           // scores of this tile; they come with its scales, and with the end of the products two
           // tiles back (issued before them): with two buffers of weights this one's is free
           if (!fail) fail = !bar_wait(&sm.s_full[n & 1], (n >> 1) & 1, gave_up);
           tc_fence_after();
           float4 sc = sm.scales[n % C::kScaleRing][token >> a.log_page];
-          const bool edge = t >= t_edge || t <= t_win;
+          const bool edge = t >= t_edge || (t <= t_win && (!SINKS || t >= sinks / kTile));
+          // whether a row at position q sees the token
+          const int reach = a.window > 0 && j >= sinks ? a.window : INT_MAX;
+          const auto seen_from = [&](int q) {
+            if constexpr (SINKS) return j <= q && j > q - reach;
+            return j <= q && (a.window <= 0 || j > q - a.window);
+          };
           bool poison = false;
           if (edge) {
             // no row may be touched by what it does not see: values that are not to be read are
             // zero, NaN codes and scales of a token that some rows see go to those rows' sums
             const int first = p.L + p.row0 / a.G, last = p.L + (p.row0 + p.nrows - 1) / a.G;
-            const bool all_see = j <= first && (a.window <= 0 || j > last - a.window);
+            const bool all_see = j <= first && (SINKS ? j > last - reach : a.window <= 0 || j > last - a.window);
             const bool gone = j >= p.L + p.n;
             const bool bad_scale = !(sc.x == sc.x && sc.z == sc.z);
             uint8_t* row = sv + (n % C::VS) * C::kTileBytes + token * D;  // whole rows: the swizzle stays inside
@@ -661,10 +680,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           const float ks = sc.x * factor;
           const u64 ks2 = pack2(ks, ks), lv2 = pack2(sc.y, sc.y), ivs2 = pack2(sc.z, sc.z);
           const uint32_t tS = tm + lanes + (n & 1) * NR + r_base;
-          const auto sees = [&](int r) {
-            const int q = sm.pos[r_base + r];
-            return j <= q && (a.window <= 0 || j > q - a.window);
-          };
+          const auto sees = [&](int r) { return seen_from(sm.pos[r_base + r]); };
           float x[RT];
 #pragma unroll
           for (int c = 0; c < RT; c += 8) tmem_ld<8>(tS + c, &x[c]);

@@ -15,7 +15,8 @@ import torch
 
 from . import binding
 
-EXPORTED = ("spec_kv_append", "spec_kv_attention", "spec_kv_attention_workspace_size", "spec_kv_capture_id")
+EXPORTED = ("spec_kv_append", "spec_kv_attention", "spec_kv_attention_sinks", "spec_kv_attention_workspace_size",
+            "spec_kv_capture_id")
 
 # spec_kv_cache and spec_kv_params of include/spec_kv.h, in native layout
 _CACHE = struct.Struct("@4i4P5q")
@@ -38,6 +39,8 @@ def _lib():
         L.spec_kv_attention_workspace_size.restype = ctypes.c_size_t
         L.spec_kv_attention.argtypes = [P] * 5
         L.spec_kv_attention.restype = ctypes.c_int
+        L.spec_kv_attention_sinks.argtypes = [P] * 3 + [ctypes.c_int32] + [P] * 2
+        L.spec_kv_attention_sinks.restype = ctypes.c_int
         L.spec_kv_append.argtypes = [P] * 7
         L.spec_kv_append.restype = ctypes.c_int
         L.spec_kv_capture_id.argtypes = [P]
@@ -248,20 +251,20 @@ def spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens=None, *, cos_s
     return q_out
 
 
-def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=None, window=0, out=None, lse=None,
+def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=None, window=0, sinks=0, out=None, lse=None,
                       return_lse=False, status=None, ws=None, stream=None):
     """Attention of the new tokens' (rotated) queries over everything stored for their sequence up to themselves.
 
     q [B, T, Hq, D] float32 or bfloat16; page_table, seq_lens and new_lens as for the spec_kv_append that stored the
     new tokens.  scale: factor of the scores (1 / sqrt(D)); window > 0: a query sees that many tokens, its own
-    included.  Returns out [B, T, Hq, D] (zero in slots past new_lens), or (out, lse) with lse [B, T, Hq] float32, the
-    natural logarithm of the sum of the weights, when return_lse or lse is given.  ws: a workspace of
-    spec_kv_attention_workspace_size bytes (uint8, CUDA, zeroed once); by default one is kept for each stream
-    and one for each graph that is captured.  The call runs on the cache's device, whichever is current."""
+    included; sinks: beside its window, it sees the first that many tokens of its sequence.  Returns out [B, T, Hq, D]
+    (zero in slots past new_lens), or (out, lse) with lse [B, T, Hq] float32, the natural logarithm of the sum of the
+    weights, when return_lse or lse is given.  ws: a workspace of spec_kv_attention_workspace_size bytes (uint8, CUDA,
+    zeroed once); by default one is kept for each stream and one for each graph that is captured.  The call runs on the cache's device, whichever is current."""
     if _current_device() != cache._index:
         with torch.cuda.device(cache._index):
-            return spec_kv_attention(q, cache, page_table, seq_lens, new_lens, scale=scale, window=window, out=out,
-                                     lse=lse, return_lse=return_lse, status=status, ws=ws, stream=stream)
+            return spec_kv_attention(q, cache, page_table, seq_lens, new_lens, scale=scale, window=window, sinks=sinks,
+                                     out=out, lse=lse, return_lse=return_lse, status=status, ws=ws, stream=stream)
     _check_stream(stream, cache.device)
     dtype = _first_check("q", q, "Hq")
     shape, dt, dev, index = q.shape, q.dtype, cache.device, cache._index
@@ -297,18 +300,17 @@ def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=No
              page_table.data_ptr(), seq_lens.data_ptr(), 0 if new_lens is None else new_lens.data_ptr(),
              row, qs[0], qs[1], qs[2], 0, 0, 0, 0, 0, 0, os[0], os[1], os[2], handle,
              0 if status is None else status.data_ptr())
-    args = (q.data_ptr(), cache._packed, out.data_ptr(), 0 if lse is None else lse.data_ptr())
+    args = (q.data_ptr(), cache._packed, sinks, out.data_ptr(), 0 if lse is None else lse.data_ptr())
     if ws is None:
         nbytes = L.spec_kv_attention_workspace_size(cache._packed, _PARAMS.pack(*fixed, 0, 0))
         ws = _workspace(key, max(nbytes, _WS_LEAST), dev, stream, capture)
-    code = L.spec_kv_attention(args[0], args[1], _PARAMS.pack(*fixed, ws.data_ptr(), ws.numel()), args[2], args[3])
+    code = L.spec_kv_attention_sinks(*args[:2], _PARAMS.pack(*fixed, ws.data_ptr(), ws.numel()), *args[2:])
     if code == binding.SPEC_ERR_INVALID_ARG and own and not capture:
         # the stream's workspace may be too small for this shape: a larger one is made, once
         nbytes = L.spec_kv_attention_workspace_size(cache._packed, _PARAMS.pack(*fixed, 0, 0))
         if nbytes > ws.numel():
             ws = _workspace(key, nbytes, dev, stream, capture)
-            code = L.spec_kv_attention(args[0], args[1], _PARAMS.pack(*fixed, ws.data_ptr(), ws.numel()), args[2],
-                                       args[3])
+            code = L.spec_kv_attention_sinks(*args[:2], _PARAMS.pack(*fixed, ws.data_ptr(), ws.numel()), *args[2:])
     if code != binding.SPEC_OK:
         raise binding.SpecError(code, "spec_kv_attention")
     return out if lse is None else (out, lse)
