@@ -9,6 +9,7 @@
  *
  *   spec_kv_append     rotates the new tokens' queries and keys by position and
  *                      stores their keys and values in the sequences' pages;
+ *   spec_kv_append_norm  the same, of heads that are normalised first;
  *   spec_kv_attention  attends from the new tokens' queries to every token
  *                      stored for their sequence up to their own position;
  *   spec_kv_attention_sinks  to the last ones and the first ones of them.
@@ -104,6 +105,25 @@ typedef struct {
  * written to that page.  Either stores SPEC_ERR_CACHE_RANGE in *status. */
 spec_status spec_kv_append(const void* q, const void* k, const void* v, const float* cos_sin,
                            const spec_kv_cache* cache, const spec_kv_params* params, void* q_out);
+
+/* Norms of queries and keys for each head, as models have them that normalise both
+ * before the rotation. */
+typedef struct {
+  const float* q_weight;     /* device: D weights of a head, contiguous; NULL: queries are not normalised */
+  const float* k_weight;     /* likewise for the keys */
+  int64_t q_head_stride;     /* elements from a head's weights to the next one's, >= 0 (0: all heads have the same) */
+  int64_t k_head_stride;
+  float eps;                 /* 2^-80 to 2^80 */
+} spec_kv_norms;
+
+/* spec_kv_append with norms (NULL: without): a head x of a query or key of a new token
+ * becomes (x r) w before it is rotated, with r = 1 / sqrt(mean of x_i^2 + eps) as the
+ * nearest float (once in about a million heads the next one), w its weights, and each
+ * product rounded to float.  A head with an infinity has r = 0, one with a NaN is NaN.
+ * Everything else is as for spec_kv_append. */
+spec_status spec_kv_append_norm(const void* q, const void* k, const void* v, const float* cos_sin,
+                                const spec_kv_norms* norms, const spec_kv_cache* cache, const spec_kv_params* params,
+                                void* q_out);
 
 /* Workspace bytes spec_kv_attention needs (0 if the parameters are invalid);
  * a function of B, T, Hq, Hkv, D and dtype alone.  A workspace is zero-filled once

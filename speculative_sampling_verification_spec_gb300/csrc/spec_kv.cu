@@ -22,6 +22,8 @@ constexpr int kMmaCtas = kSMs * 2;
 // What an item costs beside its tiles, in tiles.
 constexpr int kGenOverhead = 1;
 constexpr int kMmaOverhead = 4;
+// eps of the norms lies between this and its reciprocal: squares that get lost below the float range are nothing beside it
+constexpr float kLeastEps = 0x1p-80f;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -113,13 +115,20 @@ spec_status launch(const void* fn, int64_t grid, int threads, int smem, void* st
 }
 
 template <typename E, int PC, bool WARP>
-const void* append_ptr() {
-  return reinterpret_cast<const void*>(&spec_kv_append_kernel<E, PC, WARP>);
+const void* append_ptr(bool norm) {
+  return norm ? reinterpret_cast<const void*>(&spec_kv_append_kernel<E, PC, WARP, true>)
+              : reinterpret_cast<const void*>(&spec_kv_append_kernel<E, PC, WARP, false>);
 }
 template <typename E>
-const void* append_fn(bool vec, bool warp) {
-  return vec ? (warp ? append_ptr<E, 8, true>() : append_ptr<E, 8, false>())
-             : (warp ? append_ptr<E, 1, true>() : append_ptr<E, 1, false>());
+const void* append_fn(bool vec, bool warp, bool norm) {
+  return vec ? (warp ? append_ptr<E, 8, true>(norm) : append_ptr<E, 8, false>(norm))
+             : (warp ? append_ptr<E, 1, true>(norm) : append_ptr<E, 1, false>(norm));
+}
+
+// x as the sum of two floats
+void split(double x, float* hi, float* lo) {
+  *hi = static_cast<float>(x);
+  *lo = static_cast<float>(x - *hi);
 }
 
 // How the attention's work is cut; a function of B, T, Hq, Hkv, D and the kernel.
@@ -275,11 +284,23 @@ extern "C" {
 
 spec_status spec_kv_append(const void* q, const void* k, const void* v, const float* cos_sin,
                            const spec_kv_cache* cache, const spec_kv_params* params, void* q_out) {
+  return spec_kv_append_norm(q, k, v, cos_sin, nullptr, cache, params, q_out);
+}
+
+spec_status spec_kv_append_norm(const void* q, const void* k, const void* v, const float* cos_sin,
+                                const spec_kv_norms* norms, const spec_kv_cache* cache, const spec_kv_params* params,
+                                void* q_out) {
   spec_status s = check_shapes(cache, params);
   if (s != SPEC_OK) return s;
   const spec_kv_params* p = params;
   if (p->rot_dim < 0 || p->rot_dim % 2 || p->rot_dim > cache->D) return SPEC_ERR_INVALID_ARG;
   if (p->rot_dim > 0 && (!cos_sin || p->rot_len < 1 || !aligned(cos_sin, 16))) return SPEC_ERR_INVALID_ARG;
+  if (norms) {
+    if (!(norms->eps >= kLeastEps && norms->eps <= 1 / kLeastEps)) return SPEC_ERR_INVALID_ARG;
+    if (norms->q_head_stride < 0 || norms->k_head_stride < 0) return SPEC_ERR_INVALID_ARG;
+    if (!aligned(norms->q_weight, 4) || !aligned(norms->k_weight, 4)) return SPEC_ERR_INVALID_ARG;
+    if (norms->q_weight && !q) return SPEC_ERR_INVALID_ARG;
+  }
   if (p->B == 0) return SPEC_OK;
   s = check_cache(cache, p);
   if (s != SPEC_OK) return s;
@@ -312,11 +333,23 @@ spec_status spec_kv_append(const void* q, const void* k, const void* v, const fl
   const auto vec_ok = [&](const void* ptr, int64_t a1, int64_t a2, int64_t a3) {
     return aligned(ptr, 16) && (a1 * es) % 16 == 0 && (a2 * es) % 16 == 0 && (a3 * es) % 16 == 0;
   };
+  const bool norm = norms && (norms->q_weight || norms->k_weight);
+  if (norm) {
+    g.q_weight = norms->q_weight;
+    g.k_weight = norms->k_weight;
+    g.q_weight_head = norms->q_head_stride;
+    g.k_weight_head = norms->k_head_stride;
+    split(static_cast<double>(norms->eps) * cache->D, &g.eps_hi, &g.eps_lo);
+    split(std::sqrt(static_cast<double>(cache->D)), &g.root_hi, &g.root_lo);
+  }
   // eight pairs a thread where every chunk starts on a 16-byte boundary
-  const bool vec = p->rot_dim % 16 == 0 && vec_ok(k, g.k_seq, g.k_tok, g.k_head) &&
+  const bool vec = p->rot_dim % 16 == 0 && aligned(g.q_weight, 16) && aligned(g.k_weight, 16) &&
+                   g.q_weight_head % 4 == 0 && g.k_weight_head % 4 == 0 && vec_ok(k, g.k_seq, g.k_tok, g.k_head) &&
                    vec_ok(v, g.v_seq, g.v_tok, g.v_head) &&
                    (!q || (vec_ok(q, a.q_seq, a.q_tok, a.q_head) && vec_ok(q_out, a.o_seq, a.o_tok, a.o_head)));
-  const int per_tok = cache->D / (vec ? 16 : 2);
+  int per_tok = cache->D / (vec ? 16 : 2);
+  if (norm && vec) per_tok = per_tok > 8 ? 16 : per_tok > 4 ? 8 : per_tok > 2 ? 4 : per_tok;
+  g.tok_threads = per_tok;
   g.units_page = (p->T - 1 + S - 1) / S + 1;
   // a unit fits a warp's registers or takes a CTA
   const bool warp = per_tok <= 32 && std::min(p->T, S) <= 32 / per_tok * kAppendWarpIter;
@@ -340,7 +373,7 @@ spec_status spec_kv_append(const void* q, const void* k, const void* v, const fl
       beside * std::max<int64_t>(1, std::min<int64_t>(kAppendQueryRows, rows / (beside * kSMs * 2048 / threads))));
   const int64_t q_blocks = q ? (rows + g.q_rows_block - 1) / g.q_rows_block : 0;
   if (g.unit_blocks + q_blocks > INT_MAX) return SPEC_ERR_UNSUPPORTED;
-  const void* fn = p->dtype == SPEC_F32 ? append_fn<float>(vec, warp) : append_fn<__nv_bfloat16>(vec, warp);
+  const void* fn = p->dtype == SPEC_F32 ? append_fn<float>(vec, warp, norm) : append_fn<__nv_bfloat16>(vec, warp, norm);
   void* args[] = {&g};
   return launch(fn, g.unit_blocks + q_blocks, threads, 0, p->stream, args);
 }

@@ -1,6 +1,6 @@
 #pragma once
-// spec_kv_append.cuh -- rotate the new tokens' queries and keys, store keys and
-// values in the paged 8-bit cache.
+// spec_kv_append.cuh -- normalise each head of the new tokens' queries and keys where
+// that is asked for, rotate them, store keys and values in the paged 8-bit cache.
 //
 // A unit is what one call writes to one (page, key/value head) of the keys or of
 // the values: at most page_size tokens.  Its scale depends on all of them (the
@@ -20,6 +20,15 @@
 //
 // A thread handles chunks of PC rotation pairs, 2 * PC channels: PC = 8 moves 16
 // bytes at a time and more where everything is aligned, PC = 1 single channels.
+//
+// Norms.  r = 1 / sqrt(mean x^2 + eps) of a head goes to the keys' scales and codes
+// through comparisons and roundings, so it is made a function of the inputs alone: the
+// sum of the squares and its root are carried in two floats (some 45 bits), and r is the
+// nearest float but for one row in a million.  (In 64 bits the sums of a prompt alone
+// would take longer than the rest: the chip's rate of such multiply-adds is a hundredth
+// of that in 32.)  The threads of a head are a power of two of neighbouring lanes, the
+// last of them idle where its chunks are not, and add up by exchanging; with PC = 1 a
+// warp first takes the norms of a unit's tokens, and a whole head of a query.
 #include "spec_kv_common.cuh"
 
 namespace spec_kv_detail {
@@ -38,6 +47,12 @@ struct AppendArgs {
   int32_t unit_blocks;   // blocks that take groups; the rest take queries
   int32_t q_rows_block;  // (sequence, token) rows a query block takes
   int32_t q_heads;       // heads a query thread takes: 1 or kAppendHeads
+  int32_t tok_threads;   // threads of a token's head: its chunks, or the power of two above
+  // norms: weights (NULL: not normalised), and D * eps and sqrt(D) as sums of two floats
+  const float* q_weight;
+  const float* k_weight;
+  int64_t q_weight_head, k_weight_head;
+  float eps_hi, eps_lo, root_hi, root_lo;
 };
 
 // N consecutive elements as they are in memory: 8 of them in 16-byte words, or one
@@ -138,6 +153,12 @@ struct RawChunk {
     lo.load(row + k.lo);
     hi.load(row + k.hi);
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (uint4& u : lo.w) u = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (uint4& u : hi.w) u = make_uint4(0, 0, 0, 0);
+  }
   __device__ __forceinline__ void values(float* y) const {
     lo.values(y);
     hi.values(y + PC);
@@ -171,6 +192,87 @@ __device__ __forceinline__ void turn_chunk(const AppendArgs& g, const float* cs,
 }
 
 __device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
+// A sum of squares in two floats: s, and what roundings have taken from it.
+struct Sum2 {
+  float s, e;
+  // (the error of a rounded sum, exactly)
+  static __device__ __forceinline__ float lost(float a, float b, float sum) {
+    const float bb = __fsub_rn(sum, a);
+    return __fadd_rn(__fsub_rn(a, __fsub_rn(sum, bb)), __fsub_rn(b, bb));
+  }
+  __device__ __forceinline__ void add(const Sum2& o) {
+    const float t = __fadd_rn(s, o.s);
+    e = __fadd_rn(__fadd_rn(e, o.e), lost(s, o.s, t));
+    s = t;
+  }
+};
+
+// Of N values times `factor` (a power of two); two at a time, and their two sums at the end.
+template <typename E, int N>
+__device__ __forceinline__ Sum2 squares(const float* x, float factor) {
+  const u64 f = pack2(factor, factor), minus = pack2(-1.0f, -1.0f);
+  u64 s = pack2(0.0f, 0.0f), e = s;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const u64 y = mul2(pack2(x[i], x[i + 1]), f), p = mul2(y, y);
+    const u64 t = add2(s, p), b = fma2(s, minus, t);                   // b = t - s
+    u64 lost = add2(fma2(fma2(b, minus, t), minus, s), fma2(b, minus, p));  // (s - (t - b)) + (p - b)
+    if constexpr (sizeof(E) == 4) lost = add2(lost, fma2(y, y, mul2(p, minus)));  // (16-bit values' squares are exact)
+    e = add2(e, lost);
+    s = t;
+  }
+  Sum2 a, b;
+  unpack2(s, a.s, b.s);
+  unpack2(e, a.e, b.e);
+  a.add(b);
+  return a;
+}
+
+// sqrt(D) / sqrt(sum + D eps), to the nearest float: an approximate root and one step of Newton's in two floats.
+__device__ __forceinline__ float norm_of(const AppendArgs& g, const Sum2& a, float eps_hi, float eps_lo) {
+  const float u = __fadd_rn(a.s, eps_hi);
+  const float ul = __fadd_rn(__fadd_rn(Sum2::lost(a.s, eps_hi, u), a.e), eps_lo);
+  const float r = rsqrtf(u);
+  const float q = __fmul_rn(r, r), ql = fmaf(r, r, -q);
+  const float p = __fmul_rn(u, q), pl = fmaf(ul, q, fmaf(u, ql, fmaf(u, q, -p)));
+  const float step = __fmul_rn(__fmul_rn(0.5f, r), __fsub_rn(__fsub_rn(1.0f, p), pl));
+  const float m = __fmul_rn(r, g.root_hi);
+  return __fadd_rn(m, fmaf(step, g.root_hi, fmaf(r, g.root_lo, fmaf(r, g.root_hi, -m))));
+}
+
+// The norm factor of a head whose channels lie with `threads` neighbouring lanes (a power of two), N each.
+// Squares that come near the end of the float range are taken of the values times 2^-84.
+template <typename E, int N>
+__device__ __forceinline__ float head_norm(const AppendArgs& g, const float* x, int threads) {
+  const unsigned lane = threadIdx.x & 31;
+  const unsigned mask = threads == 32 ? kFull : ((1u << threads) - 1) << (lane & ~(threads - 1u));
+  const auto over_lanes = [&](Sum2 a) {
+    for (int d = threads >> 1; d; d >>= 1) {
+      Sum2 o;
+      o.s = __shfl_xor_sync(mask, a.s, d);
+      o.e = __shfl_xor_sync(mask, a.e, d);
+      a.add(o);
+    }
+    return a;
+  };
+  Sum2 a = over_lanes(squares<E, N>(x, 1.0f));
+  if (a.s < 0x1p80f) return norm_of(g, a, g.eps_hi, g.eps_lo);
+  a = over_lanes(squares<E, N>(x, 0x1p-84f));
+  if (!is_finite(a.s)) return a.s > 0.0f ? 0.0f : a.s;  // infinities: 0; NaN
+  return norm_of(g, a, g.eps_hi * 0x1p-84f * 0x1p-84f, g.eps_lo * 0x1p-84f * 0x1p-84f) * 0x1p-84f;
+}
+
+// Normalised values: (x r) w, each product rounded.
+template <int PC>
+__device__ __forceinline__ void scale_chunk(float* y, float r, const float* weight, const ChunkAt& k) {
+  float w[2 * PC];
+  load_n<float, PC>(weight + k.lo, w);
+  load_n<float, PC>(weight + k.hi, w + PC);
+#pragma unroll
+  for (int i = 0; i < 2 * PC; ++i) y[i] = __fmul_rn(__fmul_rn(y[i], r), w[i]);
+}
+
 
 // 2^e, e the least integer >= kMinScaleExp with amax <= 448 * 2^e (448 = 1.75 * 2^8,
 // the largest e4m3 value): from the exponent and mantissa fields, with no rounding
@@ -221,6 +323,18 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float* x, const Di
   }
 }
 
+// The norm factor of a head by a whole warp, straight from memory.
+template <typename E>
+__device__ __forceinline__ float row_norm(const AppendArgs& g, const E* x) {
+  float y[8];  // channels lane, lane + 32, ... of at most 256
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int d = (threadIdx.x & 31) + 32 * i;
+    y[i] = d < g.a.D ? to_float(x[d]) : 0.0f;
+  }
+  return head_norm<E, 8>(g, y, 32);
+}
+
 // lengths of sequence b against this call's limits
 __device__ __forceinline__ bool append_span(const AppendArgs& g, int b, int* L, int* n) {
   const KvArgs& a = g.a;
@@ -240,11 +354,12 @@ constexpr int kAppendCtaIter = sizeof(E) == 2 ? 4 : 2;
 // Heads a query thread turns by one load of a position's angles, where the call is
 // large; chunks it has under way at once, and rows it takes in all.
 constexpr int kAppendHeads = 4, kAppendQueryRows = 16;
+constexpr int kMostSlots = 128;  // of a page
 
 // A group of units: `units` consecutive (head, keys or values) of one page of a
 // sequence, by a warp or a CTA.  What they share is worked out once.
-template <typename E, int PC, bool WARP>
-__device__ __forceinline__ void append_group(const AppendArgs& g, int group, int t, uint32_t* red) {
+template <typename E, int PC, bool WARP, bool NORM>
+__device__ __forceinline__ void append_group(const AppendArgs& g, int group, int t, uint32_t* red, float* norms) {
   constexpr int nt = WARP ? 32 : kAppendCtaThreads;
   constexpr int ITER = WARP ? kAppendWarpIter : kAppendCtaIter<E>;
   const KvArgs& a = g.a;
@@ -263,9 +378,10 @@ __device__ __forceinline__ void append_group(const AppendArgs& g, int group, int
   const int page = page_of(a, b, pi);
   // a thread has one chunk of a token and every `step`th token, so that its chunk's
   // place is worked out once (threads past the last whole token have nothing)
-  const int per_tok = a.D / (2 * PC), tokens = p1 - p0;
+  const int per_tok = NORM ? g.tok_threads : a.D / (2 * PC), tokens = p1 - p0;
   const int step = nt / per_tok, tok0 = t / per_tok;
-  const ChunkAt at = chunk_at<PC>(g, t - tok0 * per_tok);
+  const bool has = !NORM || t - tok0 * per_tok < a.D / (2 * PC);  // the thread's chunk is one
+  const ChunkAt at = chunk_at<PC>(g, has ? t - tok0 * per_tok : 0);
   const int mine = tok0 < step ? (tokens - tok0 + step - 1) / step : 0;  // this thread's tokens
   const bool hold = tokens <= ITER * step;
   const int kept = p0 & (S - 1);  // earlier tokens of the sequence in this page
@@ -279,14 +395,54 @@ __device__ __forceinline__ void append_group(const AppendArgs& g, int group, int
     const E* const x = static_cast<const E*>(kv ? g.v : g.k) + b * (kv ? g.v_seq : g.k_seq) +
                        h * (kv ? g.v_head : g.k_head) + token * x_tok;
     const bool turned = !kv && g.rot > 0;
+    const float* const weight = NORM && !kv && g.k_weight ? g.k_weight + h * g.k_weight_head : nullptr;
+    if constexpr (NORM && PC == 1) {
+      // the unit's tokens, a warp each
+      if constexpr (!WARP) __syncthreads();  // the norms before have been used
+      if (weight) {
+        const E* const x0 = x - tok0 * x_tok;
+        for (int i = WARP ? 0 : t >> 5; i < tokens; i += WARP ? 1 : nt / 32) {
+          const float r = row_norm<E>(g, x0 + i * x_tok);
+          if ((t & 31) == 0) norms[i] = r;
+        }
+      }
+      if constexpr (WARP)
+        __syncwarp();
+      else
+        __syncthreads();
+    }
     RawChunk<E, PC> raw[ITER];
+    float norm[ITER];
     const auto read = [&](int i0) {
 #pragma unroll
       for (int it = 0; it < ITER; ++it)
-        if (i0 + it < mine) raw[it].load(x + (i0 + it) * x_step, at);
+        if (i0 + it < mine) {
+          if (has)
+            raw[it].load(x + (i0 + it) * x_step, at);
+          else
+            raw[it].clear();
+        }
+      if constexpr (NORM) {
+        if (weight) {
+#pragma unroll
+          for (int it = 0; it < ITER; ++it) {
+            if (i0 + it < mine) {
+              if constexpr (PC == 1) {
+                norm[it] = norms[tok0 + (i0 + it) * step];
+              } else {
+                float y[2 * PC];
+                raw[it].values(y);
+                norm[it] = head_norm<E, 2 * PC>(g, y, per_tok);
+              }
+            }
+          }
+        }
+      }
     };
     const auto values = [&](int i0, int it, float* y) {
       raw[it].values(y);
+      if constexpr (NORM)
+        if (weight) scale_chunk<PC>(y, norm[it], weight, at);
       if (turned) turn_chunk<PC>(g, cs + static_cast<int64_t>(i0 + it) * cs_step, at, y);
     };
     const auto largest = [&](uint32_t v) {
@@ -313,6 +469,7 @@ __device__ __forceinline__ void append_group(const AppendArgs& g, int group, int
         if (i0 + it < mine) {
           float y[2 * PC];
           values(i0, it, y);
+          if (!has) continue;  // (a neighbour's weights times zero may be NaN)
 #pragma unroll
           for (int j = 0; j < 2 * PC; ++j) top = max(top, __float_as_uint(y[j]) & 0x7fffffffu);
         }
@@ -341,7 +498,7 @@ __device__ __forceinline__ void append_group(const AppendArgs& g, int group, int
 #pragma unroll
             for (int j = 0; j < 2 * PC; ++j) {
               const uint32_t m = __float_as_uint(y[j]) & 0x7fffffffu;
-              top = max(top, m < 0x7f800000u ? m : 0u);
+              top = max(top, has && m < 0x7f800000u ? m : 0u);
             }
           }
         }
@@ -386,8 +543,10 @@ __device__ __forceinline__ void append_group(const AppendArgs& g, int group, int
           uint8_t* dst = codes + (i0 + it) * code_step;
           float y[2 * PC];
           values(i0, it, y);
-          store_codes<PC>(dst + at.lo, y, div, plain);
-          store_codes<PC>(dst + at.hi, y + PC, div, plain);
+          if (has) {
+            store_codes<PC>(dst + at.lo, y, div, plain);
+            store_codes<PC>(dst + at.hi, y + PC, div, plain);
+          }
         }
       }
       i0 += ITER;
@@ -395,7 +554,37 @@ __device__ __forceinline__ void append_group(const AppendArgs& g, int group, int
   }
 }
 
-template <typename E, int PC, bool WARP>
+// Queries of single channels with norms: a head of a row is a warp's, whose lanes read and write the same pairs.
+template <typename E>
+__device__ __forceinline__ void norm_queries(const AppendArgs& g, int row0, int row1, int warp, int warps) {
+  const KvArgs& a = g.a;
+  const int lane = threadIdx.x & 31;
+  for (int i = warp; i < (row1 - row0) * a.Hq; i += warps) {
+    const int row = row0 + i / a.Hq, h = i - (row - row0) * a.Hq, b = row / a.T, tok = row - b * a.T;
+    int L, n;
+    const bool ok = append_span(g, b, &L, &n);
+    if (!ok && lane == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+    const E* q = static_cast<const E*>(a.q) + b * a.q_seq + h * a.q_head + tok * a.q_tok;
+    E* o = static_cast<E*>(a.out) + b * a.o_seq + h * a.o_head + tok * a.o_tok;
+    if (!ok || tok >= n) {
+      const float fill = ok ? 0.0f : __uint_as_float(0x7fc00000u);
+      for (int d = lane; d < a.D; d += 32) from_float(fill, o + d);
+      continue;
+    }
+    const float r = row_norm<E>(g, q);  // (every lane's channels are read before any is written)
+    const float* cs = g.cos_sin + (g.rot > 0 ? static_cast<int64_t>(L + tok) * g.rot : 0);
+    for (int p = lane; p < a.D / 2; p += 32) {
+      const ChunkAt k = chunk_at<1>(g, p);
+      float y[2] = {to_float(q[k.lo]), to_float(q[k.hi])};
+      scale_chunk<1>(y, r, g.q_weight + h * g.q_weight_head, k);
+      turn_chunk<1>(g, cs, k, y);
+      from_float(y[0], o + k.lo);
+      from_float(y[1], o + k.hi);
+    }
+  }
+}
+
+template <typename E, int PC, bool WARP, bool NORM>
 __global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads, WARP ? 1 : kAppendCtas)
     spec_kv_append_kernel(const __grid_constant__ AppendArgs g) {
   constexpr int nt = WARP ? kAppendWarpThreads : kAppendCtaThreads;
@@ -405,16 +594,25 @@ __global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads,
   wait_for_grid();
   if (blockIdx.x < static_cast<unsigned>(g.unit_blocks)) {
     __shared__ __align__(16) uint32_t red[WARP ? 4 : kAppendCtaThreads / 32];
+    __shared__ float norms[NORM && PC == 1 ? (WARP ? nt / 32 : 1) : 1][NORM && PC == 1 ? kMostSlots : 1];
     if constexpr (WARP) {
       const int group = blockIdx.x * (kAppendWarpThreads / 32) + (tid >> 5);
-      if (group < g.groups) append_group<E, PC, true>(g, group, tid & 31, red);
+      if (group < g.groups)
+        append_group<E, PC, true, NORM>(g, group, tid & 31, red, norms[NORM && PC == 1 ? tid >> 5 : 0]);
     } else {
-      append_group<E, PC, false>(g, blockIdx.x, tid, red);
+      append_group<E, PC, false, NORM>(g, blockIdx.x, tid, red, norms[0]);
     }
     return;
   }
+  if constexpr (NORM && PC == 1) {
+    if (g.q_weight) {
+      const int row0 = static_cast<int>(blockIdx.x - g.unit_blocks) * g.q_rows_block;
+      norm_queries<E>(g, row0, min(a.B * a.T, row0 + g.q_rows_block), tid >> 5, nt / 32);
+      return;
+    }
+  }
   // queries: rows (sequence, token); as many side by side as the CTA has threads for
-  const int per_tok = a.D / (2 * PC), heads = a.Hq / g.q_heads, per_row = heads * per_tok;
+  const int per_tok = NORM ? g.tok_threads : a.D / (2 * PC), heads = a.Hq / g.q_heads, per_row = heads * per_tok;
   const int beside = max(1, nt / per_row);
   const int r0 = tid / per_row;  // this thread's row among those side by side
   if (beside > 1 && r0 >= beside) return;
@@ -423,7 +621,11 @@ __global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads,
   const int first = row0 + (beside > 1 ? r0 : 0), last = min(nrows, row0 + g.q_rows_block);
   for (int j = beside > 1 ? tid - r0 * per_row : tid; j < per_row; j += nt) {
     const int h = j / per_tok;
-    const ChunkAt k = chunk_at<PC>(g, j - h * per_tok);
+    const bool has = !NORM || j - h * per_tok < a.D / (2 * PC);  // the thread's chunk is one
+    const ChunkAt k = chunk_at<PC>(g, has ? j - h * per_tok : 0);
+    // (heads a thread takes lie `heads` apart)
+    const float* const weight = NORM && g.q_weight ? g.q_weight + h * g.q_weight_head : nullptr;
+    const int64_t w_heads = heads * g.q_weight_head;
     int b = first / a.T, tok = first - b * a.T;
     for (int row = first; row < last;) {
       // this sequence's rows among the CTA's: the new tokens, then the empty slots
@@ -441,9 +643,15 @@ __global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads,
         for (int i = 0; i < full; ++i, q += q_step, o += o_step, cs += beside * g.rot) {
           float y[2 * PC];
           RawChunk<E, PC> raw;
-          raw.load(q, k);
+          if (has)
+            raw.load(q, k);
+          else
+            raw.clear();
           raw.values(y);
+          if constexpr (NORM && PC > 1)
+            if (weight) scale_chunk<PC>(y, head_norm<E, 2 * PC>(g, y, per_tok), weight, k);
           turn_chunk<PC>(g, cs, k, y);
+          if (!has) continue;
           store_n<E, PC>(o + k.lo, y);
           store_n<E, PC>(o + k.hi, y + PC);
         }
@@ -451,13 +659,21 @@ __global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads,
         for (int i = 0; i < full; ++i, q += q_step, o += o_step, cs += beside * g.rot) {
           RawChunk<E, PC> raw[kAppendHeads];
 #pragma unroll
-          for (int e = 0; e < kAppendHeads; ++e) raw[e].load(q + e * q_heads, k);
+          for (int e = 0; e < kAppendHeads; ++e) {
+            if (has)
+              raw[e].load(q + e * q_heads, k);
+            else
+              raw[e].clear();
+          }
           const Angles<PC> at(g, cs, k);
 #pragma unroll
           for (int e = 0; e < kAppendHeads; ++e) {
             float y[2 * PC];
             raw[e].values(y);
+            if constexpr (NORM && PC > 1)
+              if (weight) scale_chunk<PC>(y, head_norm<E, 2 * PC>(g, y, per_tok), weight + e * w_heads, k);
             at.turn_all(g, k, y);
+            if (!has) continue;
             store_n<E, PC>(o + e * o_heads + k.lo, y);
             store_n<E, PC>(o + e * o_heads + k.hi, y + PC);
           }
@@ -466,7 +682,7 @@ __global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads,
       float fill[PC];
 #pragma unroll
       for (int e = 0; e < PC; ++e) fill[e] = ok ? 0.0f : __uint_as_float(0x7fc00000u);
-      for (int i = full; i < rows; ++i, o += o_step) {
+      for (int i = full; has && i < rows; ++i, o += o_step) {
         for (int e = 0; e < g.q_heads; ++e) {
           store_n<E, PC>(o + e * o_heads + k.lo, fill);
           store_n<E, PC>(o + e * o_heads + k.hi, fill);

@@ -15,12 +15,13 @@ import torch
 
 from . import binding
 
-EXPORTED = ("spec_kv_append", "spec_kv_attention", "spec_kv_attention_sinks", "spec_kv_attention_workspace_size",
-            "spec_kv_capture_id")
+EXPORTED = ("spec_kv_append", "spec_kv_append_norm", "spec_kv_attention", "spec_kv_attention_sinks",
+            "spec_kv_attention_workspace_size", "spec_kv_capture_id")
 
-# spec_kv_cache and spec_kv_params of include/spec_kv.h, in native layout
+# spec_kv_cache, spec_kv_params and spec_kv_norms of include/spec_kv.h, in native layout
 _CACHE = struct.Struct("@4i4P5q")
 _PARAMS = struct.Struct("@6if3i3P13q3PN")
+_NORMS = struct.Struct("@2P2qf")
 _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 _DTYPES = {_F32: binding.SPEC_F32, _BF16: binding.SPEC_BF16}
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -43,6 +44,8 @@ def _lib():
         L.spec_kv_attention_sinks.restype = ctypes.c_int
         L.spec_kv_append.argtypes = [P] * 7
         L.spec_kv_append.restype = ctypes.c_int
+        L.spec_kv_append_norm.argtypes = [P] * 8
+        L.spec_kv_append_norm.restype = ctypes.c_int
         L.spec_kv_capture_id.argtypes = [P]
         L.spec_kv_capture_id.restype = ctypes.c_uint64
         _loaded = L
@@ -197,20 +200,31 @@ def _first_check(name, t, heads):
     return dtype
 
 
-def spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens=None, *, cos_sin=None, interleaved=False,
-                   q_out=None, status=None, stream=None):
+def _weight(name, w, heads, D, device):
+    """Address and head stride of a norm's weights, after checking them."""
+    if w.dtype is not _F32 or w.get_device() != device or w.shape not in ((D,), (heads, D)) or w.stride(-1) != 1:
+        raise ValueError("%s must be float32 [head_dim] or [heads, head_dim] on the cache's device, contiguous along the "
+                         "channels" % name)
+    return w.data_ptr(), w.stride(0) if w.dim() == 2 else 0
+
+
+def spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens=None, *, cos_sin=None, interleaved=False, q_norm=None,
+                   k_norm=None, norm_eps=1e-6, q_out=None, status=None, stream=None):
     """Rotate the new tokens' queries and keys by position and store their keys and values.
 
     q [B, T, Hq, D] (or None), k and v [B, T, kv_heads, D]: float32 or bfloat16, any strides with the channels
     contiguous.  page_table int32 [B, max_pages]; seq_lens int32 [B]: tokens stored before; new_lens int32 [B]: new
     tokens, at most T (None: T each).  cos_sin float32 [positions, rot_dim]: cosines of a position's angles, then their
     sines (None: no rotation); interleaved: pairs are neighbouring channels, else channels i and i + rot_dim / 2.
+    q_norm, k_norm: float32 weights [head_dim], or [heads, head_dim], of norms of the queries' and the keys' heads before
+    the rotation, x / sqrt(mean(x ** 2) + norm_eps) * weight (None: no norm).
     Returns the rotated queries (q_out, or a new contiguous tensor; zero in slots past new_lens); q_out may be q.
     The cache is written in place.  The call runs on the cache's device, whichever is current."""
     if _current_device() != cache._index:
         with torch.cuda.device(cache._index):
             return spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens, cos_sin=cos_sin,
-                                  interleaved=interleaved, q_out=q_out, status=status, stream=stream)
+                                  interleaved=interleaved, q_norm=q_norm, k_norm=k_norm, norm_eps=norm_eps,
+                                  q_out=q_out, status=status, stream=stream)
     _check_stream(stream, cache.device)
     dtype = _first_check("k", k, "kv_heads")
     shape, dt, dev, index = k.shape, k.dtype, cache.device, cache._index
@@ -239,13 +253,18 @@ def spec_kv_append(q, k, v, cache, page_table, seq_lens, new_lens=None, *, cos_s
         else:
             os = _strides("q_out", q_out, shape, dt, index)
         qp, op = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out without q")
+    elif q_out is not None or q_norm is not None:
+        raise ValueError("q_out or q_norm without q")
+    norms = None
+    if q_norm is not None or k_norm is not None:
+        qw, qh = (0, 0) if q_norm is None else _weight("q_norm", q_norm, hq, D, index)
+        kw, kh = (0, 0) if k_norm is None else _weight("k_norm", k_norm, cache.kv_heads, D, index)
+        norms = _NORMS.pack(qw, kw, qh, kh, norm_eps)
     prm = _PARAMS.pack(B, T, hq, dtype, columns, 0, 0.0, rot, rot_len, 1 if interleaved else 0,
                        page_table.data_ptr(), seq_lens.data_ptr(), 0 if new_lens is None else new_lens.data_ptr(),
                        row, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], os[0],
                        os[1], os[2], _stream_of(stream, dev), 0 if status is None else status.data_ptr(), 0, 0)
-    code = _lib().spec_kv_append(qp, k.data_ptr(), v.data_ptr(), cs, cache._packed, prm, op)
+    code = _lib().spec_kv_append_norm(qp, k.data_ptr(), v.data_ptr(), cs, norms, cache._packed, prm, op)
     if code != binding.SPEC_OK:
         raise binding.SpecError(code, "spec_kv_append")
     return q_out
