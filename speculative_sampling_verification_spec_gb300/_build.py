@@ -1,12 +1,12 @@
 """In-tree build of libspecverify.so (CUDA kernels for sm_103a + the C ABI).
 
-Nine compilation units, one -gencode, compiled in parallel and linked with the
+Ten compilation units, one -gencode, compiled in parallel and linked with the
 shared cudart (so the process keeps a single CUDA runtime with PyTorch): the
 host side of verification (csrc/spec_verify.cu), six groups of its kernels
 (csrc/kernel_unit.cu with SPECV_UNIT = 1..6; both include
 csrc/spec_kernels.cuh), and the paged key/value cache (csrc/spec_kv.cu, with
-its tensor-core kernel in csrc/spec_kv_mma.cu).  The library is written next to
-this file.
+its tensor-core kernel in csrc/spec_kv_mma.cu and its pages in
+csrc/spec_kv_pages.cu).  The library is written next to this file.
 """
 from __future__ import annotations
 
@@ -17,7 +17,7 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-HDRS = [os.path.join(ROOT, "include", h) for h in ("spec_verify.h", "spec_kv.h")]
+HDRS = [os.path.join(ROOT, "include", h) for h in ("spec_verify.h", "spec_kv.h", "spec_kv_pages.h")]
 LIB = os.path.join(PKG, "libspecverify.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -25,7 +25,7 @@ COMPILE_FLAGS = ["-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC"]
 LINK_FLAGS = [*ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath,/usr/local/cuda/lib64"]
 # (source, extra defines); the heaviest units first, so they start first
 UNITS = [("kernel_unit.cu", ["-DSPECV_UNIT=%d" % u]) for u in (6, 5, 2, 1, 4, 3)]
-UNITS += [("spec_kv_mma.cu", []), ("spec_kv.cu", []), ("spec_verify.cu", [])]
+UNITS += [("spec_kv_mma.cu", []), ("spec_kv.cu", []), ("spec_verify.cu", []), ("spec_kv_pages.cu", [])]
 
 
 def nvcc() -> str:

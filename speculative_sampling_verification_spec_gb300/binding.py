@@ -21,7 +21,7 @@ SPEC_ERR_INVALID_ARG = 1
 SPEC_F32, SPEC_BF16 = 0, 1
 STATUS_NAMES = {0: "SPEC_OK", 1: "SPEC_ERR_INVALID_ARG", 2: "SPEC_ERR_CUDA", 3: "SPEC_ERR_NONFINITE",
                 4: "SPEC_ERR_TOKEN_RANGE", 5: "SPEC_ERR_TIMEOUT", 6: "SPEC_ERR_UNSUPPORTED",
-                7: "SPEC_ERR_SCRATCH_LIMIT", 8: "SPEC_ERR_CACHE_RANGE"}
+                7: "SPEC_ERR_SCRATCH_LIMIT", 8: "SPEC_ERR_CACHE_RANGE", 9: "SPEC_ERR_CACHE_FULL"}
 SPEC_NOALLOC_SCRATCH_BYTES = 8 << 20
 EXPORTED = ("spec_verify", "spec_sample_draft", "spec_verify_workspace_size",
             "spec_sample_draft_workspace_size", "spec_read_row_stats", "spec_status_string",

@@ -1,0 +1,500 @@
+// spec_kv_pages.cu -- the pages of the paged cache: argument checks, kernels and the
+// C ABI entry points of include/spec_kv_pages.h.
+//
+// Holding and forking are one kernel, which walks the page table and the counts:
+//
+//   1. every entry of the table is brought up to date but for the pages that are
+//      missing: releases count down, shared pages count up, and what is missing
+//      becomes a bit;
+//   2. once all counts are final, every page that is free becomes a bit;
+//   3. the k-th missing entry (sequence by sequence, page by page) takes the k-th free
+//      page: a count of the bits before it, and a search for the page.
+//
+// Between the steps everything has to be known everywhere, so the kernel is one
+// thread-block cluster, whose barrier costs well under a microsecond where another
+// launch costs one or two.  Its CTAs each have a stretch of the table and of the pool;
+// the bits and how many come before each word of them stay in their shared memory,
+// where the others search them: nothing is kept in a workspace, and the order of the
+// atomic counts (whole numbers) changes nothing.
+//
+// Forking ends with a second kernel that copies what the last pages hold.
+#include "kernel_table.h"
+#include "spec_kv_common.cuh"
+#include "spec_kv_pages.h"
+
+#include <algorithm>
+#include <atomic>
+
+namespace {
+
+using namespace spec_kv_detail;
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kMostCtas = 8;  // of a cluster
+constexpr int kBatch = 4;     // words of a warp under way at once
+
+struct PagesArgs {
+  int32_t* refs;
+  int32_t* table;
+  int64_t table_stride;
+  int32_t* free_pages;
+  int32_t* status;
+  int32_t num_pages, log_page, B, max_pages;
+  const int32_t* new_lens;
+  int32_t T, window, sinks;
+  int32_t* seq_lens;  // written by forks
+  const int32_t* parents;
+  int32_t row_words;                // words of bits of a row of the table
+  int32_t need_words, free_words;   // of all rows; of the pool
+  int32_t need_share, free_share;   // of a CTA
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// all threads of the cluster; what they wrote is seen by all
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// a word of another CTA's shared memory
+__device__ __forceinline__ uint32_t load_of(uint32_t rank, const uint32_t* here) {
+  uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(here)), v;
+  asm volatile(
+      "{\n\t.reg .b32 there;\n\tmapa.shared::cluster.u32 there, %1, %2;\n\tld.shared::cluster.u32 %0, [there];\n\t}"
+      : "=r"(v)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// What a row of the table becomes.
+struct Row {
+  bool leave;        // nothing happens to it
+  int last;          // columns from this on are empty
+  int keep, from;    // hold: columns below `keep` and from `from` on are needed
+  int parent;        // fork
+};
+
+__device__ __forceinline__ Row hold_row(const PagesArgs& a, int b) {
+  Row r;
+  const int L = a.seq_lens[b], n = a.new_lens ? a.new_lens[b] : a.T;
+  const int64_t end = static_cast<int64_t>(L) + n;
+  r.leave = L < 0 || n < 0 || end > (static_cast<int64_t>(a.max_pages) << a.log_page);
+  r.parent = -1;
+  const int S1 = (1 << a.log_page) - 1;
+  r.last = r.leave ? 0 : static_cast<int>((end + S1) >> a.log_page);
+  r.keep = a.sinks > 0 ? ((a.sinks - 1) >> a.log_page) + 1 : 0;
+  r.from = a.window > 0 && L >= a.window ? (L + 1 - a.window) >> a.log_page : 0;
+  return r;
+}
+
+// A copy's parent; -1: the row stays, -2: it should not, but its parent cannot be one.
+__device__ __forceinline__ int parent_of(const PagesArgs& a, int b, int* L) {
+  const int p = a.parents[b];
+  if (p == -1 || p == b) return -1;
+  if (p < 0 || p >= a.B) return -2;
+  const int pp = a.parents[p];
+  *L = a.seq_lens[p];
+  if ((pp != -1 && pp != p) || *L < 0 || *L > (static_cast<int64_t>(a.max_pages) << a.log_page)) return -2;
+  return p;
+}
+
+// Exclusive counts of the bits of `words` words, and their total: by all threads.
+__device__ uint32_t count_before(const uint32_t* bits, uint32_t* before, int words, uint32_t* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (words + kThreads - 1) / kThreads;
+  const int i0 = min(words, static_cast<int>(threadIdx.x) * per), i1 = min(words, i0 + per);
+  uint32_t mine = 0;
+  for (int i = i0; i < i1; ++i) mine += __popc(bits[i]);
+  uint32_t inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t o = __shfl_up_sync(kFull, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  uint32_t at = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) at += scratch[w];
+    total += scratch[w];
+  }
+  for (int i = i0; i < i1; ++i) {
+    before[i] = at;
+    at += __popc(bits[i]);
+  }
+  __syncthreads();
+  return total;
+}
+
+// Bound by latency and by what the cluster's few SMs can ask for at once.
+template <bool FORK>
+__global__ void __launch_bounds__(kThreads, 1) spec_kv_pages_kernel(const __grid_constant__ PagesArgs a) {
+  extern __shared__ uint32_t dyn[];
+  __shared__ uint32_t scratch[kWarps], total[2];            // this CTA's missing entries and free pages
+  __shared__ uint32_t need_at[kMostCtas + 1], free_at[kMostCtas + 1];
+  uint32_t* const need = dyn;
+  uint32_t* const need_before = need + a.need_share;
+  uint32_t* const avail = need_before + a.need_share;
+  uint32_t* const avail_before = avail + a.free_share;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_rank()), ctas = static_cast<int>(cluster_size());
+  const int w0 = min(a.need_words, rank * a.need_share), nw = min(a.need_words - w0, a.need_share);
+  const int f0 = min(a.free_words, rank * a.free_share), nf = min(a.free_words - f0, a.free_share);
+  start_dependents();
+  wait_for_grid();
+
+  // ---- 1. the table
+  for (int i0 = warp; i0 < nw; i0 += kWarps * kBatch) {
+    int32_t entry[kBatch], source[kBatch];
+    Row row[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kWarps;
+      entry[k] = source[k] = -1;
+      row[k].leave = true;
+      if (i >= nw) continue;
+      const int b = (w0 + i) / a.row_words, c = (w0 + i - b * a.row_words) * 32 + lane;
+      if constexpr (FORK) {
+        int L = 0;
+        const int p = parent_of(a, b, &L);
+        row[k].leave = p < 0;
+        row[k].parent = p;
+        row[k].last = L;
+        if (p == -2 && c == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+        if (p >= 0 && c == 0) a.seq_lens[b] = L;
+        if (p >= 0 && c < a.max_pages) source[k] = a.table[p * a.table_stride + c];
+      } else {
+        row[k] = hold_row(a, b);
+        if (row[k].leave && c == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+      }
+      if (!row[k].leave && c < a.max_pages) entry[k] = a.table[b * a.table_stride + c];
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kWarps;
+      if (i >= nw) continue;
+      const int b = (w0 + i) / a.row_words, c = (w0 + i - b * a.row_words) * 32 + lane;
+      int32_t* const at = a.table + b * a.table_stride + c;
+      bool missing = false;
+      if (!row[k].leave && c < a.max_pages) {
+        if constexpr (FORK) {
+          const int whole = row[k].last >> a.log_page;
+          const bool partly = c == whole && (row[k].last & ((1 << a.log_page) - 1)) != 0;
+          const bool page = source[k] >= 0 && source[k] < a.num_pages;
+          if (entry[k] >= 0 && entry[k] < a.num_pages) atomicSub(&a.refs[entry[k]], 1);
+          if (c < whole && page) atomicAdd(&a.refs[source[k]], 1);
+          missing = partly && page;
+          *at = c < whole && page ? source[k] : -1;
+          if ((c < whole && source[k] >= a.num_pages) || (partly && !page)) report(a.status, SPEC_ERR_CACHE_RANGE);
+        } else {
+          const bool wanted = c < row[k].last && (c < row[k].keep || c >= row[k].from);
+          if (wanted) {
+            missing = entry[k] < 0;
+            if (entry[k] >= a.num_pages) report(a.status, SPEC_ERR_CACHE_RANGE);
+          } else if (entry[k] != -1) {
+            if (entry[k] >= 0 && entry[k] < a.num_pages) atomicSub(&a.refs[entry[k]], 1);
+            *at = -1;
+          }
+        }
+      }
+      const uint32_t bits = __ballot_sync(kFull, missing);
+      if (lane == 0) need[i] = bits;
+    }
+  }
+  __syncthreads();
+  {
+    const uint32_t n = count_before(need, need_before, nw, scratch);
+    if (tid == 0) total[0] = n;
+  }
+  cluster_sync();  // the counts are final
+  if (warp == 0) {
+    const uint32_t n = lane < ctas ? load_of(lane, &total[0]) : 0;
+    uint32_t inc = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(kFull, inc, d);
+      if (lane >= d) inc += o;
+    }
+    if (lane <= kMostCtas) need_at[lane] = inc - n;
+  }
+  __syncthreads();
+  const uint32_t needs = need_at[ctas];
+  if (needs > 0 || a.free_pages) {
+    // ---- 2. the pool
+    for (int i0 = warp; i0 < nf; i0 += kWarps * kBatch) {
+      int32_t count[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int64_t page = static_cast<int64_t>(f0 + i0 + k * kWarps) * 32 + lane;
+        count[k] = i0 + k * kWarps < nf && page < a.num_pages ? __ldcg(a.refs + page) : 1;
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const uint32_t bits = __ballot_sync(kFull, count[k] <= 0);
+        if (lane == 0 && i0 + k * kWarps < nf) avail[i0 + k * kWarps] = bits;
+      }
+    }
+    __syncthreads();
+    {
+      const uint32_t n = count_before(avail, avail_before, nf, scratch);
+      if (tid == 0) total[1] = n;
+    }
+    cluster_sync();
+    if (warp == 0) {
+      const uint32_t n = lane < ctas ? load_of(lane, &total[1]) : 0;
+      uint32_t inc = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(kFull, inc, d);
+        if (lane >= d) inc += o;
+      }
+      if (lane <= kMostCtas) free_at[lane] = inc - n;
+    }
+    __syncthreads();
+    const uint32_t frees = free_at[ctas];
+    if (rank == 0 && tid == 0 && a.free_pages) *a.free_pages = static_cast<int32_t>(frees - min(frees, needs));
+
+    // ---- 3. pages for the missing entries: a word of bits a warp, an entry a lane
+    for (int i0 = warp * 32; i0 < nw; i0 += kThreads) {
+      uint32_t todo = __ballot_sync(kFull, i0 + lane < nw && need[i0 + lane] != 0);
+      while (todo) {
+        const int i = i0 + __ffs(todo) - 1;
+        todo &= todo - 1;
+        const uint32_t bits = need[i];
+        if (!((bits >> lane) & 1)) continue;
+        uint32_t k = need_at[rank] + need_before[i] + __popc(bits & ((1u << lane) - 1));
+        const int b = (w0 + i) / a.row_words, c = (w0 + i - b * a.row_words) * 32 + lane;
+        int32_t* const at = a.table + b * a.table_stride + c;
+        if (k >= frees) {
+          report(a.status, SPEC_ERR_CACHE_FULL);
+          continue;
+        }
+        int r = 0;
+        while (k >= free_at[r + 1]) ++r;
+        k -= free_at[r];
+        // the last word with at most k bits before it
+        int lo = 0, hi = min(a.free_words - r * a.free_share, a.free_share);
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (load_of(r, avail_before + mid) <= k)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        uint32_t word = load_of(r, avail + lo);
+        for (uint32_t skip = k - load_of(r, avail_before + lo); skip; --skip) word &= word - 1;
+        const int page = (r * a.free_share + lo) * 32 + __ffs(word) - 1;
+        *at = page;
+        a.refs[page] = 1;
+      }
+    }
+  }
+  cluster_sync();  // others may still be reading here
+}
+
+// The filled slots and the scales of the last pages of copies.  A warp has the keys or
+// the values of one head of a page: rows of D bytes, 16 a lane.
+struct CopyArgs {
+  PagesArgs a;
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scale;
+  float* v_scale;
+  int64_t page_stride, head_stride, token_stride, scale_page_stride, scale_head_stride;
+  int32_t Hkv, vecs, blocks;  // heads; 16-byte pieces of a row; blocks of a sequence
+};
+
+constexpr int kCopyThreads = 256, kCopyAhead = 4;
+
+__global__ void __launch_bounds__(kCopyThreads) spec_kv_copy_kernel(const __grid_constant__ CopyArgs g) {
+  const PagesArgs& a = g.a;
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.x / g.blocks;
+  const int unit = (blockIdx.x - b * g.blocks) * (kCopyThreads / 32) + (threadIdx.x >> 5);
+  start_dependents();
+  wait_for_grid();
+  int L = 0;
+  const int p = parent_of(a, b, &L);
+  const int filled = L & ((1 << a.log_page) - 1);
+  if (p < 0 || filled == 0 || unit >= 2 * g.Hkv) return;
+  const int c = L >> a.log_page;
+  const int from = a.table[p * a.table_stride + c], to = a.table[b * a.table_stride + c];
+  if (from < 0 || from >= a.num_pages || to < 0 || to >= a.num_pages) return;
+  const bool values = unit & 1;
+  const int h = unit >> 1;
+  uint8_t* const codes = (values ? g.v_codes : g.k_codes) + h * g.head_stride;
+  float* const scale = (values ? g.v_scale : g.k_scale) + h * g.scale_head_stride;
+  if (lane == 0) scale[to * g.scale_page_stride] = scale[from * g.scale_page_stride];
+  const uint8_t* const src = codes + from * g.page_stride;
+  uint8_t* const dst = codes + to * g.page_stride;
+  const int pieces = filled * g.vecs;
+  for (int i0 = lane; i0 < pieces; i0 += 32 * kCopyAhead) {
+    uint4 x[kCopyAhead];
+    int64_t at[kCopyAhead];
+#pragma unroll
+    for (int k = 0; k < kCopyAhead; ++k) {
+      const int i = i0 + 32 * k, tok = i / g.vecs;
+      at[k] = tok * g.token_stride + (i - tok * g.vecs) * 16;
+      if (i < pieces) x[k] = *reinterpret_cast<const uint4*>(src + at[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kCopyAhead; ++k)
+      if (i0 + 32 * k < pieces) *reinterpret_cast<uint4*>(dst + at[k]) = x[k];
+  }
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+spec_status launch(const void* fn, int64_t grid, int threads, int cluster, int smem, void* stream, void** args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) return SPEC_ERR_CUDA;
+  specv_units::count_launches(1);
+  return SPEC_OK;
+}
+
+spec_status check(const spec_kv_pages* p) {
+  if (!p || p->num_pages < 1 || p->B < 0 || p->max_pages < 1) return SPEC_ERR_INVALID_ARG;
+  if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128) return SPEC_ERR_INVALID_ARG;
+  if (!p->refs || !aligned(p->refs, 4)) return SPEC_ERR_INVALID_ARG;
+  if (p->B == 0) return SPEC_OK;
+  if (!p->page_table || !aligned(p->page_table, 4)) return SPEC_ERR_INVALID_ARG;
+  if (p->B > 1 && p->table_stride < p->max_pages) return SPEC_ERR_INVALID_ARG;
+  // positions are counted in 32 bits
+  if (static_cast<int64_t>(p->max_pages) * p->page_size > INT_MAX - 128) return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+// CTAs of the cluster, and the shared memory of each; 0: too large.
+constexpr int kMostSmem = 224 * 1024;
+int plan(PagesArgs& a, int* smem) {
+  a.row_words = (a.max_pages + 31) / 32;
+  const int64_t need = static_cast<int64_t>(a.B) * a.row_words, avail = (static_cast<int64_t>(a.num_pages) + 31) / 32;
+  if (need + avail > static_cast<int64_t>(kMostCtas) * kMostSmem / 8) return 0;
+  a.need_words = static_cast<int32_t>(need);
+  a.free_words = static_cast<int32_t>(avail);
+  int ctas = need + avail <= 256 ? 1 : kMostCtas;
+  for (;; ctas = kMostCtas) {
+    a.need_share = (a.need_words + ctas - 1) / ctas;
+    a.free_share = (a.free_words + ctas - 1) / ctas;
+    *smem = 8 * (a.need_share + a.free_share);
+    if (*smem <= kMostSmem) return ctas;
+    if (ctas == kMostCtas) return 0;
+  }
+}
+
+template <bool FORK>
+spec_status launch_pages(PagesArgs& a, void* stream) {
+  int smem = 0;
+  const int ctas = plan(a, &smem);
+  if (ctas == 0) return SPEC_ERR_UNSUPPORTED;
+  const void* fn = reinterpret_cast<const void*>(&spec_kv_pages_kernel<FORK>);
+  if (smem > 48 * 1024 - 1024) {
+    static std::atomic<bool> allowed[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
+    if (!allowed[dev].load(std::memory_order_acquire)) {
+      if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+      allowed[dev].store(true, std::memory_order_release);
+    }
+  }
+  void* args[] = {&a};
+  return launch(fn, ctas, kThreads, ctas, smem, stream, args);
+}
+
+void fill(const spec_kv_pages* p, PagesArgs& a) {
+  a.refs = p->refs;
+  a.table = p->page_table;
+  a.table_stride = p->table_stride;
+  a.free_pages = p->free_pages;
+  a.status = p->status;
+  a.num_pages = p->num_pages;
+  a.log_page = 0;
+  while ((1 << a.log_page) < p->page_size) ++a.log_page;
+  a.B = p->B;
+  a.max_pages = p->max_pages;
+}
+
+}  // namespace
+
+extern "C" {
+
+spec_status spec_kv_hold(const spec_kv_pages* pages, const int32_t* seq_lens, const int32_t* new_lens, int32_t T,
+                         int32_t window, int32_t sinks) {
+  const spec_status s = check(pages);
+  if (s != SPEC_OK) return s;
+  if (T < 0 || window < 0 || sinks < 0) return SPEC_ERR_INVALID_ARG;
+  if (pages->B > 0 && !seq_lens) return SPEC_ERR_INVALID_ARG;
+  PagesArgs a = {};
+  fill(pages, a);
+  a.seq_lens = const_cast<int32_t*>(seq_lens);  // (not written by this)
+  a.new_lens = new_lens;
+  a.T = T;
+  a.window = window;
+  a.sinks = sinks;
+  return launch_pages<false>(a, pages->stream);
+}
+
+spec_status spec_kv_fork(const spec_kv_pages* pages, const spec_kv_cache* cache, int32_t* seq_lens,
+                         const int32_t* parents) {
+  spec_status s = check(pages);
+  if (s != SPEC_OK) return s;
+  if (!cache || cache->num_pages != pages->num_pages || cache->page_size != pages->page_size) return SPEC_ERR_INVALID_ARG;
+  if (cache->Hkv < 1 || cache->D < 16 || cache->D > 256 || cache->D % 16) return SPEC_ERR_INVALID_ARG;
+  if (!cache->k_codes || !cache->v_codes || !cache->k_scale || !cache->v_scale) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(cache->k_codes, 16) || !aligned(cache->v_codes, 16)) return SPEC_ERR_INVALID_ARG;
+  if (cache->page_stride < 0 || cache->head_stride < 0 || cache->token_stride < 0 || cache->page_stride % 16 ||
+      cache->head_stride % 16 || cache->token_stride % 16 || cache->scale_page_stride < 0 || cache->scale_head_stride < 0)
+    return SPEC_ERR_INVALID_ARG;
+  if (cache->token_stride == 0 || (cache->Hkv > 1 && (cache->head_stride == 0 || cache->scale_head_stride == 0)) ||
+      (cache->num_pages > 1 && (cache->page_stride == 0 || cache->scale_page_stride == 0)))
+    return SPEC_ERR_INVALID_ARG;
+  if (pages->B > 0 && (!seq_lens || !parents)) return SPEC_ERR_INVALID_ARG;
+  CopyArgs g = {};
+  PagesArgs& a = g.a;
+  fill(pages, a);
+  a.seq_lens = seq_lens;
+  a.parents = parents;
+  constexpr int warps = kCopyThreads / 32;
+  g.blocks = (2 * cache->Hkv + warps - 1) / warps;
+  if (static_cast<int64_t>(a.B) * g.blocks > INT_MAX) return SPEC_ERR_UNSUPPORTED;
+  s = launch_pages<true>(a, pages->stream);
+  if (s != SPEC_OK || a.B == 0) return s;
+  g.k_codes = cache->k_codes;
+  g.v_codes = cache->v_codes;
+  g.k_scale = cache->k_scale;
+  g.v_scale = cache->v_scale;
+  g.page_stride = cache->page_stride;
+  g.head_stride = cache->head_stride;
+  g.token_stride = cache->token_stride;
+  g.scale_page_stride = cache->scale_page_stride;
+  g.scale_head_stride = cache->scale_head_stride;
+  g.Hkv = cache->Hkv;
+  g.vecs = cache->D / 16;
+  void* args[] = {&g};
+  return launch(reinterpret_cast<const void*>(&spec_kv_copy_kernel), static_cast<int64_t>(a.B) * g.blocks, kCopyThreads, 1,
+                0, pages->stream, args);
+}
+
+}  // extern "C"

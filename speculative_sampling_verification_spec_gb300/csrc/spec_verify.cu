@@ -543,6 +543,7 @@ const char* spec_status_string(spec_status status) {
     case SPEC_ERR_UNSUPPORTED: return "problem too large for one launch (rows x segments, or shared memory)";
     case SPEC_ERR_SCRATCH_LIMIT: return "request needs more scratch than spec_verify_noalloc's fixed array";
     case SPEC_ERR_CACHE_RANGE: return "a length or a page number outside the paged cache";
+    case SPEC_ERR_CACHE_FULL: return "no free page was left in the paged cache";
   }
   return "unknown status";
 }
