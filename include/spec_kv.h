@@ -113,12 +113,12 @@ typedef struct {
   const float* k_weight;     /* likewise for the keys */
   int64_t q_head_stride;     /* elements from a head's weights to the next one's, >= 0 (0: all heads have the same) */
   int64_t k_head_stride;
-  float eps;                 /* 2^-80 to 2^80 */
+  float eps;                 /* 2^-80 to 2^40 */
 } spec_kv_norms;
 
 /* spec_kv_append with norms (NULL: without): a head x of a query or key of a new token
  * becomes (x r) w before it is rotated, with r = 1 / sqrt(mean of x_i^2 + eps) as the
- * nearest float (once in about a million heads the next one), w its weights, and each
+ * nearest float (once in thousands of heads the next one), w its weights, and each
  * product rounded to float.  A head with an infinity has r = 0, one with a NaN is NaN.
  * Everything else is as for spec_kv_append. */
 spec_status spec_kv_append_norm(const void* q, const void* k, const void* v, const float* cos_sin,

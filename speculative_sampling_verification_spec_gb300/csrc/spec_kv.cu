@@ -22,8 +22,8 @@ constexpr int kMmaCtas = kSMs * 2;
 // What an item costs beside its tiles, in tiles.
 constexpr int kGenOverhead = 1;
 constexpr int kMmaOverhead = 4;
-// eps of the norms lies between this and its reciprocal: squares that get lost below the float range are nothing beside it
-constexpr float kLeastEps = 0x1p-80f;
+// limits of the norms' eps, which is added to squares of values scaled by powers of two
+constexpr float kLeastEps = 0x1p-80f, kMostEps = 0x1p40f;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -296,7 +296,7 @@ spec_status spec_kv_append_norm(const void* q, const void* k, const void* v, con
   if (p->rot_dim < 0 || p->rot_dim % 2 || p->rot_dim > cache->D) return SPEC_ERR_INVALID_ARG;
   if (p->rot_dim > 0 && (!cos_sin || p->rot_len < 1 || !aligned(cos_sin, 16))) return SPEC_ERR_INVALID_ARG;
   if (norms) {
-    if (!(norms->eps >= kLeastEps && norms->eps <= 1 / kLeastEps)) return SPEC_ERR_INVALID_ARG;
+    if (!(norms->eps >= kLeastEps && norms->eps <= kMostEps)) return SPEC_ERR_INVALID_ARG;
     if (norms->q_head_stride < 0 || norms->k_head_stride < 0) return SPEC_ERR_INVALID_ARG;
     if (!aligned(norms->q_weight, 4) || !aligned(norms->k_weight, 4)) return SPEC_ERR_INVALID_ARG;
     if (norms->q_weight && !q) return SPEC_ERR_INVALID_ARG;
@@ -341,6 +341,8 @@ spec_status spec_kv_append_norm(const void* q, const void* k, const void* v, con
     g.k_weight_head = norms->k_head_stride;
     split(static_cast<double>(norms->eps) * cache->D, &g.eps_hi, &g.eps_lo);
     split(std::sqrt(static_cast<double>(cache->D)), &g.root_hi, &g.root_lo);
+    // D eps, scaled like the squares, stays below 2^60
+    g.least_exp = 127 - (60 - (std::ilogb(static_cast<double>(norms->eps) * cache->D) + 1)) / 2;
   }
   // eight pairs a thread where every chunk starts on a 16-byte boundary
   const bool vec = p->rot_dim % 16 == 0 && aligned(g.q_weight, 16) && aligned(g.k_weight, 16) &&
@@ -350,6 +352,7 @@ spec_status spec_kv_append_norm(const void* q, const void* k, const void* v, con
   int per_tok = cache->D / (vec ? 16 : 2);
   if (norm && vec) per_tok = per_tok > 8 ? 16 : per_tok > 4 ? 8 : per_tok > 2 ? 4 : per_tok;
   g.tok_threads = per_tok;
+  g.one = 1.0f;
   g.units_page = (p->T - 1 + S - 1) / S + 1;
   // a unit fits a warp's registers or takes a CTA
   const bool warp = per_tok <= 32 && std::min(p->T, S) <= 32 / per_tok * kAppendWarpIter;

@@ -23,8 +23,8 @@
 //
 // Norms.  r = 1 / sqrt(mean x^2 + eps) of a head goes to the keys' scales and codes
 // through comparisons and roundings, so it is made a function of the inputs alone: the
-// sum of the squares and its root are carried in two floats (some 45 bits), and r is the
-// nearest float but for one row in a million.  (In 64 bits the sums of a prompt alone
+// sum of the squares and its root are carried in two floats (some 37 bits), and r is the
+// nearest float but for one head in thousands.  (In 64 bits the sums of a prompt alone
 // would take longer than the rest: the chip's rate of such multiply-adds is a hundredth
 // of that in 32.)  The threads of a head are a power of two of neighbouring lanes, the
 // last of them idle where its chunks are not, and add up by exchanging; with PC = 1 a
@@ -47,12 +47,14 @@ struct AppendArgs {
   int32_t unit_blocks;   // blocks that take groups; the rest take queries
   int32_t q_rows_block;  // (sequence, token) rows a query block takes
   int32_t q_heads;       // heads a query thread takes: 1 or kAppendHeads
+  float one;             // 1
   int32_t tok_threads;   // threads of a token's head: its chunks, or the power of two above
   // norms: weights (NULL: not normalised), and D * eps and sqrt(D) as sums of two floats
   const float* q_weight;
   const float* k_weight;
   int64_t q_weight_head, k_weight_head;
   float eps_hi, eps_lo, root_hi, root_lo;
+  int32_t least_exp;  // of what sums of squares are scaled by: below, the squares are nothing beside eps
 };
 
 // N consecutive elements as they are in memory: 8 of them in 16-byte words, or one
@@ -65,6 +67,20 @@ struct Raw {
     } else {
 #pragma unroll
       for (int i = 0; i < static_cast<int>(sizeof(E) * N / 16); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+  }
+  // the largest magnitude, NaN aside
+  __device__ __forceinline__ float top() const {
+    if constexpr (N > 1 && sizeof(E) == 2) {
+      const auto two = [](uint32_t u) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u)); };
+      const __nv_bfloat162 m = __hmax2(__hmax2(two(w[0].x), two(w[0].y)), __hmax2(two(w[0].z), two(w[0].w)));
+      return fmaxf(__low2float(m), __high2float(m));
+    } else {
+      float x[N], m = 0.0f;
+      values(x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(x[i]));
+      return m;
     }
   }
   __device__ __forceinline__ void values(float* x) const {
@@ -153,6 +169,9 @@ struct RawChunk {
     lo.load(row + k.lo);
     hi.load(row + k.hi);
   }
+  __device__ __forceinline__ float top() const {
+    return fmaxf(lo.top(), hi.top());
+  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (uint4& u : lo.w) u = make_uint4(0, 0, 0, 0);
@@ -180,8 +199,20 @@ struct Angles {
 #pragma unroll
       for (int i = 0; i < PC; ++i) turn(y[2 * i], y[2 * i + 1], co[i], si[i]);
     } else {
+      if constexpr (PC == 1) {
+        turn(y[0], y[1], co[0], si[0]);
+      } else {
+        // Two pairs at a time, rounded alike.  The sums are written as multiplications by a 1 that the assembler
+        // does not know: a plain packed addition of a packed product it makes one operation, with one rounding.
+        const u64 plus = pack2(g.one, g.one), minus = pack2(-g.one, -g.one);
 #pragma unroll
-      for (int i = 0; i < PC; ++i) turn(y[i], y[PC + i], co[i], si[i]);
+        for (int i = 0; i < PC; i += 2) {
+          const u64 a = pack2(y[i], y[i + 1]), b = pack2(y[PC + i], y[PC + i + 1]);
+          const u64 c = pack2(co[i], co[i + 1]), d = pack2(si[i], si[i + 1]);
+          unpack2(fma2(mul2(b, d), minus, mul2(a, c)), y[i], y[i + 1]);
+          unpack2(fma2(mul2(a, d), plus, mul2(b, c)), y[PC + i], y[PC + i + 1]);
+        }
+      }
     }
   }
 };
@@ -193,86 +224,123 @@ __device__ __forceinline__ void turn_chunk(const AppendArgs& g, const float* cs,
 
 __device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
-// A sum of squares in two floats: s, and what roundings have taken from it.
-struct Sum2 {
-  float s, e;
-  // (the error of a rounded sum, exactly)
-  static __device__ __forceinline__ float lost(float a, float b, float sum) {
-    const float bb = __fsub_rn(sum, a);
-    return __fadd_rn(__fsub_rn(a, __fsub_rn(sum, bb)), __fsub_rn(b, bb));
-  }
-  __device__ __forceinline__ void add(const Sum2& o) {
-    const float t = __fadd_rn(s, o.s);
-    e = __fadd_rn(__fadd_rn(e, o.e), lost(s, o.s, t));
-    s = t;
-  }
+// The sum of the squares of a head's channels, times the square of a power of two f that brings the largest to [1, 4):
+// hi + lo.  The sum is run on top of kBias, which no square and no sum reaches: every addition leaves a multiple of the
+// bias's last place in the sum, exactly, and the rest of the square, exactly, for a second sum (of at most 2^-12 each,
+// so that its own roundings are some 2^-37 of the whole).
+constexpr float kBias = 4096.0f;
+struct Squares {
+  float hi, lo, f;
 };
 
-// Of N values times `factor` (a power of two); two at a time, and their two sums at the end.
-template <typename E, int N>
-__device__ __forceinline__ Sum2 squares(const float* x, float factor) {
-  const u64 f = pack2(factor, factor), minus = pack2(-1.0f, -1.0f);
-  u64 s = pack2(0.0f, 0.0f), e = s;
+// Of R heads whose channels lie with `threads` neighbouring lanes (a power of two), N each: values(r, y) gives the
+// lane's, top(r) the largest magnitude among them (NaN aside, which comes up in the sum).  Step by step for all heads,
+// whose chains run side by side.
+template <int N, int R, typename Values, typename Top>
+__device__ __forceinline__ void squares(const AppendArgs& g, const Values& values, const Top& top, unsigned mask,
+                                        int threads, Squares* a) {
+  float m[R];
 #pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const u64 y = mul2(pack2(x[i], x[i + 1]), f), p = mul2(y, y);
-    const u64 t = add2(s, p), b = fma2(s, minus, t);                   // b = t - s
-    u64 lost = add2(fma2(fma2(b, minus, t), minus, s), fma2(b, minus, p));  // (s - (t - b)) + (p - b)
-    if constexpr (sizeof(E) == 4) lost = add2(lost, fma2(y, y, mul2(p, minus)));  // (16-bit values' squares are exact)
-    e = add2(e, lost);
-    s = t;
+  for (int r = 0; r < R; ++r) m[r] = top(r);
+  for (int d = threads >> 1; d; d >>= 1) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) m[r] = fmaxf(m[r], __shfl_xor_sync(mask, m[r], d));
   }
-  Sum2 a, b;
-  unpack2(s, a.s, b.s);
-  unpack2(e, a.e, b.e);
-  a.add(b);
-  return a;
+  const u64 minus = pack2(-1.0f, -1.0f), bias = pack2(kBias, kBias);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int e = min(max(static_cast<int>(__float_as_uint(m[r]) >> 23), g.least_exp), 253);
+    a[r].f = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+    const u64 f = pack2(a[r].f, a[r].f);
+    u64 sum = bias, rest = pack2(0.0f, 0.0f);
+    float x[N];
+    values(r, x);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const u64 y = mul2(pack2(x[i], x[i + 1]), f), next = fma2(y, y, sum);
+      const u64 taken = fma2(next, minus, sum);  // less what the sum has grown by
+      rest = add2(rest, fma2(y, y, taken));
+      sum = next;
+    }
+    sum = fma2(bias, minus, sum);
+    float b1, c1;
+    unpack2(sum, a[r].hi, b1);
+    unpack2(rest, a[r].lo, c1);
+    a[r].hi += b1;
+    a[r].lo += c1;
+  }
+  for (int d = threads >> 1; d; d >>= 1) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      a[r].hi += __shfl_xor_sync(mask, a[r].hi, d);
+      a[r].lo += __shfl_xor_sync(mask, a[r].lo, d);
+    }
+  }
 }
 
 // sqrt(D) / sqrt(sum + D eps), to the nearest float: an approximate root and one step of Newton's in two floats.
-__device__ __forceinline__ float norm_of(const AppendArgs& g, const Sum2& a, float eps_hi, float eps_lo) {
-  const float u = __fadd_rn(a.s, eps_hi);
-  const float ul = __fadd_rn(__fadd_rn(Sum2::lost(a.s, eps_hi, u), a.e), eps_lo);
-  const float r = rsqrtf(u);
+__device__ __forceinline__ float norm_of(const AppendArgs& g, const Squares& a) {
+  const float eps = g.eps_hi * a.f * a.f, u = __fadd_rn(a.hi, eps);
+  const float b = __fsub_rn(u, a.hi);  // u's own rounding: (hi - (u - b)) + (eps - b)
+  const float lost = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(u, b)), __fsub_rn(eps, b));
+  const float ul = __fadd_rn(__fadd_rn(lost, a.lo), g.eps_lo * a.f * a.f);
+  const float r = rsqrtf(__fadd_rn(u, ul));
   const float q = __fmul_rn(r, r), ql = fmaf(r, r, -q);
   const float p = __fmul_rn(u, q), pl = fmaf(ul, q, fmaf(u, ql, fmaf(u, q, -p)));
   const float step = __fmul_rn(__fmul_rn(0.5f, r), __fsub_rn(__fsub_rn(1.0f, p), pl));
   const float m = __fmul_rn(r, g.root_hi);
-  return __fadd_rn(m, fmaf(step, g.root_hi, fmaf(r, g.root_lo, fmaf(r, g.root_hi, -m))));
+  const float n = __fadd_rn(m, fmaf(step, g.root_hi, fmaf(r, g.root_lo, fmaf(r, g.root_hi, -m))));
+  // infinities: 0; NaN
+  return a.hi < INFINITY ? n * a.f : a.hi > 0.0f ? 0.0f : a.hi;
 }
 
-// The norm factor of a head whose channels lie with `threads` neighbouring lanes (a power of two), N each.
-// Squares that come near the end of the float range are taken of the values times 2^-84.
-template <typename E, int N>
-__device__ __forceinline__ float head_norm(const AppendArgs& g, const float* x, int threads) {
+// The lanes that share a head.
+__device__ __forceinline__ unsigned lanes_of(int threads) {
   const unsigned lane = threadIdx.x & 31;
-  const unsigned mask = threads == 32 ? kFull : ((1u << threads) - 1) << (lane & ~(threads - 1u));
-  const auto over_lanes = [&](Sum2 a) {
-    for (int d = threads >> 1; d; d >>= 1) {
-      Sum2 o;
-      o.s = __shfl_xor_sync(mask, a.s, d);
-      o.e = __shfl_xor_sync(mask, a.e, d);
-      a.add(o);
-    }
-    return a;
-  };
-  Sum2 a = over_lanes(squares<E, N>(x, 1.0f));
-  if (a.s < 0x1p80f) return norm_of(g, a, g.eps_hi, g.eps_lo);
-  a = over_lanes(squares<E, N>(x, 0x1p-84f));
-  if (!is_finite(a.s)) return a.s > 0.0f ? 0.0f : a.s;  // infinities: 0; NaN
-  return norm_of(g, a, g.eps_hi * 0x1p-84f * 0x1p-84f, g.eps_lo * 0x1p-84f * 0x1p-84f) * 0x1p-84f;
+  return threads == 32 ? kFull : ((1u << threads) - 1) << (lane & ~(threads - 1u));
 }
 
-// Normalised values: (x r) w, each product rounded.
-template <int PC>
-__device__ __forceinline__ void scale_chunk(float* y, float r, const float* weight, const ChunkAt& k) {
-  float w[2 * PC];
-  load_n<float, PC>(weight + k.lo, w);
-  load_n<float, PC>(weight + k.hi, w + PC);
+// The norm factors of R heads at once, whose chunks are raw[0] .. raw[R - 1]: with as many lanes to a head, each takes
+// one of the roots.
+template <int R, typename E, int PC>
+__device__ __forceinline__ void norms_of(const AppendArgs& g, const RawChunk<E, PC>* raw, float* r, int threads) {
+  const unsigned mask = lanes_of(threads);
+  Squares a[R];
+  squares<2 * PC, R>(
+      g, [&](int k, float* y) { raw[k].values(y); }, [&](int k) { return raw[k].top(); }, mask, threads, a);
+  if (R == 4 && threads >= 4) {
+    const int mine = threadIdx.x & 3;
+    Squares b = a[0];
 #pragma unroll
-  for (int i = 0; i < 2 * PC; ++i) y[i] = __fmul_rn(__fmul_rn(y[i], r), w[i]);
+    for (int k = 1; k < R; ++k) {
+      b.hi = mine == k ? a[k].hi : b.hi;
+      b.lo = mine == k ? a[k].lo : b.lo;
+      b.f = mine == k ? a[k].f : b.f;
+    }
+    const float n = norm_of(g, b);
+#pragma unroll
+    for (int k = 0; k < R; ++k) r[k] = __shfl_sync(mask, n, ((threadIdx.x & 31) & ~3u) + k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < R; ++k) r[k] = norm_of(g, a[k]);
+  }
 }
 
+// The weights of a chunk, and its normalised values: (x r) w, each product rounded.
+template <int PC>
+struct Weights {
+  float w[2 * PC];
+  __device__ __forceinline__ void load(const float* weight, const ChunkAt& k) {
+    load_n<float, PC>(weight + k.lo, w);
+    load_n<float, PC>(weight + k.hi, w + PC);
+  }
+  __device__ __forceinline__ void scale(float* y, float r) const {
+    const u64 r2 = pack2(r, r);
+#pragma unroll
+    for (int i = 0; i < 2 * PC; i += 2)
+      unpack2(mul2(mul2(pack2(y[i], y[i + 1]), r2), pack2(w[i], w[i + 1])), y[i], y[i + 1]);
+  }
+};
 
 // 2^e, e the least integer >= kMinScaleExp with amax <= 448 * 2^e (448 = 1.75 * 2^8,
 // the largest e4m3 value): from the exponent and mantissa fields, with no rounding
@@ -332,7 +400,16 @@ __device__ __forceinline__ float row_norm(const AppendArgs& g, const E* x) {
     const int d = (threadIdx.x & 31) + 32 * i;
     y[i] = d < g.a.D ? to_float(x[d]) : 0.0f;
   }
-  return head_norm<E, 8>(g, y, 32);
+  Squares a;
+  squares<8, 1>(
+      g, [&](int, float* z) { for (int i = 0; i < 8; ++i) z[i] = y[i]; },
+      [&](int) {
+        float m = 0.0f;
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
+        return m;
+      },
+      kFull, 32, &a);
+  return norm_of(g, a);
 }
 
 // lengths of sequence b against this call's limits
@@ -402,7 +479,7 @@ __device__ __forceinline__ void append_group(const AppendArgs& g, int group, int
       if (weight) {
         const E* const x0 = x - tok0 * x_tok;
         for (int i = WARP ? 0 : t >> 5; i < tokens; i += WARP ? 1 : nt / 32) {
-          const float r = row_norm<E>(g, x0 + i * x_tok);
+          const float r = row_norm(g, x0 + i * x_tok);
           if ((t & 31) == 0) norms[i] = r;
         }
       }
@@ -411,30 +488,25 @@ __device__ __forceinline__ void append_group(const AppendArgs& g, int group, int
       else
         __syncthreads();
     }
+    Weights<PC> weights;
+    if (weight) weights.load(weight, at);
     RawChunk<E, PC> raw[ITER];
     float norm[ITER];
     const auto read = [&](int i0) {
 #pragma unroll
       for (int it = 0; it < ITER; ++it)
-        if (i0 + it < mine) {
-          if (has)
-            raw[it].load(x + (i0 + it) * x_step, at);
-          else
-            raw[it].clear();
-        }
+        if (i0 + it < mine && has)
+          raw[it].load(x + (i0 + it) * x_step, at);
+        else if (NORM)
+          raw[it].clear();
       if constexpr (NORM) {
         if (weight) {
+          if constexpr (PC == 1) {
 #pragma unroll
-          for (int it = 0; it < ITER; ++it) {
-            if (i0 + it < mine) {
-              if constexpr (PC == 1) {
-                norm[it] = norms[tok0 + (i0 + it) * step];
-              } else {
-                float y[2 * PC];
-                raw[it].values(y);
-                norm[it] = head_norm<E, 2 * PC>(g, y, per_tok);
-              }
-            }
+            for (int it = 0; it < ITER; ++it)
+              if (i0 + it < mine) norm[it] = norms[tok0 + (i0 + it) * step];
+          } else {
+            norms_of<ITER>(g, raw, norm, per_tok);  // (of tokens that are not there, too: they are zero)
           }
         }
       }
@@ -442,7 +514,7 @@ __device__ __forceinline__ void append_group(const AppendArgs& g, int group, int
     const auto values = [&](int i0, int it, float* y) {
       raw[it].values(y);
       if constexpr (NORM)
-        if (weight) scale_chunk<PC>(y, norm[it], weight, at);
+        if (weight) weights.scale(y, norm[it]);
       if (turned) turn_chunk<PC>(g, cs + static_cast<int64_t>(i0 + it) * cs_step, at, y);
     };
     const auto largest = [&](uint32_t v) {
@@ -571,12 +643,14 @@ __device__ __forceinline__ void norm_queries(const AppendArgs& g, int row0, int 
       for (int d = lane; d < a.D; d += 32) from_float(fill, o + d);
       continue;
     }
-    const float r = row_norm<E>(g, q);  // (every lane's channels are read before any is written)
+    const float r = row_norm(g, q);  // (every lane's channels are read before any is written)
     const float* cs = g.cos_sin + (g.rot > 0 ? static_cast<int64_t>(L + tok) * g.rot : 0);
     for (int p = lane; p < a.D / 2; p += 32) {
       const ChunkAt k = chunk_at<1>(g, p);
       float y[2] = {to_float(q[k.lo]), to_float(q[k.hi])};
-      scale_chunk<1>(y, r, g.q_weight + h * g.q_weight_head, k);
+      Weights<1> w;
+      w.load(g.q_weight + h * g.q_weight_head, k);
+      w.scale(y, r);
       turn_chunk<1>(g, cs, k, y);
       from_float(y[0], o + k.lo);
       from_float(y[1], o + k.hi);
@@ -585,7 +659,7 @@ __device__ __forceinline__ void norm_queries(const AppendArgs& g, int row0, int 
 }
 
 template <typename E, int PC, bool WARP, bool NORM>
-__global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads, WARP ? 1 : kAppendCtas)
+__global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads, WARP ? 1 : NORM ? 2 : kAppendCtas)
     spec_kv_append_kernel(const __grid_constant__ AppendArgs g) {
   constexpr int nt = WARP ? kAppendWarpThreads : kAppendCtaThreads;
   const KvArgs& a = g.a;
@@ -648,8 +722,15 @@ __global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads,
           else
             raw.clear();
           raw.values(y);
-          if constexpr (NORM && PC > 1)
-            if (weight) scale_chunk<PC>(y, head_norm<E, 2 * PC>(g, y, per_tok), weight, k);
+          if constexpr (NORM && PC > 1) {
+            if (weight) {
+              float norm;
+              norms_of<1>(g, &raw, &norm, per_tok);
+              Weights<PC> w;
+              w.load(weight, k);
+              w.scale(y, norm);
+            }
+          }
           turn_chunk<PC>(g, cs, k, y);
           if (!has) continue;
           store_n<E, PC>(o + k.lo, y);
@@ -665,13 +746,30 @@ __global__ void __launch_bounds__(WARP ? kAppendWarpThreads : kAppendCtaThreads,
             else
               raw[e].clear();
           }
+          if (NORM && i + 1 < full) {
+#pragma unroll
+            for (int e = 0; e < kAppendHeads; ++e) {
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(q + q_step + e * q_heads + k.lo));
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(q + q_step + e * q_heads + k.hi));
+            }
+          }
           const Angles<PC> at(g, cs, k);
+          float norm[kAppendHeads];
+          if constexpr (NORM && PC > 1) {
+            if (weight) norms_of<kAppendHeads>(g, raw, norm, per_tok);
+          }
+          Weights<PC> w;
+          if (weight) w.load(weight, k);
 #pragma unroll
           for (int e = 0; e < kAppendHeads; ++e) {
             float y[2 * PC];
             raw[e].values(y);
-            if constexpr (NORM && PC > 1)
-              if (weight) scale_chunk<PC>(y, head_norm<E, 2 * PC>(g, y, per_tok), weight + e * w_heads, k);
+            if constexpr (NORM && PC > 1) {
+              if (weight) {
+                if (e > 0 && w_heads) w.load(weight + e * w_heads, k);
+                w.scale(y, norm[e]);
+              }
+            }
             at.turn_all(g, k, y);
             if (!has) continue;
             store_n<E, PC>(o + e * o_heads + k.lo, y);

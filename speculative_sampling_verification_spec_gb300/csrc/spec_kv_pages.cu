@@ -30,8 +30,9 @@ namespace {
 using namespace spec_kv_detail;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kMostCtas = 8;  // of a cluster
-constexpr int kBatch = 4;     // words of a warp under way at once
+constexpr int kMostCtas = 16, kPortableCtas = 8;  // of a cluster
+constexpr int kWordsAlone = 256;  // of bits, that one CTA takes on alone
+constexpr int kAhead = 4;      // loads of counts of a lane under way at once
 
 struct PagesArgs {
   int32_t* refs;
@@ -44,9 +45,11 @@ struct PagesArgs {
   int32_t T, window, sinks;
   int32_t* seq_lens;  // written by forks
   const int32_t* parents;
-  int32_t row_words;                // words of bits of a row of the table
+  int32_t vec, refs_vec;            // the table, the counts can be read four at a time
+  int32_t row_words;                // words of bits of a row of the table (a whole number of stretches)
   int32_t need_words, free_words;   // of all rows; of the pool
   int32_t need_share, free_share;   // of a CTA
+  uint64_t row_recip;               // 2^64 over the stretches of a row
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -74,22 +77,55 @@ __device__ __forceinline__ uint32_t load_of(uint32_t rank, const uint32_t* here)
   return v;
 }
 
+// Four neighbouring entries of a row, or counts of pages.
+struct Four {
+  int32_t x[4];
+  __device__ __forceinline__ void load(const int32_t* row, int c, int columns, bool vec) {
+    if (vec && c + 4 <= columns) {
+      *reinterpret_cast<int4*>(x) = *reinterpret_cast<const int4*>(row + c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = c + e < columns ? row[c + e] : -1;
+    }
+  }
+  __device__ __forceinline__ void store(int32_t* row, const Four& old, int c, int columns) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (x[e] != old.x[e] && c + e < columns) row[c + e] = x[e];
+  }
+  // (atomics have been at the counts: not from the first-level cache)
+  __device__ __forceinline__ void load_counts(const PagesArgs& a, int page) {
+    if (a.refs_vec && page + 4 <= a.num_pages) {
+      *reinterpret_cast<int4*>(x) = __ldcg(reinterpret_cast<const int4*>(a.refs + page));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = page + e < a.num_pages ? __ldcg(a.refs + page + e) : 1;
+    }
+  }
+};
+
+// The bits of eight neighbouring lanes, four each, side by side.
+__device__ __forceinline__ uint32_t word_of(uint32_t bits) {
+  uint32_t w = bits << (4 * (threadIdx.x & 7));
+  w |= __shfl_xor_sync(kFull, w, 1);
+  w |= __shfl_xor_sync(kFull, w, 2);
+  w |= __shfl_xor_sync(kFull, w, 4);
+  return w;
+}
+
 // What a row of the table becomes.
 struct Row {
-  bool leave;        // nothing happens to it
-  int last;          // columns from this on are empty
-  int keep, from;    // hold: columns below `keep` and from `from` on are needed
-  int parent;        // fork
+  int last;        // hold: columns from this on are empty; fork: the parent's tokens.  -1: nothing happens to it
+  int keep, from;  // hold: columns below `keep` and from `from` on are needed
+  __device__ __forceinline__ bool needs(int c) const { return c < last && (c < keep || c >= from); }
 };
 
 __device__ __forceinline__ Row hold_row(const PagesArgs& a, int b) {
   Row r;
   const int L = a.seq_lens[b], n = a.new_lens ? a.new_lens[b] : a.T;
   const int64_t end = static_cast<int64_t>(L) + n;
-  r.leave = L < 0 || n < 0 || end > (static_cast<int64_t>(a.max_pages) << a.log_page);
-  r.parent = -1;
-  const int S1 = (1 << a.log_page) - 1;
-  r.last = r.leave ? 0 : static_cast<int>((end + S1) >> a.log_page);
+  const bool out = L < 0 || n < 0 || end > (static_cast<int64_t>(a.max_pages) << a.log_page);
+  r.last = out ? -1 : static_cast<int>((end + (1 << a.log_page) - 1) >> a.log_page);
   r.keep = a.sinks > 0 ? ((a.sinks - 1) >> a.log_page) + 1 : 0;
   r.from = a.window > 0 && L >= a.window ? (L + 1 - a.window) >> a.log_page : 0;
   return r;
@@ -105,6 +141,59 @@ __device__ __forceinline__ int parent_of(const PagesArgs& a, int b, int* L) {
   if ((pp != -1 && pp != p) || *L < 0 || *L > (static_cast<int64_t>(a.max_pages) << a.log_page)) return -2;
   return p;
 }
+
+// A warp's columns of a row: four a lane, N times.  Tables of up to 128 columns take N = 1, others 4, because a
+// stretch costs about as many instructions however long it is.
+template <bool FORK, int N>
+struct Stretch {
+  static constexpr int kWords = 4 * N;  // of bits
+  int b, c;  // row; the lane's first column
+  Row row;
+  Four entry[N], source[FORK ? N : 1];  // source: of the parent's row
+  __device__ __forceinline__ int column(int k) const { return c + k * 128; }
+  __device__ __forceinline__ void load(const PagesArgs& a, int i) {
+    const int of_row = a.row_words / kWords;
+    b = of_row == 1 ? i : static_cast<int>(__umul64hi(i, a.row_recip));
+    c = (i - b * of_row) * N * 128 + (threadIdx.x & 31) * 4;
+    const int32_t* const at = a.table + b * a.table_stride;
+    if constexpr (FORK) {
+      int L = 0;
+      const int p = parent_of(a, b, &L);
+      row.last = p < 0 ? -1 : L;
+      if (p == -2 && c == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+      if (p < 0) return;
+#pragma unroll
+      for (int k = 0; k < N; ++k) source[k].load(a.table + p * a.table_stride, column(k), a.max_pages, a.vec);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) entry[k].load(at, column(k), a.max_pages, a.vec);
+    if constexpr (!FORK) {
+      row = hold_row(a, b);
+      if (row.last < 0 && c == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+    }
+  }
+  // Whether there is anything to do.  Most stretches of a long table are all needed and there, or neither.
+  __device__ __forceinline__ bool some(const PagesArgs& a) const {
+    if (row.last < 0) return false;
+    if constexpr (FORK) return true;
+    const int c0 = c - (threadIdx.x & 31) * 4, c1 = c0 + 128 * N;
+    if (c0 >= row.last || (c0 >= row.keep && c1 <= row.from)) {  // none is needed
+      int all = -1;
+#pragma unroll
+      for (int k = 0; k < N; ++k) all &= entry[k].x[0] & entry[k].x[1] & entry[k].x[2] & entry[k].x[3];
+      return __any_sync(kFull, all != -1);
+    }
+    if (c1 <= row.last && (c0 >= row.from || c1 <= row.keep)) {  // all are
+      uint32_t most = 0;
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = max(most, static_cast<uint32_t>(entry[k].x[e]));
+      return __any_sync(kFull, most >= static_cast<uint32_t>(a.num_pages));
+    }
+    return true;
+  }
+};
 
 // Exclusive counts of the bits of `words` words, and their total: by all threads.
 __device__ uint32_t count_before(const uint32_t* bits, uint32_t* before, int words, uint32_t* scratch) {
@@ -136,7 +225,7 @@ __device__ uint32_t count_before(const uint32_t* bits, uint32_t* before, int wor
 }
 
 // Bound by latency and by what the cluster's few SMs can ask for at once.
-template <bool FORK>
+template <bool FORK, int N>
 __global__ void __launch_bounds__(kThreads, 1) spec_kv_pages_kernel(const __grid_constant__ PagesArgs a) {
   extern __shared__ uint32_t dyn[];
   __shared__ uint32_t scratch[kWarps], total[2];            // this CTA's missing entries and free pages
@@ -152,63 +241,57 @@ __global__ void __launch_bounds__(kThreads, 1) spec_kv_pages_kernel(const __grid
   start_dependents();
   wait_for_grid();
 
-  // ---- 1. the table
-  for (int i0 = warp; i0 < nw; i0 += kWarps * kBatch) {
-    int32_t entry[kBatch], source[kBatch];
-    Row row[kBatch];
+  // ---- 1. the table: a stretch a warp, the next one under way
+  // (of forks, whose stretches have two rows, one at a time)
+  Stretch<FORK, N> now, next;
+  constexpr int kStretchWords = Stretch<FORK, N>::kWords;
+  if (!FORK && warp < nw / kStretchWords) now.load(a, w0 / kStretchWords + warp);
+  for (int i = warp; i < nw / kStretchWords; i += kWarps) {
+    if (FORK)
+      now.load(a, w0 / kStretchWords + i);
+    else if (i + kWarps < nw / kStretchWords)
+      next.load(a, w0 / kStretchWords + i + kWarps);
+    if (!now.some(a)) {
+      if (lane < kStretchWords) need[i * kStretchWords + lane] = 0;
+    } else {
+      bool bad = false;
+      uint32_t missing[N] = {};
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * kWarps;
-      entry[k] = source[k] = -1;
-      row[k].leave = true;
-      if (i >= nw) continue;
-      const int b = (w0 + i) / a.row_words, c = (w0 + i - b * a.row_words) * 32 + lane;
-      if constexpr (FORK) {
-        int L = 0;
-        const int p = parent_of(a, b, &L);
-        row[k].leave = p < 0;
-        row[k].parent = p;
-        row[k].last = L;
-        if (p == -2 && c == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
-        if (p >= 0 && c == 0) a.seq_lens[b] = L;
-        if (p >= 0 && c < a.max_pages) source[k] = a.table[p * a.table_stride + c];
-      } else {
-        row[k] = hold_row(a, b);
-        if (row[k].leave && c == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
-      }
-      if (!row[k].leave && c < a.max_pages) entry[k] = a.table[b * a.table_stride + c];
-    }
+      for (int k = 0; k < N; ++k) {
+        Four to = now.entry[k];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * kWarps;
-      if (i >= nw) continue;
-      const int b = (w0 + i) / a.row_words, c = (w0 + i - b * a.row_words) * 32 + lane;
-      int32_t* const at = a.table + b * a.table_stride + c;
-      bool missing = false;
-      if (!row[k].leave && c < a.max_pages) {
-        if constexpr (FORK) {
-          const int whole = row[k].last >> a.log_page;
-          const bool partly = c == whole && (row[k].last & ((1 << a.log_page) - 1)) != 0;
-          const bool page = source[k] >= 0 && source[k] < a.num_pages;
-          if (entry[k] >= 0 && entry[k] < a.num_pages) atomicSub(&a.refs[entry[k]], 1);
-          if (c < whole && page) atomicAdd(&a.refs[source[k]], 1);
-          missing = partly && page;
-          *at = c < whole && page ? source[k] : -1;
-          if ((c < whole && source[k] >= a.num_pages) || (partly && !page)) report(a.status, SPEC_ERR_CACHE_RANGE);
-        } else {
-          const bool wanted = c < row[k].last && (c < row[k].keep || c >= row[k].from);
-          if (wanted) {
-            missing = entry[k] < 0;
-            if (entry[k] >= a.num_pages) report(a.status, SPEC_ERR_CACHE_RANGE);
-          } else if (entry[k] != -1) {
-            if (entry[k] >= 0 && entry[k] < a.num_pages) atomicSub(&a.refs[entry[k]], 1);
-            *at = -1;
+        for (int e = 0; e < 4; ++e) {
+          const int c = now.column(k) + e;
+          const int32_t old = now.entry[k].x[e];
+          if constexpr (FORK) {
+            const int whole = now.row.last >> a.log_page;
+            const bool partly = c == whole && (now.row.last & ((1 << a.log_page) - 1)) != 0;
+            const int32_t src = now.source[k].x[e];
+            const bool page = src >= 0 && src < a.num_pages;
+            if (old >= 0 && old < a.num_pages) atomicSub(&a.refs[old], 1);
+            if (c < whole && page) atomicAdd(&a.refs[src], 1);
+            if (partly && page) missing[k] |= 1u << e;
+            to.x[e] = c < whole && page ? src : -1;
+            bad |= (c < whole && src >= a.num_pages) || (partly && !page);
+          } else if (now.row.needs(c)) {
+            if (old < 0) missing[k] |= 1u << e;
+            bad |= old >= a.num_pages;
+          } else if (old != -1) {
+            if (old >= 0 && old < a.num_pages) atomicSub(&a.refs[old], 1);
+            to.x[e] = -1;
           }
         }
+        to.store(a.table + now.b * a.table_stride, now.entry[k], now.column(k), a.max_pages);
       }
-      const uint32_t bits = __ballot_sync(kFull, missing);
-      if (lane == 0) need[i] = bits;
+      if (bad) report(a.status, SPEC_ERR_CACHE_RANGE);
+      if (FORK && now.column(0) == 0) a.seq_lens[now.b] = now.row.last;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const uint32_t word = word_of(missing[k]);
+        if ((lane & 7) == 0) need[i * kStretchWords + k * 4 + lane / 8] = word;
+      }
     }
+    if (!FORK) now = next;
   }
   __syncthreads();
   {
@@ -229,18 +312,21 @@ __global__ void __launch_bounds__(kThreads, 1) spec_kv_pages_kernel(const __grid
   __syncthreads();
   const uint32_t needs = need_at[ctas];
   if (needs > 0 || a.free_pages) {
-    // ---- 2. the pool
-    for (int i0 = warp; i0 < nf; i0 += kWarps * kBatch) {
-      int32_t count[kBatch];
+    // ---- 2. the pool: 128 pages a warp
+    for (int i0 = warp; i0 < nf / 4; i0 += kWarps * kAhead) {
+      Four count[kAhead];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int64_t page = static_cast<int64_t>(f0 + i0 + k * kWarps) * 32 + lane;
-        count[k] = i0 + k * kWarps < nf && page < a.num_pages ? __ldcg(a.refs + page) : 1;
-      }
+      for (int k = 0; k < kAhead; ++k)
+        if (i0 + k * kWarps < nf / 4) count[k].load_counts(a, (f0 / 4 + i0 + k * kWarps) * 128 + lane * 4);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const uint32_t bits = __ballot_sync(kFull, count[k] <= 0);
-        if (lane == 0 && i0 + k * kWarps < nf) avail[i0 + k * kWarps] = bits;
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * kWarps;
+        if (i >= nf / 4) continue;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bits |= count[k].x[e] <= 0 ? 1u << e : 0u;
+        const uint32_t word = word_of(bits);
+        if ((lane & 7) == 0) avail[i * 4 + lane / 8] = word;
       }
     }
     __syncthreads();
@@ -263,11 +349,12 @@ __global__ void __launch_bounds__(kThreads, 1) spec_kv_pages_kernel(const __grid
     const uint32_t frees = free_at[ctas];
     if (rank == 0 && tid == 0 && a.free_pages) *a.free_pages = static_cast<int32_t>(frees - min(frees, needs));
 
-    // ---- 3. pages for the missing entries: a word of bits a warp, an entry a lane
-    for (int i0 = warp * 32; i0 < nw; i0 += kThreads) {
-      uint32_t todo = __ballot_sync(kFull, i0 + lane < nw && need[i0 + lane] != 0);
+    // ---- 3. pages for the missing entries: a word of bits a warp (neighbouring words go to
+    // different warps), an entry a lane
+    for (int i0 = warp; i0 < nw; i0 += kThreads) {
+      uint32_t todo = __ballot_sync(kFull, i0 + lane * kWarps < nw && need[i0 + lane * kWarps] != 0);
       while (todo) {
-        const int i = i0 + __ffs(todo) - 1;
+        const int i = i0 + (__ffs(todo) - 1) * kWarps;
         todo &= todo - 1;
         const uint32_t bits = need[i];
         if (!((bits >> lane) & 1)) continue;
@@ -354,23 +441,40 @@ __global__ void __launch_bounds__(kCopyThreads) spec_kv_copy_kernel(const __grid
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-spec_status launch(const void* fn, int64_t grid, int threads, int cluster, int smem, void* stream, void** args) {
+struct Launch {
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) return SPEC_ERR_CUDA;
+  Launch(int64_t grid, int threads, int cluster, int smem, void* stream) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
+spec_status launch(const void* fn, int64_t grid, int threads, int cluster, int smem, void* stream, void** args) {
+  const Launch l(grid, threads, cluster, smem, stream);
+  if (cudaLaunchKernelExC(&l.cfg, fn, args) != cudaSuccess) return SPEC_ERR_CUDA;
   specv_units::count_launches(1);
   return SPEC_OK;
+}
+
+// how many clusters of this size the device has room for at once
+int clusters(const void* fn, int ctas, int threads, int smem) {
+  const Launch l(ctas, threads, ctas, smem, nullptr);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
 }
 
 spec_status check(const spec_kv_pages* p) {
@@ -385,42 +489,50 @@ spec_status check(const spec_kv_pages* p) {
   return SPEC_OK;
 }
 
-// CTAs of the cluster, and the shared memory of each; 0: too large.
+// CTAs of the cluster, of at most `most`, and the shared memory of each; 0: too large.
 constexpr int kMostSmem = 224 * 1024;
-int plan(PagesArgs& a, int* smem) {
-  a.row_words = (a.max_pages + 31) / 32;
-  const int64_t need = static_cast<int64_t>(a.B) * a.row_words, avail = (static_cast<int64_t>(a.num_pages) + 31) / 32;
-  if (need + avail > static_cast<int64_t>(kMostCtas) * kMostSmem / 8) return 0;
+int plan(PagesArgs& a, int batch, int most, int* smem) {
+  const int stretches = (a.max_pages + 128 * batch - 1) / (128 * batch), words = 4 * batch;
+  a.row_words = stretches * words;
+  a.row_recip = ~uint64_t(0) / static_cast<uint64_t>(stretches) + 1;
+  const int64_t need = static_cast<int64_t>(a.B) * a.row_words, avail = (static_cast<int64_t>(a.num_pages) + 127) / 128 * 4;
+  if (need + avail > static_cast<int64_t>(most) * kMostSmem / 8) return 0;
   a.need_words = static_cast<int32_t>(need);
   a.free_words = static_cast<int32_t>(avail);
-  int ctas = need + avail <= 256 ? 1 : kMostCtas;
-  for (;; ctas = kMostCtas) {
-    a.need_share = (a.need_words + ctas - 1) / ctas;
-    a.free_share = (a.free_words + ctas - 1) / ctas;
-    *smem = 8 * (a.need_share + a.free_share);
-    if (*smem <= kMostSmem) return ctas;
-    if (ctas == kMostCtas) return 0;
+  // a small call is quickest with one CTA, another with all that a cluster may have
+  const int ctas = need + avail <= kWordsAlone ? 1 : most;
+  a.need_share = (a.need_words / words + ctas - 1) / ctas * words;
+  a.free_share = (a.free_words / 4 + ctas - 1) / ctas * 4;
+  *smem = 8 * (a.need_share + a.free_share);
+  return *smem <= kMostSmem ? ctas : 0;
+}
+
+template <bool FORK, int N>
+spec_status launch_pages(PagesArgs& a, void* stream) {
+  int smem = 0;
+  if (plan(a, N, kMostCtas, &smem) == 0) return SPEC_ERR_UNSUPPORTED;
+  const void* fn = reinterpret_cast<const void*>(&spec_kv_pages_kernel<FORK, N>);
+  // once for a kernel and device: allow what it takes, and ask whether the device has room for the largest cluster
+  static std::atomic<int> most[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
+  int ctas = most[dev].load(std::memory_order_acquire);
+  if (ctas == 0) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return SPEC_ERR_CUDA;
+    ctas = clusters(fn, kMostCtas, kThreads, kMostSmem) > 0 ? kMostCtas : kPortableCtas;
+    most[dev].store(ctas, std::memory_order_release);
   }
+  ctas = plan(a, N, ctas, &smem);
+  if (ctas == 0) return SPEC_ERR_UNSUPPORTED;
+  void* args[] = {&a};
+  return launch(fn, ctas, kThreads, ctas, smem, stream, args);
 }
 
 template <bool FORK>
 spec_status launch_pages(PagesArgs& a, void* stream) {
-  int smem = 0;
-  const int ctas = plan(a, &smem);
-  if (ctas == 0) return SPEC_ERR_UNSUPPORTED;
-  const void* fn = reinterpret_cast<const void*>(&spec_kv_pages_kernel<FORK>);
-  if (smem > 48 * 1024 - 1024) {
-    static std::atomic<bool> allowed[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
-    if (!allowed[dev].load(std::memory_order_acquire)) {
-      if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) != cudaSuccess)
-        return SPEC_ERR_CUDA;
-      allowed[dev].store(true, std::memory_order_release);
-    }
-  }
-  void* args[] = {&a};
-  return launch(fn, ctas, kThreads, ctas, smem, stream, args);
+  return a.max_pages <= 128 ? launch_pages<FORK, 1>(a, stream) : launch_pages<FORK, 4>(a, stream);
 }
 
 void fill(const spec_kv_pages* p, PagesArgs& a) {
@@ -434,6 +546,8 @@ void fill(const spec_kv_pages* p, PagesArgs& a) {
   while ((1 << a.log_page) < p->page_size) ++a.log_page;
   a.B = p->B;
   a.max_pages = p->max_pages;
+  a.vec = aligned(p->page_table, 16) && (p->B == 1 || p->table_stride % 4 == 0);
+  a.refs_vec = aligned(p->refs, 16);
 }
 
 }  // namespace

@@ -49,7 +49,7 @@ def _norms(qw=0xD000, kw=0xE000, qh=0, kh=0, eps=EPS):
 
 
 @pytest.mark.parametrize("over", [dict(eps=0.0), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(eps=1e-25),
-                                  dict(eps=1e25), dict(qh=-1), dict(kh=-64), dict(qw=0xD002), dict(kw=0xE001)], ids=str)
+                                  dict(eps=1.2e12), dict(qh=-1), dict(kh=-64), dict(qw=0xD002), dict(kw=0xE001)], ids=str)
 def test_refuses(L, over):  # noqa: F811
     c, p = _pack({})
     assert L.spec_kv_append_norm(0x8000, 0xA000, 0xB000, 0xC000, _norms(**over), c, p, 0x9000) == 1
@@ -156,8 +156,8 @@ def test_one_side_strides_and_in_place(dtype, D, off):
 @pytest.mark.parametrize("dtype,D,rot", [("bf16", 128, 128), ("f32", 80, 80), ("bf16", 48, 10), ("f32", 256, 0)])
 def test_sizes_of_heads(dtype, D, rot):
     """Heads of magnitudes from 2^-70 to 2^126, one of zeros, one with one large channel among small ones; eps from 2^-80
-    to 2^80."""
-    for eps in (2.0 ** -80, 1e-12, 1e-6, 1.0, 2.0 ** 80):
+    to 2^40."""
+    for eps in (2.0 ** -80, 1e-12, 1e-6, 1.0, 2.0 ** 40):
         s = Setup(650, 1, 24, 3, 3, D, 32, [0], [24], dtype, rot)
         size = np.exp2(np.linspace(-70, 123, 22)).astype(np.float32)[None, :, None, None]
         for x in (s.q, s.k):
