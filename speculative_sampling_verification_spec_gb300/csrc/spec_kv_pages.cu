@@ -29,9 +29,11 @@ namespace {
 
 using namespace spec_kv_detail;
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMostCtas = 16, kPortableCtas = 8;  // of a cluster
 constexpr int kWordsAlone = 256;  // of bits, that one CTA takes on alone
+// Words up to which CTAs have 256 threads, past it 1024: fewer make for quicker barriers (32 sequences, 2831 pages: 5.6 us
+// a call, 7.5 with 1024), more have more of a large table under way (256 x 8194 entries: 23 us, 33 with 256).
+constexpr int kWordsFew = 4096;
 constexpr int kAhead = 4;      // loads of counts of a lane under way at once
 
 struct PagesArgs {
@@ -72,8 +74,7 @@ __device__ __forceinline__ uint32_t load_of(uint32_t rank, const uint32_t* here)
   asm volatile(
       "{\n\t.reg .b32 there;\n\tmapa.shared::cluster.u32 there, %1, %2;\n\tld.shared::cluster.u32 %0, [there];\n\t}"
       : "=r"(v)
-      : "r"(at), "r"(rank)
-      : "memory");
+      : "r"(at), "r"(rank));
   return v;
 }
 
@@ -196,7 +197,9 @@ struct Stretch {
 };
 
 // Exclusive counts of the bits of `words` words, and their total: by all threads.
+template <int kThreads>
 __device__ uint32_t count_before(const uint32_t* bits, uint32_t* before, int words, uint32_t* scratch) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (words + kThreads - 1) / kThreads;
   const int i0 = min(words, static_cast<int>(threadIdx.x) * per), i1 = min(words, i0 + per);
@@ -224,9 +227,35 @@ __device__ uint32_t count_before(const uint32_t* bits, uint32_t* before, int wor
   return total;
 }
 
+// The last of n ascending numbers, load(0) = 0 .. load(n - 1), that is at most k: seven looks at a time, since a look
+// into another CTA's memory takes long.
+template <typename Load>
+__device__ __forceinline__ int last_at_most(uint32_t k, int n, const Load& load) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 7) / 8;
+    int below = 0;
+#pragma unroll
+    for (int q = 1; q < 8; ++q) {
+      const int at = lo + q * step;
+      below += at < hi && load(min(at, n - 1)) <= k;
+    }
+    lo += below * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// The place of the k-th bit (from 0) of a word.
+__device__ __forceinline__ int bit_of(uint32_t word, uint32_t k) {
+  for (; k; --k) word &= word - 1;
+  return __ffs(word) - 1;
+}
+
 // Bound by latency and by what the cluster's few SMs can ask for at once.
-template <bool FORK, int N>
+template <bool FORK, int N, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1) spec_kv_pages_kernel(const __grid_constant__ PagesArgs a) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ uint32_t dyn[];
   __shared__ uint32_t scratch[kWarps], total[2];            // this CTA's missing entries and free pages
   __shared__ uint32_t need_at[kMostCtas + 1], free_at[kMostCtas + 1];
@@ -295,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_kv_pages_kernel(const __grid
   }
   __syncthreads();
   {
-    const uint32_t n = count_before(need, need_before, nw, scratch);
+    const uint32_t n = count_before<kThreads>(need, need_before, nw, scratch);
     if (tid == 0) total[0] = n;
   }
   cluster_sync();  // the counts are final
@@ -331,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_kv_pages_kernel(const __grid
     }
     __syncthreads();
     {
-      const uint32_t n = count_before(avail, avail_before, nf, scratch);
+      const uint32_t n = count_before<kThreads>(avail, avail_before, nf, scratch);
       if (tid == 0) total[1] = n;
     }
     cluster_sync();
@@ -349,40 +378,27 @@ __global__ void __launch_bounds__(kThreads, 1) spec_kv_pages_kernel(const __grid
     const uint32_t frees = free_at[ctas];
     if (rank == 0 && tid == 0 && a.free_pages) *a.free_pages = static_cast<int32_t>(frees - min(frees, needs));
 
-    // ---- 3. pages for the missing entries: a word of bits a warp (neighbouring words go to
-    // different warps), an entry a lane
-    for (int i0 = warp; i0 < nw; i0 += kThreads) {
-      uint32_t todo = __ballot_sync(kFull, i0 + lane * kWarps < nw && need[i0 + lane * kWarps] != 0);
-      while (todo) {
-        const int i = i0 + (__ffs(todo) - 1) * kWarps;
-        todo &= todo - 1;
-        const uint32_t bits = need[i];
-        if (!((bits >> lane) & 1)) continue;
-        uint32_t k = need_at[rank] + need_before[i] + __popc(bits & ((1u << lane) - 1));
-        const int b = (w0 + i) / a.row_words, c = (w0 + i - b * a.row_words) * 32 + lane;
-        int32_t* const at = a.table + b * a.table_stride + c;
-        if (k >= frees) {
-          report(a.status, SPEC_ERR_CACHE_FULL);
-          continue;
-        }
-        int r = 0;
-        while (k >= free_at[r + 1]) ++r;
-        k -= free_at[r];
-        // the last word with at most k bits before it
-        int lo = 0, hi = min(a.free_words - r * a.free_share, a.free_share);
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) / 2;
-          if (load_of(r, avail_before + mid) <= k)
-            lo = mid;
-          else
-            hi = mid;
-        }
-        uint32_t word = load_of(r, avail + lo);
-        for (uint32_t skip = k - load_of(r, avail_before + lo); skip; --skip) word &= word - 1;
-        const int page = (r * a.free_share + lo) * 32 + __ffs(word) - 1;
-        *at = page;
-        a.refs[page] = 1;
+    // ---- 3. pages for the missing entries, one a thread
+    const uint32_t mine = total[0];
+    for (uint32_t n = tid; n < mine; n += kThreads) {
+      uint32_t k = need_at[rank] + n;
+      if (k >= frees) {
+        report(a.status, SPEC_ERR_CACHE_FULL);
+        break;
       }
+      const int i = last_at_most(n, nw, [&](int w) { return need_before[w]; });
+      const int b = (w0 + i) / a.row_words;
+      const int c = (w0 + i - b * a.row_words) * 32 + bit_of(need[i], n - need_before[i]);
+      int r = 0;
+#pragma unroll
+      for (int q = 1; q < kMostCtas; ++q) r += q < ctas && k >= free_at[q];
+      k -= free_at[r];
+      const int lo = last_at_most(k, min(a.free_words - r * a.free_share, a.free_share),
+                                  [&](int w) { return load_of(r, avail_before + w); });
+      const uint32_t word = load_of(r, avail + lo), before = load_of(r, avail_before + lo);
+      const int page = (r * a.free_share + lo) * 32 + bit_of(word, k - before);
+      a.table[b * a.table_stride + c] = page;
+      a.refs[page] = 1;
     }
   }
   cluster_sync();  // others may still be reading here
@@ -507,11 +523,11 @@ int plan(PagesArgs& a, int batch, int most, int* smem) {
   return *smem <= kMostSmem ? ctas : 0;
 }
 
-template <bool FORK, int N>
+template <bool FORK, int N, int kThreads>
 spec_status launch_pages(PagesArgs& a, void* stream) {
   int smem = 0;
   if (plan(a, N, kMostCtas, &smem) == 0) return SPEC_ERR_UNSUPPORTED;
-  const void* fn = reinterpret_cast<const void*>(&spec_kv_pages_kernel<FORK, N>);
+  const void* fn = reinterpret_cast<const void*>(&spec_kv_pages_kernel<FORK, N, kThreads>);
   // once for a kernel and device: allow what it takes, and ask whether the device has room for the largest cluster
   static std::atomic<int> most[64];
   int dev = 0;
@@ -532,7 +548,10 @@ spec_status launch_pages(PagesArgs& a, void* stream) {
 
 template <bool FORK>
 spec_status launch_pages(PagesArgs& a, void* stream) {
-  return a.max_pages <= 128 ? launch_pages<FORK, 1>(a, stream) : launch_pages<FORK, 4>(a, stream);
+  const int64_t words = (static_cast<int64_t>(a.B) * a.max_pages + a.num_pages) / 32;
+  if (words <= kWordsFew)
+    return a.max_pages <= 128 ? launch_pages<FORK, 1, 256>(a, stream) : launch_pages<FORK, 4, 256>(a, stream);
+  return a.max_pages <= 128 ? launch_pages<FORK, 1, 1024>(a, stream) : launch_pages<FORK, 4, 1024>(a, stream);
 }
 
 void fill(const spec_kv_pages* p, PagesArgs& a) {
