@@ -659,38 +659,44 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           const uint32_t tS = tm + lanes + (n & 1) * NR + r_base;
           const auto sees = [&](int r) { return seen_from(sm.pos[r_base + r]); };
           float x[RT];
-#pragma unroll
-          for (int c = 0; c < RT; c += 8) tmem_ld<8>(tS + c, &x[c]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < RT; c += 8) tmem_tie<8>(&x[c]);
-          if (!one_factor) {
-#pragma unroll
-            for (int r = 0; r < RU; ++r) x[r] *= sm.factor[r_base + r];
-          }
-          // scores in log2 units against the rows' references
-#pragma unroll
-          for (int c = 0; c < RU; c += CH) {
-            if (c < fours) {
-              const float4 ref = *reinterpret_cast<const float4*>(&sm.refs[r_base + c]);
-              unpack2(fma2(pack2(x[c], x[c + 1]), ks2, add2(lv2, pack2(ref.x, ref.y))), x[c], x[c + 1]);
-              unpack2(fma2(pack2(x[c + 2], x[c + 3]), ks2, add2(lv2, pack2(ref.z, ref.w))), x[c + 2], x[c + 3]);
-            }
-          }
-          if (edge) {
-#pragma unroll
-            for (int r = 0; r < RU; ++r) x[r] = sees(r) ? x[r] : -INFINITY;
-          }
+          // a warp none of whose tokens any row sees has nothing to do but to say so
+          const int j_warp = j - lane;
+          const bool idle = SINKS && edge &&
+                            (j_warp > pos_hi || (j_warp >= sinks && j_warp + 31 <= p.L + p.row0 / a.G - a.window));
           float top = -INFINITY;
+          if (!idle) {
 #pragma unroll
-          for (int c = 0; c < RU; c += CH)
-            if (c < fours) top = fmaxf(fmaxf(top, fmaxf(x[c], x[c + 1])), fmaxf(x[c + 2], x[c + 3]));
+            for (int c = 0; c < RT; c += 8) tmem_ld<8>(tS + c, &x[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < RT; c += 8) tmem_tie<8>(&x[c]);
+            if (!one_factor) {
+#pragma unroll
+              for (int r = 0; r < RU; ++r) x[r] *= sm.factor[r_base + r];
+            }
+            // scores in log2 units against the rows' references
+#pragma unroll
+            for (int c = 0; c < RU; c += CH) {
+              if (c < fours) {
+                const float4 ref = *reinterpret_cast<const float4*>(&sm.refs[r_base + c]);
+                unpack2(fma2(pack2(x[c], x[c + 1]), ks2, add2(lv2, pack2(ref.x, ref.y))), x[c], x[c + 1]);
+                unpack2(fma2(pack2(x[c + 2], x[c + 3]), ks2, add2(lv2, pack2(ref.z, ref.w))), x[c + 2], x[c + 3]);
+              }
+            }
+            if (edge) {
+#pragma unroll
+              for (int r = 0; r < RU; ++r) x[r] = sees(r) ? x[r] : -INFINITY;
+            }
+#pragma unroll
+            for (int c = 0; c < RU; c += CH)
+              if (c < fours) top = fmaxf(fmaxf(top, fmaxf(x[c], x[c + 1])), fmaxf(x[c + 2], x[c + 3]));
+          }
           // would some weight leave the pieces' range, or has some row no reference yet?
           if (group_any(group, top > static_cast<float>(kTop) || t <= t_unset)) {
             float most = -INFINITY;  // of row `lane`, over the warp's tokens
 #pragma unroll
             for (int c = 0; c < RU; c += CH) {
-              if (c < fours) {
+              if (!idle && c < fours) {
 #pragma unroll
                 for (int i = 0; i < CH; ++i) {
                   const float w = of_order(__reduce_max_sync(kFull, order_of(x[c + i])));
@@ -716,7 +722,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             group_sync(group);
 #pragma unroll
             for (int c = 0; c < RU; c += CH) {
-              if (c < fours) {
+              if (!idle && c < fours) {
                 const float4 u = *reinterpret_cast<const float4*>(&sm.up()[r_base + c]);
                 x[c] -= u.x;
                 x[c + 1] -= u.y;
@@ -768,7 +774,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
             uint32_t w[kPieces][4] = {};
 #pragma unroll
             for (int i = 0; i < 16; i += CH) {
-              if (i < n16 && c + i < RU && c + i < fours) {
+              if (!idle && i < n16 && c + i < RU && c + i < fours) {
                 uint32_t u[kPieces][2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {

@@ -118,7 +118,6 @@ __device__ __forceinline__ uint32_t word_of(uint32_t bits) {
 struct Row {
   int last;        // hold: columns from this on are empty; fork: the parent's tokens.  -1: nothing happens to it
   int keep, from;  // hold: columns below `keep` and from `from` on are needed
-  __device__ __forceinline__ bool needs(int c) const { return c < last && (c < keep || c >= from); }
 };
 
 __device__ __forceinline__ Row hold_row(const PagesArgs& a, int b) {
@@ -142,6 +141,9 @@ __device__ __forceinline__ int parent_of(const PagesArgs& a, int b, int* L) {
   if ((pp != -1 && pp != p) || *L < 0 || *L > (static_cast<int64_t>(a.max_pages) << a.log_page)) return -2;
   return p;
 }
+
+// n of four bits, from the lowest on
+__device__ __forceinline__ uint32_t first_of(int n) { return (1u << min(max(n, 0), 4)) - 1; }
 
 // A warp's columns of a row: four a lane, N times.  Tables of up to 128 columns take N = 1, others 4, because a
 // stretch costs about as many instructions however long it is.
@@ -173,24 +175,15 @@ struct Stretch {
       if (row.last < 0 && c == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
     }
   }
-  // Whether there is anything to do.  Most stretches of a long table are all needed and there, or neither.
-  __device__ __forceinline__ bool some(const PagesArgs& a) const {
-    if (row.last < 0) return false;
-    if constexpr (FORK) return true;
-    const int c0 = c - (threadIdx.x & 31) * 4, c1 = c0 + 128 * N;
-    if (c0 >= row.last || (c0 >= row.keep && c1 <= row.from)) {  // none is needed
-      int all = -1;
-#pragma unroll
-      for (int k = 0; k < N; ++k) all &= entry[k].x[0] & entry[k].x[1] & entry[k].x[2] & entry[k].x[3];
-      return __any_sync(kFull, all != -1);
-    }
-    if (c1 <= row.last && (c0 >= row.from || c1 <= row.keep)) {  // all are
-      uint32_t most = 0;
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) most = max(most, static_cast<uint32_t>(entry[k].x[e]));
-      return __any_sync(kFull, most >= static_cast<uint32_t>(a.num_pages));
+  // hold: whether this lane has something to do among the 128 columns of the k-th time.  Most are all needed and there,
+  // or neither.
+  __device__ __forceinline__ bool some(const PagesArgs& a, int k) const {
+    const int c0 = column(k) - (threadIdx.x & 31) * 4, c1 = c0 + 128;
+    const int32_t* const x = entry[k].x;
+    if (c0 >= row.last || (c0 >= row.keep && c1 <= row.from)) return (x[0] & x[1] & x[2] & x[3]) != -1;
+    if (c1 <= row.last && (c0 >= row.from || c1 <= row.keep)) {
+      const auto u = [&](int e) { return static_cast<uint32_t>(x[e]); };
+      return max(max(u(0), u(1)), max(u(2), u(3))) >= static_cast<uint32_t>(a.num_pages);
     }
     return true;
   }
@@ -280,45 +273,53 @@ __global__ void __launch_bounds__(kThreads, 1) spec_kv_pages_kernel(const __grid
       now.load(a, w0 / kStretchWords + i);
     else if (i + kWarps < nw / kStretchWords)
       next.load(a, w0 / kStretchWords + i + kWarps);
-    if (!now.some(a)) {
+    bool some = FORK;
+    if constexpr (!FORK) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) some |= now.some(a, k);
+    }
+    if (now.row.last < 0 || !__any_sync(kFull, some)) {
       if (lane < kStretchWords) need[i * kStretchWords + lane] = 0;
     } else {
       bool bad = false;
-      uint32_t missing[N] = {};
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        Four to = now.entry[k];
+        const int c0 = now.column(k);
+        const Four& old = now.entry[k];
+        Four to = old;
+        uint32_t missing = 0;
+        if constexpr (FORK) {
+          const int whole = now.row.last >> a.log_page;
+          const bool rest = (now.row.last & ((1 << a.log_page) - 1)) != 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = now.column(k) + e;
-          const int32_t old = now.entry[k].x[e];
-          if constexpr (FORK) {
-            const int whole = now.row.last >> a.log_page;
-            const bool partly = c == whole && (now.row.last & ((1 << a.log_page) - 1)) != 0;
+          for (int e = 0; e < 4; ++e) {
             const int32_t src = now.source[k].x[e];
-            const bool page = src >= 0 && src < a.num_pages;
-            if (old >= 0 && old < a.num_pages) atomicSub(&a.refs[old], 1);
-            if (c < whole && page) atomicAdd(&a.refs[src], 1);
-            if (partly && page) missing[k] |= 1u << e;
-            to.x[e] = c < whole && page ? src : -1;
-            bad |= (c < whole && src >= a.num_pages) || (partly && !page);
-          } else if (now.row.needs(c)) {
-            if (old < 0) missing[k] |= 1u << e;
-            bad |= old >= a.num_pages;
-          } else if (old != -1) {
-            if (old >= 0 && old < a.num_pages) atomicSub(&a.refs[old], 1);
-            to.x[e] = -1;
+            const bool partly = rest && c0 + e == whole, page = src >= 0 && src < a.num_pages;
+            if (old.x[e] >= 0 && old.x[e] < a.num_pages) atomicSub(&a.refs[old.x[e]], 1);
+            if (c0 + e < whole && page) atomicAdd(&a.refs[src], 1);
+            if (partly && page) missing |= 1u << e;
+            to.x[e] = c0 + e < whole && page ? src : -1;
+            bad |= (c0 + e < whole && src >= a.num_pages) || (partly && !page);
+          }
+        } else if (__any_sync(kFull, now.some(a, k))) {
+          const uint32_t needed = first_of(now.row.last - c0) & (first_of(now.row.keep - c0) | ~first_of(now.row.from - c0));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if ((needed >> e) & 1) {
+              if (old.x[e] < 0) missing |= 1u << e;
+              bad |= old.x[e] >= a.num_pages;
+            } else if (old.x[e] != -1) {
+              if (old.x[e] >= 0 && old.x[e] < a.num_pages) atomicSub(&a.refs[old.x[e]], 1);
+              to.x[e] = -1;
+            }
           }
         }
-        to.store(a.table + now.b * a.table_stride, now.entry[k], now.column(k), a.max_pages);
+        to.store(a.table + now.b * a.table_stride, old, c0, a.max_pages);
+        const uint32_t word = word_of(missing);
+        if ((lane & 7) == 0) need[i * kStretchWords + k * 4 + lane / 8] = word;
       }
       if (bad) report(a.status, SPEC_ERR_CACHE_RANGE);
       if (FORK && now.column(0) == 0) a.seq_lens[now.b] = now.row.last;
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const uint32_t word = word_of(missing[k]);
-        if ((lane & 7) == 0) need[i * kStretchWords + k * 4 + lane / 8] = word;
-      }
     }
     if (!FORK) now = next;
   }
