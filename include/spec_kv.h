@@ -118,7 +118,7 @@ typedef struct {
 
 /* spec_kv_append with norms (NULL: without): a head x of a query or key of a new token
  * becomes (x r) w before it is rotated, with r = 1 / sqrt(mean of x_i^2 + eps) as the
- * nearest float (once in thousands of heads the next one), w its weights, and each
+ * nearest float (once in about a hundred thousand heads the next one), w its weights, and each
  * product rounded to float.  A head with an infinity has r = 0, one with a NaN is NaN.
  * Everything else is as for spec_kv_append. */
 spec_status spec_kv_append_norm(const void* q, const void* k, const void* v, const float* cos_sin,

@@ -341,6 +341,7 @@ spec_status spec_kv_append_norm(const void* q, const void* k, const void* v, con
     g.k_weight_head = norms->k_head_stride;
     split(static_cast<double>(norms->eps) * cache->D, &g.eps_hi, &g.eps_lo);
     split(std::sqrt(static_cast<double>(cache->D)), &g.root_hi, &g.root_lo);
+    for (g.bias = 2; g.bias < 2 * cache->D;) g.bias *= 2;
     // D eps, scaled like the squares, stays below 2^60
     g.least_exp = 127 - (60 - (std::ilogb(static_cast<double>(norms->eps) * cache->D) + 1)) / 2;
   }

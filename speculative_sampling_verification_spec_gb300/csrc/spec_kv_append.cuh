@@ -23,8 +23,8 @@
 //
 // Norms.  r = 1 / sqrt(mean x^2 + eps) of a head goes to the keys' scales and codes
 // through comparisons and roundings, so it is made a function of the inputs alone: the
-// sum of the squares and its root are carried in two floats (some 37 bits), and r is the
-// nearest float but for one head in thousands.  (In 64 bits the sums of a prompt alone
+// sum of the squares and its root are carried in two floats (some 40 bits), and r is the
+// nearest float but for one head in a hundred thousand.  (In 64 bits the sums of a prompt alone
 // would take longer than the rest: the chip's rate of such multiply-adds is a hundredth
 // of that in 32.)  The threads of a head are a power of two of neighbouring lanes, the
 // last of them idle where its chunks are not, and add up by exchanging; with PC = 1 a
@@ -54,6 +54,7 @@ struct AppendArgs {
   const float* k_weight;
   int64_t q_weight_head, k_weight_head;
   float eps_hi, eps_lo, root_hi, root_lo;
+  float bias;         // see squares
   int32_t least_exp;  // of what sums of squares are scaled by: below, the squares are nothing beside eps
 };
 
@@ -224,11 +225,10 @@ __device__ __forceinline__ void turn_chunk(const AppendArgs& g, const float* cs,
 
 __device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
-// The sum of the squares of a head's channels, times the square of a power of two f that brings the largest to [1, 4):
-// hi + lo.  The sum is run on top of kBias, which no square and no sum reaches: every addition leaves a multiple of the
-// bias's last place in the sum, exactly, and the rest of the square, exactly, for a second sum (of at most 2^-12 each,
-// so that its own roundings are some 2^-37 of the whole).
-constexpr float kBias = 4096.0f;
+// The sum of the squares of a head's channels, times the square of a power of two f that brings the largest to [1, 2):
+// hi + lo.  A lane's sum is run on top of a bias, 2 D or the power of two above, which no lane's sum reaches: every
+// addition leaves a multiple of the bias's last place in the sum, exactly, and the rest of the square, all but exactly,
+// for a second sum of small numbers.  The multiples of all lanes add up exactly, too.
 struct Squares {
   float hi, lo, f;
 };
@@ -246,7 +246,7 @@ __device__ __forceinline__ void squares(const AppendArgs& g, const Values& value
 #pragma unroll
     for (int r = 0; r < R; ++r) m[r] = fmaxf(m[r], __shfl_xor_sync(mask, m[r], d));
   }
-  const u64 minus = pack2(-1.0f, -1.0f), bias = pack2(kBias, kBias);
+  const u64 minus = pack2(-1.0f, -1.0f), bias = pack2(g.bias, g.bias);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int e = min(max(static_cast<int>(__float_as_uint(m[r]) >> 23), g.least_exp), 253);

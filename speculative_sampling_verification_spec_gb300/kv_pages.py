@@ -19,6 +19,7 @@ EXPORTED = ("spec_kv_fork", "spec_kv_hold")
 # spec_kv_pages of include/spec_kv_pages.h, in native layout
 _PAGES = struct.Struct("@4i2Pq3P")
 _I32 = torch.int32
+_MOST_INT = (1 << 31) - 1     # (ctypes would drop the bits above)
 
 _loaded = None
 
@@ -81,6 +82,8 @@ def spec_kv_hold(refs, page_table, seq_lens, new_lens=None, *, page_size, T=0, w
         with torch.cuda.device(refs.device):
             return spec_kv_hold(refs, page_table, seq_lens, new_lens, page_size=page_size, T=T, window=window, sinks=sinks,
                                 free=free, status=status, stream=stream)
+    if max(T, window, sinks, page_size) > _MOST_INT:
+        raise binding.SpecError(binding.SPEC_ERR_INVALID_ARG, "spec_kv_hold")
     pages = _pages(refs, page_table, page_size, free, status, stream)
     B, dev = page_table.shape[0], refs.get_device()
     code = _lib().spec_kv_hold(pages, _check("seq_lens", seq_lens, B, dev),
