@@ -1,6 +1,6 @@
 """Speculative decoding with a paged 8-bit key/value cache: draft, score in one pass, verify, go on.
 
-    python examples/paged_decode.py [--batch 8] [--draft 4] [--rounds 32] [--greedy]
+    python examples/paged_decode.py [--batch 8] [--draft 4] [--rounds 32] [--greedy] [--window 64 [--sinks 4]]
 
 The target is one attention layer with random weights between an embedding and its transpose, small enough to read but
 with the real flow of a serving loop: each round feeds K + 1 tokens a sequence (the last emitted one and K drafted ones),
@@ -8,6 +8,10 @@ stores their keys and values with `spec_kv_append`, attends over everything stor
 the logits of the K + 1 positions to `spec_verify`.  Rejected tokens are dropped by moving the length back; the next
 round writes over them.  The draft is the same model with noise on its logits, drawn from with `spec_sample_draft`;
 it is stateless (it sees the last token alone), so that the cache is the target's only.
+
+With a window, the target normalises its queries and keys, attends to the last tokens and the first ones alone, and
+`spec_kv_hold` hands out its pages: a sequence has those of the tokens it still sees, and the pool holds for any number of
+rounds.
 """
 from __future__ import annotations
 
@@ -29,10 +33,12 @@ def angles(positions, rot_dim, device, base=10000.0):
 
 
 class Target:
-    """Embedding, one attention layer over a paged cache, unembedding.  dtype: bfloat16 or float32."""
+    """Embedding, one attention layer over a paged cache, unembedding.  dtype: bfloat16 or float32.  window > 0: attention
+    to that many tokens and the first `sinks` ones, with norms of queries and keys, over a pool of pages that has room for
+    `new_tokens` at a time beside what is seen."""
 
     def __init__(self, vocab=512, heads=8, kv_heads=2, head_dim=64, batch=8, max_tokens=512, page_size=16,
-                 dtype=torch.bfloat16, seed=0, device="cuda"):
+                 dtype=torch.bfloat16, seed=0, device="cuda", window=0, sinks=0, new_tokens=8):
         g = torch.Generator(device=device).manual_seed(seed)
         d = heads * head_dim
 
@@ -43,11 +49,20 @@ class Target:
         self.embed = torch.randn(vocab, d, generator=g, device=device).to(dtype)
         self.wqkv, self.wo = w(d, (heads + 2 * kv_heads) * head_dim), w(d, d)
         self.unembed = w(d, vocab)
-        # every sequence owns the pages its table names; which ones they are does not matter
         pages = -(-max_tokens // page_size)
+        self.cos_sin = angles(pages * page_size, head_dim, device)
+        self.window, self.sinks, self.refs, self.norms = window, sinks, None, {}
+        if window:
+            # the pages of the sinks, and those that a window and the new tokens touch wherever they begin
+            each = -(-sinks // page_size) + (window + new_tokens - 2) // page_size + 2
+            self.refs = torch.zeros(batch * min(each, pages), dtype=torch.int32, device=device)
+            self.table = torch.full((batch, pages), -1, dtype=torch.int32, device=device)
+            self.norms = {n: 1 + 0.1 * torch.randn(head_dim, generator=g, device=device) for n in ("q_norm", "k_norm")}
+            self.cache = sv.PagedKVCache.empty(self.refs.numel(), page_size, kv_heads, head_dim, device)
+            return
+        # every sequence owns the pages its table names; which ones they are does not matter
         self.table = torch.randperm(batch * pages, generator=g, device=device).to(torch.int32).view(batch, pages)
         self.cache = sv.PagedKVCache.empty(batch * pages, page_size, kv_heads, head_dim, device)
-        self.cos_sin = angles(pages * page_size, head_dim, device)
 
     def __call__(self, tokens, seq_lens, new_lens=None):
         """tokens [B, T] at positions seq_lens[b] + t -> logits [B, T, vocab] (float32)."""
@@ -56,8 +71,11 @@ class Target:
         x = self.embed[tokens.long()]
         qkv = (x @ self.wqkv).view(B, T, h + 2 * k, d)
         q, keys, values = qkv[:, :, :h], qkv[:, :, h:h + k], qkv[:, :, h + k:]      # views: strides of the fused product
-        q = sv.spec_kv_append(q, keys, values, self.cache, self.table, seq_lens, new_lens, cos_sin=self.cos_sin)
-        y = sv.spec_kv_attention(q, self.cache, self.table, seq_lens, new_lens)
+        if self.refs is not None:                  # what left the window and what was rejected make room
+            sv.spec_kv_hold(self.refs, self.table, seq_lens, new_lens, T=T, page_size=self.cache.page_size,
+                            window=self.window, sinks=self.sinks)
+        q = sv.spec_kv_append(q, keys, values, self.cache, self.table, seq_lens, new_lens, cos_sin=self.cos_sin, **self.norms)
+        y = sv.spec_kv_attention(q, self.cache, self.table, seq_lens, new_lens, window=self.window, sinks=self.sinks)
         return ((x + y.reshape(B, T, h * d) @ self.wo) @ self.unembed).float()
 
     def draft(self, tokens, noise):
@@ -106,8 +124,11 @@ def main():
     ap.add_argument("--draft", type=int, default=4, help="drafted tokens a round")
     ap.add_argument("--rounds", type=int, default=32)
     ap.add_argument("--greedy", action="store_true")
+    ap.add_argument("--window", type=int, default=0, help="tokens that a query sees (0: all)")
+    ap.add_argument("--sinks", type=int, default=0, help="first tokens that it sees beside them")
     a = ap.parse_args()
-    target = Target(batch=a.batch, max_tokens=a.rounds * (a.draft + 1) + a.draft + 1)
+    target = Target(batch=a.batch, max_tokens=a.rounds * (a.draft + 1) + a.draft + 1, window=a.window, sinks=a.sinks,
+                    new_tokens=a.draft + 1)
     first = torch.arange(a.batch, device="cuda", dtype=torch.int32) % target.vocab
     tokens, accepted = decode(target, first, a.draft, a.rounds, greedy=a.greedy)
     n = accepted.float().mean().item()

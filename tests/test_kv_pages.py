@@ -306,7 +306,8 @@ def test_python_checks():
                      ((r, t, s), dict(status=s.cpu()))):
         with pytest.raises(ValueError):
             sv.spec_kv_hold(*args, page_size=16, **kw)
-    for kw in (dict(page_size=17), dict(page_size=16, T=-1), dict(page_size=16, window=-1), dict(page_size=16, sinks=-1)):
+    for kw in (dict(page_size=17), dict(page_size=16, T=-1), dict(page_size=16, window=-1), dict(page_size=16, sinks=-1),
+               dict(page_size=16, T=(1 << 32) + 1), dict(page_size=16, window=1 << 31)):
         with pytest.raises(sv.SpecError):
             sv.spec_kv_hold(r, t, s, **kw)
     with pytest.raises(sv.SpecError):

@@ -148,6 +148,9 @@ def test_limits_are_the_calls_that_were_there(dtype, D):
     assert torch.equal(sv.spec_kv_attention(q, cache, *idx, window=(1 << 31) - 1, sinks=4), full)
     assert torch.equal(sv.spec_kv_attention(q, cache, *idx, window=1, sinks=(1 << 31) - 1), full)
     assert not torch.equal(sv.spec_kv_attention(q, cache, *idx, window=200, sinks=4), win)
+    for kw in (dict(sinks=-1), dict(window=200, sinks=1 << 31), dict(window=200, sinks=(1 << 32) + 4), dict(window=1 << 32)):
+        with pytest.raises(sv.SpecError):
+            sv.spec_kv_attention(q, cache, *idx, **kw)
 
 
 @gpu
@@ -172,14 +175,15 @@ def test_nan_tokens_touch_the_rows_that_see_them(dtype):
 
 
 @gpu
-@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("f32", 128)])
-def test_missing_pages(dtype, D):
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("f32", 128)])
+@pytest.mark.parametrize("S", [16, 128])
+def test_missing_pages(dtype, D, S):
     """A page of the sinks or of the window that is not the pool's is an error; one between is none."""
-    for column, bad in ((0, True), (1, True), (2, False), (30, False), (700 + 1 - 100, True)):
-        s = Setup(550, 2, 2, 4, 2, D, 16, [700, 700], [2, 2], dtype)
+    for column, bad in ((0, True), (20 // S, True), (20 // S + 1, False), (600 // S - 1, False), (601 // S, True)):
+        s = Setup(550, 2, 2, 4, 2, D, S, [700, 700], [2, 2], dtype)
         cache = s.cache()
         s.append(cache)
-        s.table[0, column if column < 32 else column // 16] = 1 << 20
+        s.table[0, column] = 1 << 20
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         out, lse = run(s, 100, 20, cache=cache, status=status)
         assert status.item() == (8 if bad else 0), column
