@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
   Piece p;
   while (walk_next(a, walk, p)) {
     // the piece's tokens are counted from 0, without what is left out; position_of: where they are
-    const int j0 = p.tile0 << a.log_tile, near = p.near << a.log_tile, skip = p.skip << a.log_tile;
-    const int count = min(p.tile1 << a.log_tile, p.L + p.n) - j0 - skip;
+    const int j0 = p.tile0 << a.log_tile, near = p.near - j0, skip = p.skip;
+    const int count = min(p.tile1 << a.log_tile, p.L + p.n - skip) - j0;
     const auto position_of = [&](int i) { return j0 + i + (i >= near ? skip : 0); };
     float q[ROWS][CH], acc[ROWS][CH];  // queries in log2 units; zero past the last row and channel
 #pragma unroll

@@ -4,10 +4,14 @@
 //
 // The attention's work is a list of tiles of 2^log_tile tokens: sequence after
 // sequence, within a sequence head after head, within a head in order of
-// position: from the first tile that the window reaches, or from 0; where first
-// tokens stay visible beside a window, their tiles come first and the tiles between
-// are left out.  Before each head's tiles come `overhead` places without one, for what
-// it costs to take up a head.  The list is cut into `nranges` equal ranges (from
+// position: from the first tile that the window reaches, or from 0.  Before each head's
+// tiles come `overhead` places without one, for what it costs to take up a head.
+//
+// Where first tokens stay visible beside a window (sinks), the tokens of a row tile are
+// the pages of the sinks and those from its window's first page on, as if they lay side
+// by side: tiles are cut from that sequence, `skip` positions are left out of it after
+// the first `near`.  (A tile of their own for the sinks costs as much as any: 9
+// drafts each of 32 sequences on windows of 4096 tokens 72 us, 76 then.)  The list is cut into `nranges` equal ranges (from
 // the lengths on the device, so a batch of unequal sequences is spread evenly and
 // no length crosses to the host); a range is walked by one CTA for one row tile.
 // An item (sequence, head, row tile) that lies in one range is finished there; one
@@ -112,17 +116,21 @@ __device__ __forceinline__ float2 codes2_to_float2(uint16_t c) {
   return __half22float2(__half2(h));
 }
 
-// tiles that hold the sinks
-__device__ __forceinline__ int sink_tiles(const KvArgs& a) { return a.sinks > 0 ? ((a.sinks - 1) >> a.log_tile) + 1 : 0; }
+// positions of the sinks' pages
+__device__ __forceinline__ int64_t near_tokens(const KvArgs& a) {
+  return a.sinks > 0 ? ((static_cast<int64_t>(a.sinks) - 1) >> a.log_page) + 1 << a.log_page : 0;
+}
 
-// The tokens of sequence b and the tiles its rows read: the first ns (before t0), and
-// from tile t0 to position L + n.  No tiles when it has no new token or its lengths are
-// out of range.
+// The tokens of sequence b and the tiles its rows read: positions from tile t0 to L + n,
+// or, with sinks, at most nt tiles of what lies side by side.  No tiles when it has no new
+// token or its lengths are out of range.
 struct SeqSpan {
-  int L, n, t0, ns, nt;
+  int L, n, t0, nt;
   int places;  // a head's in the list
   bool bad;
 };
+// SINKS: the call may have some (what a kernel for calls without them need not ask).
+template <bool SINKS = true>
 __device__ __forceinline__ SeqSpan seq_span(const KvArgs& a, int b) {
   SeqSpan s;
   s.L = a.seq_lens[b];
@@ -130,14 +138,19 @@ __device__ __forceinline__ SeqSpan seq_span(const KvArgs& a, int b) {
   const int64_t cap = static_cast<int64_t>(a.max_pages) << a.log_page;
   s.bad = s.L < 0 || s.n < 0 || s.n > a.T || static_cast<int64_t>(s.L) + s.n > cap;
   s.t0 = 0;
-  s.ns = 0;
   s.nt = 0;
   s.places = 0;
   if (!s.bad && s.n > 0) {
     const int first = (a.window > 0 && s.L + 1 > a.window) ? s.L + 1 - a.window : 0;
     s.t0 = first >> a.log_tile;
-    s.ns = min(s.t0, sink_tiles(a));
-    s.nt = s.ns + ((s.L + s.n - 1) >> a.log_tile) + 1 - s.t0;
+    s.nt = ((s.L + s.n - 1) >> a.log_tile) + 1 - s.t0;
+    if (SINKS && a.sinks > 0) {
+      // the sinks' pages, the window, the tokens of a row tile's rows, and what comes before the
+      // window in its first page
+      const int64_t most = near_tokens(a) + a.window + (a.rows - 1) / a.G + (1 << a.log_page);
+      s.nt = static_cast<int>(min(int64_t(s.nt) + s.t0, (most >> a.log_tile) + 1));
+      s.t0 = 0;
+    }
     s.places = s.nt + a.overhead;
   }
   return s;
@@ -151,13 +164,13 @@ struct RangePlan {
 
 // All threads of the CTA (NT of them) take part, once; `plan` and `scratch` are in
 // shared memory.  When prefix is given, it gets the places before each sequence.
-template <int NT>
+template <int NT, bool SINKS = true>
 __device__ void make_plan_range(const KvArgs& a, int range, RangePlan* plan, int* scratch, int32_t* prefix) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = (a.B + NT - 1) / NT;
   const int b0 = min(a.B, tid * c), b1 = min(a.B, b0 + c);
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_span(a, b).places * a.Hkv;
+  for (int b = b0; b < b1; ++b) mine += seq_span<SINKS>(a, b).places * a.Hkv;
   int inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -185,7 +198,7 @@ __device__ void make_plan_range(const KvArgs& a, int range, RangePlan* plan, int
   if (w0 < w1 && before <= w0 && w0 < before + mine) {
     int at = before;
     for (int b = b0; b < b1; ++b) {
-      const int k = seq_span(a, b).places * a.Hkv;
+      const int k = seq_span<SINKS>(a, b).places * a.Hkv;
       if (w0 < at + k) {
         plan->b = b;
         plan->off = w0 - at;
@@ -198,7 +211,7 @@ __device__ void make_plan_range(const KvArgs& a, int range, RangePlan* plan, int
     int at = before;
     for (int b = b0; b < b1; ++b) {
       prefix[b] = at;
-      at += seq_span(a, b).places * a.Hkv;
+      at += seq_span<SINKS>(a, b).places * a.Hkv;
     }
   }
   __syncthreads();
@@ -210,8 +223,8 @@ struct Piece {
   int b, h;
   int L, n;          // tokens before the new ones; new tokens
   int row0, nrows;   // rows of this row tile
-  int tile0, tile1;  // absolute tiles [tile0, tile1); may be empty
-  int near, skip;    // the `skip` tiles from tile0 + near on are left out (0: none)
+  int tile0, tile1;  // tiles [tile0, tile1); may be empty
+  int near, skip;    // the `skip` positions (whole pages) from `near` on are left out (0: none)
   int first;         // first position that a row sees through its window
   int c0, c1;        // first and last range that hold tiles of the item
   int slot;          // where a partial result goes, when these differ
@@ -242,9 +255,10 @@ __device__ __forceinline__ int part_slot(const KvArgs& a, int c, int c0, int rt)
 }
 
 // The next piece that has rows; false at the range's end.
+template <bool SINKS = true>
 __device__ __forceinline__ bool walk_next(const KvArgs& a, Walk& k, Piece& p) {
   while (k.w < k.w1) {
-    const SeqSpan s = seq_span(a, k.b);
+    const SeqSpan s = seq_span<SINKS>(a, k.b);
     if (k.off >= s.places * a.Hkv) {  // on to the next sequence
       ++k.b;
       k.off = 0;
@@ -271,16 +285,20 @@ __device__ __forceinline__ bool walk_next(const KvArgs& a, Walk& k, Piece& p) {
     const int hi = ((s.L + t_last) >> a.log_tile) + 1;
     const int lo = (a.window > 0 && s.L + t_first + 1 > a.window) ? s.L + t_first + 1 - a.window : 0;
     p.first = lo;
-    // Of the tiles of sinks, those in the piece (they may go on past t0, where nothing is left out
-    // and places are tiles); of the others, those in it from tile `far` on, where this row tile's
-    // window begins.
-    const int st = sink_tiles(a), near0 = min(t0, st), near1 = max(near0, min(min(t1, st), hi));
-    const int far = max(max(s.t0 + max(t0 - s.ns, 0), lo >> a.log_tile), st);
-    const int more = max(min(s.t0 + t1 - s.ns, hi) - far, 0);
-    p.near = near1 - near0;
-    p.tile0 = p.near > 0 ? near0 : far;
-    p.tile1 = more > 0 ? far + more : p.tile0 + p.near;
-    p.skip = p.near > 0 && more > 0 ? far - near1 : 0;
+    p.near = 0;
+    p.skip = 0;
+    if (SINKS && a.sinks > 0) {
+      const int64_t near = near_tokens(a);
+      const int from = lo >> a.log_page << a.log_page;
+      p.near = static_cast<int>(min(near, int64_t(INT_MAX)));
+      if (from > near) p.skip = from - p.near;
+      p.tile0 = t0;
+      p.tile1 = min(t1, ((s.L + t_last - p.skip) >> a.log_tile) + 1);
+    } else {
+      p.tile0 = max(s.t0 + t0, lo >> a.log_tile);
+      p.tile1 = min(s.t0 + t1, hi);
+    }
+    if (p.tile1 < p.tile0) p.tile1 = p.tile0;
     return true;
   }
   return false;

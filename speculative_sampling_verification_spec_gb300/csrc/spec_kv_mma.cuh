@@ -51,7 +51,12 @@
 // tokens, 36 rows: 1.24 GB in 219 us, 5.7 TB/s; a tile costs a softmax warp about
 // 3000 cycles beside three others on its scheduler, the tensor unit is busy a fifth
 // of the time).  Part of a prompt (512 queries on 8192 tokens): the same instructions,
-// 142 GFLOP in 299 us.  Short calls: the chain of dependent steps (lengths, page
+// 142 GFLOP in 299 us.  Windows with sinks: the same, and what it costs to take up a
+// piece (queries, first references, results: about 10 us beside its tiles) and its tiles
+// that rows see in part, which are 3 to 5 of the 18 of a window of 2048: 9 drafts each of
+// 32 sequences on windows of 4096 72 us, 512 queries on windows of 2048 145 us (35 GFLOP),
+// one token each of 128 sequences on windows of 4096 163 us (1.08 GB, 6.6 TB/s).  Short
+// calls: the chain of dependent steps (lengths, page
 // numbers, keys, scores, weights, output, join: 1000 tokens take 10.5 us).
 #include <cuda_fp16.h>
 
@@ -259,8 +264,8 @@ static __device__ __noinline__ void abandon(const KvArgs& a, const RangePlan& pl
 }
 
 // RU: rows that a softmax group keeps in registers, at most NR / 2
-// SINKS: first tokens may be seen beside the window (a few instructions a tile, which cost the calls without
-// them 3 to 5 % where rows are many: 36 rows on 32768 tokens 219 -> 226 us, 512 queries on 8192 297 -> 314)
+// SINKS: first tokens may be seen beside the window (a few instructions a tile, which would cost the calls without
+// them 3 to 5 % where rows are many: 36 rows on 32768 tokens 226 us for 219, 512 queries on 8192 314 for 299)
 template <int D, int NR, int RU, bool SINKS>
 __global__ void __launch_bounds__(kMmaThreads, 2)
     spec_kv_attention_mma_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ MmaMaps maps) {
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   start_dependents();
   wait_for_grid();
   tc_fence_before();
-  make_plan_range<kMmaThreads>(a, range, &sm.plan, sm.scratch, blockIdx.x == 0 ? a.prefix : nullptr);
+  make_plan_range<kMmaThreads, SINKS>(a, range, &sm.plan, sm.scratch, blockIdx.x == 0 ? a.prefix : nullptr);
   tc_fence_after();
   const uint32_t tm = sm.tmem;
   volatile int* const gave_up = &sm.gave_up;
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       Piece p;
       Walk walk = walk_begin(sm.plan, range, rt);
       while (ok) {
-        if (!walk_next(a, walk, p)) p.b = -1;
+        if (!walk_next<SINKS>(a, walk, p)) p.b = -1;
         if (lane == 0) {
           sm.pieces[pieces % kPieceRing] = p;
           bar_arrive(&sm.piece_full[pieces % kPieceRing]);
@@ -332,12 +337,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         ++pieces;
         if (p.b < 0) break;
         // The pages of the piece, without what is left out: page i is page i + skip of the sequence from
-        // `near` on.  One that no row sees (beside a tile's sinks, before the window) or that is not the
-        // pool's has NaN scales and is not fetched: its tokens are treated by these, whatever shared
-        // memory holds.
-        const int near = (p.tile0 + p.near) * np, skip = SINKS ? p.skip * np : 0;
+        // `near` on.  One that no row sees (before a tile's window) or that is not the pool's has NaN
+        // scales and is not fetched: its tokens are treated by these, whatever shared memory holds.
+        const int near = p.near >> a.log_page, skip = SINKS ? p.skip >> a.log_page : 0;
         const int first = p.tile0 * np;
-        const int last = min(p.tile1 * np, (p.L + p.n + (1 << a.log_page) - 1) >> a.log_page) - skip;
+        const int last = min(p.tile1 * np, ((p.L + p.n + (1 << a.log_page) - 1) >> a.log_page) - skip);
         // 32 pages at a time, one a lane: numbers, then scales; the next 32 are under way
         const auto number = [&](int base) {
           int pid = -1;
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         int base = first;
         int pid = number(base), pid_next = 0;
         float2 sc = scales(base, pid), sc_next = make_float2(0.0f, 0.0f);
-        for (int t = p.tile0; t < p.tile1 - (SINKS ? p.skip : 0); ++t, ++n) {
+        for (int t = p.tile0; t < p.tile1; ++t, ++n) {
           int in = t * np - base;  // the tile's first page among the 32
           if (in == 32) {
             base += 32;
@@ -452,7 +456,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           if (!ok) break;
           const Piece& p = sm.pieces[pieces % kPieceRing];
           if (p.b < 0) break;
-          const int m = p.tile1 - p.tile0 - (SINKS ? p.skip : 0);
+          const int m = p.tile1 - p.tile0;
           if (m == 0) continue;
           ok = bar_wait(&sm.q_full, queries & 1, gave_up);
           if (!ok) break;
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         }
         fail = soft_any(fail);  // the piece before has been written out
         if (fail || p.b < 0) break;
-        const int m = p.tile1 - p.tile0 - (SINKS ? p.skip : 0);
+        const int m = p.tile1 - p.tile0;
         const int fours = max(0, (rows_mine() + 3) / 4 * 4);  // this group's rows, in fours
         float l[RT];
 #pragma unroll
@@ -601,18 +605,17 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           if (tid == 0) bar_arrive(&sm.q_full);
         }
         const int tile0 = p.tile0, tile1 = p.tile1;
-        const int t_near = SINKS && p.skip > 0 ? tile0 + p.near : -1;  // the first of the tiles that are left out
-        const int sinks = SINKS ? a.sinks : 0;
+        const int sinks = SINKS ? a.sinks : 0, skip = SINKS ? p.skip : 0;
         const int pos_hi = p.L + (p.row0 + p.nrows - 1) / a.G;
         // tiles that some row sees only in part: from t_edge on, and up to t_win but for those of sinks
         // alone; and the tile up to which a row may not have seen a token (a row that sees nothing of
         // a first tile with sinks sees nothing of the piece)
-        const int t_edge = (p.L + p.row0 / a.G + 1) / kTile;
-        const int t_win = a.window > 0 && pos_hi >= a.window ? (pos_hi - a.window) / kTile : -1;
-        const int t_unset = max(tile0, a.window > 0 && (!SINKS || tile0 * kTile >= sinks) ? (pos_hi + 1 - a.window) / kTile : 0);
+        const int t_edge = (p.L + p.row0 / a.G + 1 - skip) / kTile;
+        const int t_win = a.window > 0 && pos_hi >= a.window ? (pos_hi - a.window - skip) / kTile : -1;
+        const int t_unset = max(
+            tile0, a.window > 0 && (!SINKS || tile0 * kTile >= sinks) ? (pos_hi + 1 - a.window - skip) / kTile : 0);
         for (int t = tile0; t < tile1; ++t, ++n) {
-          if (SINKS && t == t_near) t += p.skip;
-          const int j = t * kTile + token;
+          const int j = t * kTile + token + (SINKS && t * kTile + token >= p.near ? skip : 0);
           // scores of this tile; they come with its scales, and with the end of the products two
           // tiles back (issued before them): with two buffers of weights this one's is free
           if (!fail) fail = !bar_wait(&sm.s_full[n & 1], (n >> 1) & 1, gave_up);
@@ -660,9 +663,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           const auto sees = [&](int r) { return seen_from(sm.pos[r_base + r]); };
           float x[RT];
           // a warp none of whose tokens any row sees has nothing to do but to say so
-          const int j_warp = j - lane;
-          const bool idle = SINKS && edge &&
-                            (j_warp > pos_hi || (j_warp >= sinks && j_warp + 31 <= p.L + p.row0 / a.G - a.window));
+          const bool idle =
+              SINKS && edge && __all_sync(kFull, j > pos_hi || (j >= sinks && j <= p.L + p.row0 / a.G - a.window));
           float top = -INFINITY;
           if (!idle) {
 #pragma unroll
