@@ -165,6 +165,15 @@ def test_refusals_of_arguments_and_sizes(L):
         assert L.spec_kv_fork(p, _cache(**over), 0x3000, 0x4000) == 1, over
 
 
+def test_host_tensors_are_refused(L):
+    import speculative_sampling_verification_spec_gb300 as sv
+    t, r, s = torch.full((2, 8), -1, dtype=torch.int32), torch.zeros(9, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        sv.spec_kv_hold(r, t, s, page_size=16)
+    with pytest.raises(ValueError):
+        sv.spec_kv_fork(None, r, t, s, s)
+
+
 # --------------------------------------------------------------------------
 # hold
 
