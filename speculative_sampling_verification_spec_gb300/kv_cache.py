@@ -292,7 +292,7 @@ def spec_kv_attention(q, cache, page_table, seq_lens, new_lens=None, *, scale=No
         raise ValueError("q must be [B, T, Hq, %d], got %s" % (cache.head_dim, tuple(shape)))
     qs = _strides("q", q, shape, dt, index)
     columns, row = _check_table(cache, B, page_table, seq_lens, new_lens, status)
-    if max(window, sinks) >= 1 << 31:      # (more than the C interface's integers hold)
+    if min(window, sinks) < 0 or max(window, sinks) >= 1 << 31:      # (beyond the C interface's integers, ctypes drops bits)
         raise binding.SpecError(binding.SPEC_ERR_INVALID_ARG, "spec_kv_attention")
     if out is None:
         out = _new(shape, dt, dev, stream)

@@ -19,7 +19,7 @@ EXPORTED = ("spec_kv_fork", "spec_kv_hold")
 # spec_kv_pages of include/spec_kv_pages.h, in native layout
 _PAGES = struct.Struct("@4i2Pq3P")
 _I32 = torch.int32
-_MOST_INT = (1 << 31) - 1     # (ctypes would drop the bits above)
+_MOST_INT = (1 << 31) - 1     # (ctypes would drop the bits above, of negative ones too)
 
 _loaded = None
 
@@ -82,7 +82,7 @@ def spec_kv_hold(refs, page_table, seq_lens, new_lens=None, *, page_size, T=0, w
         with torch.cuda.device(refs.device):
             return spec_kv_hold(refs, page_table, seq_lens, new_lens, page_size=page_size, T=T, window=window, sinks=sinks,
                                 free=free, status=status, stream=stream)
-    if max(T, window, sinks, page_size) > _MOST_INT:
+    if min(T, window, sinks) < 0 or max(T, window, sinks, page_size) > _MOST_INT:
         raise binding.SpecError(binding.SPEC_ERR_INVALID_ARG, "spec_kv_hold")
     pages = _pages(refs, page_table, page_size, free, status, stream)
     B, dev = page_table.shape[0], refs.get_device()
