@@ -18,10 +18,6 @@ const void* stream_bf16_topp();
 const void* stream_f32_k();
 const void* stream_bf16_k();
 
-// the tensor-core attention over the paged cache for head size D (64, 128) and up
-// to `rows` rows (at most 48) a row tile, for calls with or without sinks, and its
-// shared memory
-const void* kv_mma(int D, int rows, bool sinks, int* smem_bytes);
 // adds n to the kernels that spec_launch_count reports (spec_verify.cu)
 void count_launches(int n);
 

@@ -5,6 +5,7 @@
 #include "spec_kv_append.cuh"
 #include "spec_kv_attn.cuh"
 #include "spec_kv_mma.cuh"
+#include "spec_kv_units.h"
 
 #include <algorithm>
 #include <atomic>

@@ -1,6 +1,6 @@
 // spec_kv_mma.cu -- the instantiations of the tensor-core attention kernel.
-#include "kernel_table.h"
 #include "spec_kv_mma.cuh"
+#include "spec_kv_units.h"
 
 namespace specv_units {
 namespace {
