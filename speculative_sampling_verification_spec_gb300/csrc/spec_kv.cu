@@ -247,19 +247,21 @@ bool allow_smem(const void* fn, int slot, int bytes) {
 }
 
 template <typename E, int CH, int ROWS>
-const void* general_ptr() {
-  return reinterpret_cast<const void*>(&spec_kv_attention_kernel<E, CH, ROWS>);
+const void* general_ptr(bool sinks) {
+  return sinks ? reinterpret_cast<const void*>(&spec_kv_attention_kernel<E, CH, ROWS, true>)
+               : reinterpret_cast<const void*>(&spec_kv_attention_kernel<E, CH, ROWS, false>);
 }
 template <typename E>
-const void* general_fn(int D, int rows) {
-  if (D > 128) return general_ptr<E, 8, 4>();
-  return rows == 4 ? general_ptr<E, 4, 4>() : general_ptr<E, 4, 8>();
+const void* general_fn(int D, int rows, bool sinks) {
+  if (D > 128) return general_ptr<E, 8, 4>(sinks);
+  return rows == 4 ? general_ptr<E, 4, 4>(sinks) : general_ptr<E, 4, 8>(sinks);
 }
 
 spec_status launch_general(const KvArgs& args, bool f32, int grid, cudaStream_t st) {
   KvArgs a = args;
   void* params[] = {&a};
-  const void* fn = f32 ? general_fn<float>(a.D, a.rows) : general_fn<__nv_bfloat16>(a.D, a.rows);
+  const bool sinks = a.sinks > 0;
+  const void* fn = f32 ? general_fn<float>(a.D, a.rows, sinks) : general_fn<__nv_bfloat16>(a.D, a.rows, sinks);
   return launch(fn, grid, kGenThreads, 0, st, params);
 }
 

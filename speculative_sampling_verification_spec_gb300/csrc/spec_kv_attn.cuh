@@ -213,13 +213,16 @@ constexpr int kGenMaxD = 256;
 // Bound by the float units: a token and row cost 4 D / 32 multiply-adds a lane and
 // about half as many instructions for the sums over lanes and the conversions (16
 // sequences of 8000 tokens, 4 float32 rows a key/value head of 128 channels: 263 MB
-// in 131 us; 8 of 4000 with 20 rows: 151 us).  An earlier form with keys and weights
+// in 131 us; 8 of 4000 with 20 rows: 140 us).  An earlier form with keys and weights
 // in shared memory took 299 and 293 us, bound by its reads.
 //
 // CH: 4 or 8, for head sizes up to 128 or 256; ROWS: rows of a row tile, 4 or 8.
+// SINKS: first tokens may be seen beside the window, which costs the calls without
+// them 2 to 6 % (16 sequences of 8000 as above 76.9 us for 72.7, 64 of up to 8192
+// 328 for 310, 256 channels 60.4 for 58.8).
 constexpr int gen_ctas_an_sm(int ch, int rows) { return ch == 8 ? 2 : rows == 4 ? 4 : 3; }
 
-template <typename E, int CH, int ROWS>
+template <typename E, int CH, int ROWS, bool SINKS>
 __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
     spec_kv_attention_kernel(const __grid_constant__ KvArgs a) {
   constexpr int kWords = CH / 4;  // 32-bit words of codes a token and lane
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
   const int range = blockIdx.x / a.nrt, rt = blockIdx.x - range * a.nrt;
   start_dependents();
   wait_for_grid();
-  make_plan_range<kGenThreads>(a, range, &plan, scratch, blockIdx.x == 0 ? a.prefix : nullptr);
+  make_plan_range<kGenThreads, SINKS>(a, range, &plan, scratch, blockIdx.x == 0 ? a.prefix : nullptr);
   fill_empty<E>(a, tid, kGenThreads);
   if (plan.w0 >= plan.w1) return;
   const int D = a.D, d0 = lane * CH;
@@ -241,11 +244,14 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
   const int my_row = (lane >> 2) % ROWS, my_tok = lane & 3;
   Walk walk = walk_begin(plan, range, rt);
   Piece p;
-  while (walk_next(a, walk, p)) {
-    // the piece's tokens are counted from 0, without what is left out; position_of: where they are
-    const int j0 = p.tile0 << a.log_tile, near = p.near - j0, skip = p.skip;
-    const int count = min(p.tile1 << a.log_tile, p.L + p.n - skip) - j0;
-    const auto position_of = [&](int i) { return j0 + i + (i >= near ? skip : 0); };
+  while (walk_next<SINKS>(a, walk, p)) {
+    // The piece's tokens i without what is left out, `begin` to `end`; position_of: where they are.  They are counted
+    // from 0, but from the first position on where 8 channels a lane leave no registers for that (256 channels without
+    // sinks: 58.8 us for 59.5; 128 channels and 20 rows: 83.9 for 78.0).
+    constexpr bool kFromZero = SINKS || CH == 4;
+    const int skip = SINKS ? p.skip : 0, tile_at = p.tile0 << a.log_tile, j0 = kFromZero ? tile_at : 0;
+    const int begin = tile_at - j0, near = p.near - j0, end = min(p.tile1 << a.log_tile, p.L + p.n - skip) - j0;
+    const auto position_of = [&](int i) { return j0 + i + (SINKS && i >= near ? skip : 0); };
     float q[ROWS][CH], acc[ROWS][CH];  // queries in log2 units; zero past the last row and channel
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
@@ -266,13 +272,13 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
 
     uint32_t kc[kGenStep][kWords], vc[kGenStep][kWords];
     float ks, vs;
-    const auto number = [&](int i) { return i < count ? page_of(a, p.b, position_of(i) >> a.log_page) : 0; };
+    const auto number = [&](int i) { return i < end ? page_of(a, p.b, position_of(i) >> a.log_page) : 0; };
     const auto fetch = [&](int i, int page) {
-      ks = vs = __uint_as_float(0x7fc00000u);  // a page that is not the pool's, or tokens that no row sees
+      ks = vs = __uint_as_float(0x7fc00000u);  // a page that is not the pool's, or, with sinks, tokens that no row sees
       const int base = position_of(i);
-      const bool sees = i < count && piece_sees(a, p, base, base + kGenStep);
-      const bool ok = sees && page >= 0;
-      if (sees && page < 0 && lane == 0) report(a.status, SPEC_ERR_CACHE_RANGE);
+      const bool want = i < end && (!SINKS || piece_sees(a, p, base, base + kGenStep)), ok = want && page >= 0;
+      if (want && page < 0 && lane == 0 && piece_sees<SINKS>(a, p, base, ((base >> a.log_page) + 1) << a.log_page))
+        report(a.status, SPEC_ERR_CACHE_RANGE);
       if (ok) {
         const int64_t at = page * a.scale_page_stride + p.h * a.scale_head_stride;
         ks = a.k_scale[at];
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
                           (base & ((1 << a.log_page) - 1)) * a.token_stride + d0;
 #pragma unroll
       for (int t = 0; t < kGenStep; ++t) {
-        const bool get = ok && mine && i + t < count;
+        const bool get = ok && mine && i + t < end;
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
           kc[t][w] = get ? *reinterpret_cast<const uint32_t*>(a.k_codes + row + t * a.token_stride + 4 * w) : 0u;
@@ -291,10 +297,10 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
       }
     };
     constexpr int kStride = kGenStep * kGenWarps;
-    int i = warp * kGenStep;
+    int i = begin + warp * kGenStep;
     int page = number(i), next_page = number(i + kStride);
-    if (i < count) fetch(i, page);
-    for (; i < count; i += kStride) {
+    if (i < end) fetch(i, page);
+    for (; i < end; i += kStride) {
       const int base = position_of(i);
       float kf[kGenStep][CH];
       uint32_t vnow[kGenStep][kWords];
@@ -314,8 +320,8 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
       }
       page = next_page;
       next_page = number(i + 2 * kStride);
-      if (i + kStride < count) fetch(i + kStride, page);
-      const bool all = (base >= all_from || base + kGenStep <= a.sinks) && base + kGenStep - 1 <= all_to;
+      if (i + kStride < end) fetch(i + kStride, page);
+      const bool all = (base >= all_from || (SINKS && base + kGenStep <= a.sinks)) && base + kGenStep - 1 <= all_to;
 #pragma unroll
       for (int t0 = 0; t0 < kGenStep; t0 += 4) {
         float s[ROWS * 4];
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(kGenThreads, gen_ctas_an_sm(CH, ROWS))
         }
         const float score = lane_sums<ROWS * 4>(s) * ks_now;
         const int j = base + t0 + my_tok;
-        const bool see = j <= pos && (j > low || j < a.sinks);  // (positions past the last are past every row's own)
+        const bool see = j <= pos && (j > low || (SINKS && j < a.sinks));  // (positions past the last are past every row's own)
         const float x = see ? score : -INFINITY;
         float top = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));

@@ -306,8 +306,9 @@ __device__ __forceinline__ bool walk_next(const KvArgs& a, Walk& k, Piece& p) {
 
 // Whether some row of the piece sees a token of [from, to) (which begins at or before
 // the last position that a row sees).
+template <bool SINKS = true>
 __device__ __forceinline__ bool piece_sees(const KvArgs& a, const Piece& p, int from, int to) {
-  return to > p.first || from < a.sinks;
+  return to > p.first || (SINKS && from < a.sinks);
 }
 
 // page number of a token's page, -1 where it is not one of the pool's (an error
