@@ -31,9 +31,12 @@ namespace {
 using namespace spec_kv_detail;
 
 constexpr int kMostCtas = 16, kPortableCtas = 8;  // of a cluster
-constexpr int kWordsAlone = 256;  // of bits, that one CTA takes on alone
-// Words up to which CTAs have 256 threads, past it 1024: fewer make for quicker barriers (32 sequences, 2831 pages: 5.6 us
-// a call, 7.5 with 1024), more have more of a large table under way (256 x 8194 entries: 23 us, 33 with 256).
+// Words of bits up to which one CTA takes a call on alone: it has no other to wait for, but 15 fewer to share the work
+// with (8 sequences, 3000 pages, 128 words: 4.0 us a call either way; 32 and 2800, 216 words: 6.6, by a cluster 4.2).
+constexpr int kWordsAlone = 128;
+// Words up to which CTAs have 256 threads, past it 1024: fewer make for quicker barriers (128 rows of 128 entries, 100 000
+// pages, 3637 words: 5.1 us a call, 6.3 with 1024; a fork 10.1 and 11.3), more have more of a large table under way (300
+// rows, 120 000 pages, 4950 words: 6.9 us with 256, 6.6 with 1024, a fork 12.3 and 11.8; 256 x 8194 entries: 33 and 23).
 constexpr int kWordsFew = 4096;
 constexpr int kAhead = 4;      // loads of counts of a lane under way at once
 
