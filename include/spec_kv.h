@@ -168,11 +168,14 @@ spec_status spec_kv_attention(const void* q, const spec_kv_cache* cache, const s
                               float* lse);
 
 /* The same with first tokens that stay visible: beside its window, a query sees the
- * positions j < sinks (those up to its own).  sinks >= 0; without a window (0) every
- * position is seen anyway.  A token of both counts once.  Entries of the table for pages
- * that lie wholly behind the sinks and before what any query of the sequence sees through
- * its window may hold anything.  Everything else, the workspace's size among it, is as for
- * spec_kv_attention, which is this with no sinks. */
+ * positions j < sinks (those up to its own).  They keep the positions that they were
+ * appended (and rotated) at: none is counted anew inside the cache, so a stream's positions
+ * go on growing; and a sink that has a learned logit and no token is not one of these (its
+ * weight can be added to the sum that lse is the logarithm of).  sinks >= 0; without a
+ * window (0) every position is seen anyway.  A token of both counts once.  Entries of the
+ * table for pages that lie wholly behind the sinks and before what any query of the
+ * sequence sees through its window may hold anything.  Everything else, the workspace's
+ * size among it, is as for spec_kv_attention, which is this with no sinks. */
 spec_status spec_kv_attention_sinks(const void* q, const spec_kv_cache* cache, const spec_kv_params* params,
                                     int32_t sinks, void* out, float* lse);
 

@@ -15,9 +15,11 @@
  *
  * Conventions: those of spec_verify.h, without a workspace.  What one call does goes by
  * the inputs alone, not by timing.  Calls that share counts must not overlap in time on
- * the GPU.  The table's entries (rows of more than 128 count up to the next 512) and the
- * pool's pages are tracked in one cluster's shared memory, a bit each: beyond some 14
- * million together a call is SPEC_ERR_UNSUPPORTED.
+ * the GPU.  The table's entries (rows count up to the next 128, those of more than 128 up
+ * to the next 512) and the pool's pages are tracked in one cluster's shared memory, a bit
+ * each: beyond some 14 million together (7 million where the device has no room for a
+ * cluster of 16 CTAs) a call is SPEC_ERR_UNSUPPORTED.  Tables of that size are held by the
+ * host.
  *
  * Counts.  refs[p] is the number of table entries that hold page p; 0 (or less): the
  * page is free.  All zero, with a table of -1, is an empty pool.  A caller may count

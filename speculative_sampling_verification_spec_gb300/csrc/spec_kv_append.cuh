@@ -230,9 +230,10 @@ __device__ __forceinline__ void turn_chunk(const AppendArgs& g, const float* cs,
 __device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
 // The sum of the squares of a head's channels, times the square of a power of two f that brings the largest to [1, 2):
-// hi + lo.  A lane's sum is run on top of a bias, 2 D or the power of two above, which no lane's sum reaches: every
-// addition leaves a multiple of the bias's last place in the sum, exactly, and the rest of the square, all but exactly,
-// for a second sum of small numbers.  The multiples of all lanes add up exactly, too.
+// hi + lo.  A lane runs two sums side by side, of every second square, each on top of a bias, 2 D or the power of two above
+// (32 at least), which neither reaches (8 squares below 4 at most): every addition leaves a multiple of the bias's last
+// place in the sum, exactly, and the rest of the square, all but exactly, for a second sum of small numbers.  The multiples
+// of all lanes add up exactly, too.
 struct Squares {
   float hi, lo, f;
 };
