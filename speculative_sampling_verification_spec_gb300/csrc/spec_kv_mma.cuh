@@ -400,8 +400,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           // the tile's scales come with its keys: the arrival that the copies' bytes wait for is after them
           if (in == 0) {
             // (without sinks, pages before the window have their scales here, which are nothing to those that are seen)
-            const bool seen = SINKS || (base + lane + 1) << a.log_page > p.first;
-            const bool counts = base + lane < last && seen && sc.y > 0.0f && is_finite(sc.y);
+            const bool counts = base + lane < last && (SINKS || (base + lane + 1) << a.log_page > p.first) && sc.y > 0.0f &&
+                                is_finite(sc.y);
             v_top = max(v_top, __reduce_max_sync(kFull, counts ? __float_as_uint(sc.y) : 0u));
           }
           if (mine >= 0 && mine < np) {
